@@ -61,6 +61,8 @@ typedef enum plx_dtype { PLX_F32 = 0, PLX_BF16 = 1 } plx_dtype;
 #define PLX_DEVERR_TIMEOUT    2   /* an mbarrier / pipeline wait gave up         */
 #define PLX_DEVERR_BAD_LENGTH 4   /* a sequence length outside its allowed range */
 #define PLX_DEVERR_SINGULAR   8   /* LLA: S_KK + ridge I not positive definite     */
+#define PLX_DEVERR_NO_PAGES  16   /* page plan: the free pages ran out             */
+#define PLX_DEVERR_BAD_POSITION 32 /* norm + rotation: position >= max_pos or < -1  */
 
 /* ------------------------------------------------------------------------
  * Decode: one new query per (sequence, query head) over its KV cache.
@@ -428,6 +430,208 @@ plx_status parallax_prefill_paged(const void* q, const void* rho,
                                   const int32_t* page_table, const int32_t* cu_seqlens_q,
                                   const int32_t* seq_lens, void* out,
                                   const plx_prefill_paged_params* p, cudaStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Page plan: the tables of one serving step, built on the device from the
+ * requests' lengths.  Request b holds cached_lens[b] tokens and gets
+ * new_lens[b] more; the step's new tokens are packed request after request
+ * into rows (the layout of parallax_prefill_paged's q; with one new token
+ * each, the batch of parallax_decode).  With L = cached + new:
+ *     seq_lens[b] = L
+ *     cu_seqlens  = exclusive prefix sum of new_lens (cu_seqlens[B] = rows in use)
+ *     page_table[b][ceil(cached/64) ..  ceil(L/64) - 1] = the next free pages,
+ *                   request after request, from free_pages[*free_head] on
+ *     positions[r] = cached + (r - cu_seqlens[b])         for a row r of request b
+ *     slot_map[r]  = 64 * page_table[b][positions[r] / 64] + positions[r] % 64
+ *     *pages_used  = free pages handed out
+ * Rows from cu_seqlens[B] to num_rows - 1 (a captured graph's padding) get
+ * position -1 and slot -1, which parallax_norm_rope and parallax_cache_append
+ * skip.
+ * ---------------------------------------------------------------------- */
+typedef struct plx_page_plan_params {
+  int32_t batch;              /* 1 <= B <= 8192                                */
+  int32_t num_rows;           /* rows of slot_map and positions, >= 0          */
+  int32_t page_size;          /* 64                                            */
+  int32_t num_pages;          /* P, pages in the pool                          */
+  int32_t max_pages_per_seq;  /* page_table row stride                         */
+  int32_t num_free;           /* entries of free_pages, >= 0                   */
+} plx_page_plan_params;
+
+/* Page plan.
+ *   cached_lens, new_lens  device int32 [B], >= 0.
+ *   page_table   device int32 [B, max_pages_per_seq], updated in place: only
+ *                the new pages' entries are written.
+ *   free_pages   device int32 [num_free] page ids (may be NULL when num_free is 0).
+ *   free_head    device int32: first entry of free_pages still free; NULL means 0.
+ *   seq_lens     device int32 [B].
+ *   cu_seqlens   device int32 [B + 1].
+ *   slot_map     device int64 [num_rows]; positions device int32 [num_rows].
+ *   pages_used   device int32.
+ * No output may overlap an input or another output (PLX_ERR_INVALID_ARG), so
+ * that the same inputs give the same outputs again.  One launch.
+ * On the device, a request whose lengths are negative or exceed
+ * 64 * max_pages_per_seq, or whose rows do not fit in num_rows, sets
+ * PLX_DEVERR_BAD_LENGTH; one whose new pages are not there any more sets
+ * PLX_DEVERR_NO_PAGES (later requests that need a page fail too); a page id
+ * outside [0, P) sets PLX_DEVERR_BAD_PAGE.  A failed request gets seq_lens 0
+ * and position and slot -1 for its rows, takes no page and leaves its table
+ * row; with a bad page only the slots on it are -1 (a bad free page is
+ * entered as -1). */
+plx_status parallax_page_plan(const int32_t* cached_lens, const int32_t* new_lens, int32_t* page_table,
+                              const int32_t* free_pages, const int32_t* free_head, int32_t* seq_lens,
+                              int32_t* cu_seqlens, int64_t* slot_map, int32_t* positions, int32_t* pages_used,
+                              const plx_page_plan_params* p, cudaStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * RMS norm of every head's row with the position rotation in the same pass:
+ * what turns projected rows into the queries, probes and keys that the
+ * attention entry points read.  For a row x of d columns at position t:
+ *     n = x / sqrt(mean(x^2) + eps) * w           (norm = 0: n = x)
+ *     y_i = n_i cos_t,f - n_j sin_t,f,  y_j = n_j cos_t,f + n_i sin_t,f
+ * for the pairs f < rot_dim / 2 of the first rot_dim columns: (i, j) =
+ * (f, f + rot_dim / 2), or (2f, 2f + 1) with `interleaved`.  Columns from
+ * rot_dim on pass through.  Sums are fp32; y is rounded once.
+ * ---------------------------------------------------------------------- */
+typedef struct plx_norm_rope_params {
+  int32_t batch;              /* B >= 1                                        */
+  int32_t tokens;             /* T >= 0 per batch entry (packed rows: B = 1)   */
+  int32_t head_dim;           /* d: 64 or 128                                  */
+  int32_t rot_dim;            /* multiple of 16, 0 .. d; 0: no rotation        */
+  int32_t max_pos;            /* rows of cos and sin                           */
+  int32_t interleaved;        /* pairs (2f, 2f + 1) instead of (f, f + rot/2)  */
+  int32_t norm;               /* 1: RMS norm; 0: rotation only                 */
+  int32_t dtype;              /* plx_dtype of x, y, w                          */
+  float eps;                  /* > 0 with norm                                 */
+  int64_t pos_batch_stride;   /* positions of batch entry b start at b * this;
+                                 0: one row of T positions for all             */
+} plx_norm_rope_params;
+
+/* One set of head rows: x[b, t, h] at x + b * x_stride[0] + t * x_stride[1] +
+ * h * x_stride[2] elements, d contiguous columns; y likewise.  Pointers are
+ * 16-byte aligned and strides multiples of 16 bytes.  y may be x itself with
+ * the same strides (in place); otherwise it must not overlap any input. */
+typedef struct plx_head_rows {
+  const void* x;
+  void* y;
+  const void* w;              /* [d], 16-byte aligned, or NULL: ones           */
+  int32_t heads;              /* >= 1                                          */
+  int64_t x_stride[3], y_stride[3];
+} plx_head_rows;
+
+/* Up to three sets (queries, probes, keys) in one launch.
+ *   positions   device int32, see pos_batch_stride; NULL: row t has position t.
+ *   cos, sin    device float32 [max_pos, rot_dim / 2]; unused when rot_dim is 0.
+ * A row at position -1 is padding: its y is left as it was.  Any other
+ * position outside [0, max_pos) sets PLX_DEVERR_BAD_POSITION and is treated
+ * the same.  T == 0 returns PLX_OK without a launch. */
+plx_status parallax_norm_rope(const plx_head_rows* rows, int32_t num_sets, const int32_t* positions,
+                              const float* cos, const float* sin, const plx_norm_rope_params* p,
+                              cudaStream_t stream);
+
+/* Gradients.  Set i of the forward has its x and w in rows[i].x and .w, and
+ * grads[i]:
+ *   dy          device, dL/dy, strides dy_stride (as x_stride).
+ *   dx          device, dL/dx, strides dx_stride; may be dy itself with the same strides.
+ *   dw          device float32 [d], dL/dw summed over every row, or NULL.
+ * rows[i].y is not used.  Padding rows (as above) get dx = 0 and add nothing
+ * to dw.  With norm 0 dw must be NULL.
+ *   workspace   device, >= parallax_norm_rope_backward_workspace_size() bytes,
+ *               16-byte aligned; no initialisation needed.  May be NULL when no dw is asked for.
+ * Every output element is written exactly once and every sum has a fixed
+ * order (no atomics, deterministic).  Two launches, one without any dw. */
+typedef struct plx_head_grads {
+  const void* dy;
+  void* dx;
+  float* dw;
+  int64_t dy_stride[3], dx_stride[3];
+} plx_head_grads;
+
+size_t parallax_norm_rope_backward_workspace_size(const plx_norm_rope_params* p, int32_t num_sets);
+plx_status parallax_norm_rope_backward(const plx_head_rows* rows, const plx_head_grads* grads, int32_t num_sets,
+                                       const int32_t* positions, const float* cos, const float* sin,
+                                       void* workspace, size_t workspace_bytes, const plx_norm_rope_params* p,
+                                       cudaStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Cache append: a step's keys and values into the paged cache, row r at slot
+ * slot_map[r] = 64 * page + row in the page (parallax_page_plan's map).
+ * ---------------------------------------------------------------------- */
+typedef struct plx_append_params {
+  int32_t num_rows;           /* N >= 0                                        */
+  int32_t num_kv_heads;       /* Hkv                                           */
+  int32_t head_dim;           /* d: 64 or 128                                  */
+  int32_t page_size;          /* 64                                            */
+  int32_t num_pages;          /* P                                             */
+  int32_t dtype;              /* plx_dtype of k and v (and of the plain pools) */
+  int64_t k_stride[2];        /* elements between rows and between heads of k  */
+  int64_t v_stride[2];        /* likewise for v; multiples of 16 bytes         */
+} plx_append_params;
+
+/* Append to the pools that parallax_decode and parallax_prefill_paged read.
+ *   k, v       device [N, Hkv, d] of p->dtype with the strides above.
+ *   slot_map   device int64 [N].  A negative slot skips its row; one past the
+ *              pool sets PLX_DEVERR_BAD_PAGE and skips it.  Slots are distinct
+ *              (a slot that two rows share gets either's bytes, or some of both).
+ *   k_cache, v_cache  device [P, Hkv, 64, d] of p->dtype. */
+plx_status parallax_cache_append(const void* k, const void* v, const int64_t* slot_map, void* k_cache,
+                                 void* v_cache, const plx_append_params* p, cudaStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * The cache in 4 bits.  Each group of 64 columns of a key or value row is
+ * held as 4-bit codes n with a bf16 scale s and a bf16 minimum m and stands
+ * for s n + m:
+ *     m = min x,  s = bf16((max x - m) / 15),  n = round((x - m) / s) in 0 .. 15
+ * (differences and quotients in fp32, rounded to nearest even; n = 0 where
+ * s = 0).  m is a value of the row and so exact.  A group with a value that is
+ * not finite, or whose range overflows fp32, stands for NaN.
+ *
+ * One block of 72 d bytes per (page, KV head), blocks [P, Hkv]:
+ *     K codes   64 rows of d/2 bytes.  32-bit word (d/32) c + j of a row
+ *               (c < 4, j < d/32) holds columns 32 j + 8 c + i, i < 8, at
+ *               bits 16 (i % 2) + 4 (i / 2).
+ *     V codes   32 rows of d bytes, row u for tokens 2u and 2u + 1.  Word
+ *               (d/32) r + j (r < 8) holds columns 32 j + 4 r + i, i < 4, of
+ *               token 2u + e at bits 16 e + 4 i.
+ *     K params  [64][d/64] words: s in the low half, m in the high half
+ *     V params  likewise
+ * ---------------------------------------------------------------------- */
+#define PARALLAX_Q4_GROUP 64
+
+/* Bytes of one block: 72 d (4608 or 9216), or 0 for an unsupported head_dim. */
+size_t parallax_q4_block_bytes(int32_t head_dim);
+
+/* Quantises and appends; as parallax_cache_append otherwise.
+ *   k, v       bf16 (p->dtype PLX_BF16, else PLX_ERR_UNSUPPORTED).
+ *   kv_cache   device [P, Hkv] blocks, 16-byte aligned. */
+plx_status parallax_cache_append_q4(const void* k, const void* v, const int64_t* slot_map, void* kv_cache,
+                                    const plx_append_params* p, cudaStream_t stream);
+
+/* The keys and values that the slots stand for: k, v [N, Hkv, d] of p->dtype
+ * (fp32: s n + m rounded once; bf16: that rounded again) with p's strides.
+ * Rows with a negative slot, or one past the pool (PLX_DEVERR_BAD_PAGE), are
+ * left as they were. */
+plx_status parallax_cache_gather_q4(const void* kv_cache, const int64_t* slot_map, void* k, void* v,
+                                    const plx_append_params* p, cudaStream_t stream);
+
+/* parallax_decode over the 4-bit cache: the same definition on the keys and
+ * values that the blocks stand for.
+ *   q, rho      device bf16 [B, Hq, d] (p->in_dtype PLX_BF16, else
+ *               PLX_ERR_UNSUPPORTED).
+ *   kv_cache    paged (page_size 64): blocks [P, Hkv], token t of sequence b
+ *               in row t % 64 of page page_table[b][t / 64].  Contiguous
+ *               (page_size 0): blocks [B, Hkv, ceil(kv_len / 64)].
+ *               16-byte aligned.  Rows past a sequence's length may hold
+ *               anything.
+ *   workspace   device, >= parallax_decode_q4_workspace_size() bytes, 256-byte
+ *               aligned, with parallax_decode's rule: the counter region at its
+ *               front (4 bytes per (sequence, KV head), padded to 256) is zero
+ *               before the first use, and every call leaves it zero.
+ *   the rest    as parallax_decode.  Hq / Hkv <= 8.
+ * One launch. */
+size_t parallax_decode_q4_workspace_size(const plx_decode_params* p, int32_t num_sms);
+plx_status parallax_decode_q4(const void* q, const void* rho, const void* kv_cache, const int32_t* page_table,
+                              const int32_t* seq_lens, void* out, void* workspace, size_t workspace_bytes,
+                              const plx_decode_params* p, cudaStream_t stream);
 
 /* ------------------------------------------------------------------------
  * Errors and introspection.

@@ -9,6 +9,8 @@ no fallback.
 
 from __future__ import annotations
 
+import collections
+import contextlib
 import ctypes
 import os
 import threading
@@ -28,6 +30,7 @@ PLX_F32, PLX_BF16 = 0, 1
 STATUS = {0: "PLX_OK", 1: "PLX_ERR_INVALID_ARG", 2: "PLX_ERR_UNSUPPORTED", 3: "PLX_ERR_WORKSPACE",
           4: "PLX_ERR_CUDA", 5: "PLX_ERR_DEVICE_FAULT", 6: "PLX_ERR_TIMEOUT"}
 DEVERR_BAD_PAGE, DEVERR_TIMEOUT, DEVERR_BAD_LENGTH, DEVERR_SINGULAR = 1, 2, 4, 8
+DEVERR_NO_PAGES, DEVERR_BAD_POSITION = 16, 32
 PAGE_SIZE = 64
 
 
@@ -56,6 +59,34 @@ class PrefillPagedParams(ctypes.Structure):
                 ("max_pages_per_seq", ctypes.c_int32), ("in_dtype", ctypes.c_int32),
                 ("out_dtype", ctypes.c_int32), ("scale", ctypes.c_float),
                 ("causal", ctypes.c_int32)]
+
+
+class PagePlanParams(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int32), ("num_rows", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("num_pages", ctypes.c_int32), ("max_pages_per_seq", ctypes.c_int32), ("num_free", ctypes.c_int32)]
+
+
+class NormRopeParams(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int32), ("tokens", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("rot_dim", ctypes.c_int32), ("max_pos", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("norm", ctypes.c_int32), ("dtype", ctypes.c_int32), ("eps", ctypes.c_float),
+                ("pos_batch_stride", ctypes.c_int64)]
+
+
+class HeadRows(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("y", ctypes.c_void_p), ("w", ctypes.c_void_p), ("heads", ctypes.c_int32),
+                ("x_stride", ctypes.c_int64 * 3), ("y_stride", ctypes.c_int64 * 3)]
+
+
+class HeadGrads(ctypes.Structure):
+    _fields_ = [("dy", ctypes.c_void_p), ("dx", ctypes.c_void_p), ("dw", ctypes.c_void_p),
+                ("dy_stride", ctypes.c_int64 * 3), ("dx_stride", ctypes.c_int64 * 3)]
+
+
+class AppendParams(ctypes.Structure):
+    _fields_ = [("num_rows", ctypes.c_int32), ("num_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("num_pages", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("k_stride", ctypes.c_int64 * 2), ("v_stride", ctypes.c_int64 * 2)]
 
 
 _vp, _i32p = ctypes.c_void_p, ctypes.c_void_p
@@ -108,6 +139,31 @@ lib.parallax_cuda_error_string.restype = ctypes.c_char_p
 lib.parallax_cuda_error_string.argtypes = [ctypes.c_int32]
 lib.parallax_last_device_error.restype = ctypes.c_int
 lib.parallax_last_device_error.argtypes = [_vp, ctypes.POINTER(ctypes.c_int32)]
+
+lib.parallax_page_plan.restype = ctypes.c_int
+lib.parallax_page_plan.argtypes = [_vp] * 10 + [ctypes.POINTER(PagePlanParams), _vp]
+lib.parallax_norm_rope.restype = ctypes.c_int
+lib.parallax_norm_rope.argtypes = [ctypes.POINTER(HeadRows), ctypes.c_int32, _i32p, _vp, _vp,
+                                   ctypes.POINTER(NormRopeParams), _vp]
+lib.parallax_norm_rope_backward_workspace_size.restype = ctypes.c_size_t
+lib.parallax_norm_rope_backward_workspace_size.argtypes = [ctypes.POINTER(NormRopeParams), ctypes.c_int32]
+lib.parallax_norm_rope_backward.restype = ctypes.c_int
+lib.parallax_norm_rope_backward.argtypes = [ctypes.POINTER(HeadRows), ctypes.POINTER(HeadGrads), ctypes.c_int32,
+                                            _i32p, _vp, _vp, _vp, ctypes.c_size_t, ctypes.POINTER(NormRopeParams),
+                                            _vp]
+lib.parallax_cache_append.restype = ctypes.c_int
+lib.parallax_cache_append.argtypes = [_vp] * 5 + [ctypes.POINTER(AppendParams), _vp]
+lib.parallax_q4_block_bytes.restype = ctypes.c_size_t
+lib.parallax_q4_block_bytes.argtypes = [ctypes.c_int32]
+lib.parallax_cache_append_q4.restype = ctypes.c_int
+lib.parallax_cache_append_q4.argtypes = [_vp] * 4 + [ctypes.POINTER(AppendParams), _vp]
+lib.parallax_cache_gather_q4.restype = ctypes.c_int
+lib.parallax_cache_gather_q4.argtypes = [_vp] * 4 + [ctypes.POINTER(AppendParams), _vp]
+lib.parallax_decode_q4_workspace_size.restype = ctypes.c_size_t
+lib.parallax_decode_q4_workspace_size.argtypes = [ctypes.POINTER(DecodeParams), ctypes.c_int32]
+lib.parallax_decode_q4.restype = ctypes.c_int
+lib.parallax_decode_q4.argtypes = [_vp, _vp, _vp, _i32p, _i32p, _vp, _vp, ctypes.c_size_t,
+                                   ctypes.POINTER(DecodeParams), _vp]
 
 SIZE_MAX = ctypes.c_size_t(-1).value
 
@@ -618,6 +674,465 @@ def prefill_paged(q, rho, k_cache, v_cache, page_table, cu_seqlens_q, seq_lens, 
                                     _stream_ptr(q.device))
     if st != 0:
         raise ParallaxError(st, "parallax_prefill_paged")
+    return out
+
+
+# ---------------------------------------------------------------- the step around attention
+
+def _check_device(device, tensors):
+    """Every given (name, tensor, dtype) is a CUDA tensor of ``device`` and dtype (None: any)."""
+    for name, t, dtype in tensors:
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor")
+        if t.device != device:
+            raise ValueError(f"{name} is on {t.device}, not on {device}")
+        if dtype is not None and t.dtype != dtype:
+            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+
+
+def _check_shape(name, t, shape):
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+_no_guard = contextlib.nullcontext()
+
+
+def _device_guard(device):
+    """The library launches on the current device: make it the tensors' own."""
+    return _no_guard if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+
+
+def _raw_stream(device):
+    return torch.cuda.current_stream(device).cuda_stream
+
+
+def _raw(t):
+    return None if t is None else t.data_ptr()
+
+
+PagePlan = collections.namedtuple("PagePlan", "seq_lens cu_seqlens slot_map positions pages_used")
+
+
+def page_plan(cached_lens, new_lens, page_table, free_pages, *, num_rows, num_pages, free_head=None):
+    """The tables of one serving step, from the requests' lengths (parallax_page_plan).
+
+    cached_lens, new_lens: int32 [B], the tokens that each request has in the
+    cache and gets now.  page_table: int32 [B, max_pages], updated in place
+    with the new pages, which are taken in order from free_pages (int32
+    [num_free]) at ``free_head`` (a device int32 tensor of one element; None
+    means 0).  ``num_rows`` is the number of packed new-token rows (a host
+    int: the sum of new_lens, or more where a captured graph pads) and
+    ``num_pages`` the pool's size.
+
+    Returns PagePlan(seq_lens int32 [B], cu_seqlens int32 [B + 1], slot_map
+    int64 [num_rows], positions int32 [num_rows], pages_used int32 [1]): what
+    decode / decode_q4 / prefill_paged, cache_append and norm_rope take.  Rows
+    past the last request have slot and position -1.  Requests that do not fit
+    are reported through last_device_error and get seq_lens 0 and slots -1.
+    """
+    if cached_lens.dim() != 1 or page_table.dim() != 2 or free_pages.dim() != 1:
+        raise ValueError("cached_lens and free_pages must be 1-D and page_table 2-D")
+    B, width = cached_lens.shape[0], page_table.shape[1]
+    for name, t, shape in (("cached_lens", cached_lens, (B,)), ("new_lens", new_lens, (B,)),
+                           ("page_table", page_table, (B, width)), ("free_pages", free_pages, free_pages.shape)):
+        _check_shape(name, t, shape)
+    if free_head is not None and (free_head.numel() != 1):
+        raise ValueError("free_head must hold one element")
+    device = cached_lens.device
+    _check_device(device, (("cached_lens", cached_lens, torch.int32), ("new_lens", new_lens, torch.int32),
+                           ("page_table", page_table, torch.int32), ("free_pages", free_pages, torch.int32),
+                           ("free_head", free_head, torch.int32)))
+    # one allocation: slots first (8-byte entries), every part from a 16-byte boundary
+    n, b = (int(num_rows) + 3) & ~3, (B + 4) & ~3
+    buf = torch.empty(3 * n + 2 * b + 4, dtype=torch.int32, device=device)
+    slots = buf[:2 * n].view(torch.int64)[:num_rows]
+    at = 2 * n
+    positions, seq_lens = buf[at:at + num_rows], buf[at + n:at + n + B]
+    at += n + b
+    cu, used = buf[at:at + B + 1], buf[at + b:at + b + 1]
+    p = PagePlanParams(B, num_rows, PAGE_SIZE, num_pages, width, free_pages.shape[0])
+    with _device_guard(device):
+        st = lib.parallax_page_plan(_raw(cached_lens), _raw(new_lens), _raw(page_table), _raw(free_pages),
+                                    _raw(free_head), _raw(seq_lens), _raw(cu), _raw(slots), _raw(positions),
+                                    _raw(used), ctypes.byref(p), _raw_stream(device))
+    if st != 0:
+        raise ParallaxError(st, "parallax_page_plan")
+    return PagePlan(seq_lens, cu, slots, positions, used)
+
+
+def _head_strides(name, t, batched):
+    """Element strides (batch entry, token, head) of [B, H, T, d] or packed [N, H, d] rows."""
+    if t.stride(-1) != 1 and t.numel() > 0:
+        raise ValueError(f"{name}'s last dimension must be contiguous")
+    s = t.stride()
+    return (s[0], s[2], s[1]) if batched else (0, s[0], s[1])
+
+
+def _head_like(x):
+    """A tensor for a row set's results: x's own strides where x is dense, else plain contiguous."""
+    return torch.empty_like(x, memory_format=torch.contiguous_format)
+
+
+def _norm_rope_call(q, rho, k, cos, sin, positions, weights, eps, norm, interleaved):
+    """Checks and parameters that the two directions share: (sets, params, device), a set being
+    (name, x, weight)."""
+    batched = q.dim() == 4
+    if q.dim() not in (3, 4):
+        raise ValueError(f"q must be [B, H, T, d] or packed [N, H, d], got {tuple(q.shape)}")
+    if rho is not None and rho.shape != q.shape:
+        raise ValueError(f"rho must have q's shape {tuple(q.shape)}, got {tuple(rho.shape)}")
+    d = q.shape[-1]
+    B, T = (q.shape[0], q.shape[2]) if batched else (1, q.shape[0])
+    if k is not None and (k.dim() != q.dim() or k.shape[-1] != d or k.shape[0] != q.shape[0]
+                          or (batched and k.shape[2] != T)):
+        raise ValueError(f"k's rows {tuple(k.shape)} do not match q's {tuple(q.shape)}")
+    if (cos is None) != (sin is None):
+        raise ValueError("cos and sin come together")
+    rot, max_pos = 0, 0
+    if cos is not None:
+        if cos.dim() != 2 or cos.shape != sin.shape:
+            raise ValueError("cos and sin must be [max_pos, rot_dim / 2] and alike")
+        if not (cos.is_contiguous() and sin.is_contiguous()):
+            raise ValueError("cos and sin must be contiguous")
+        max_pos, rot = cos.shape[0], 2 * cos.shape[1]
+    pos_stride = 0
+    if positions is not None:
+        shapes = ((T,), (B, T)) if batched else ((T,),)
+        if tuple(positions.shape) not in shapes:
+            raise ValueError(f"positions must have shape {' or '.join(map(str, shapes))}, got {tuple(positions.shape)}")
+        if not positions.is_contiguous():
+            raise ValueError("positions must be contiguous")
+        pos_stride = T if positions.dim() == 2 else 0
+    elif rot and T > max_pos:
+        raise ValueError(f"{T} tokens need as many rows of cos and sin, got {max_pos}")
+    device = q.device
+    sets = [s for s in zip(("q", "rho", "k"), (q, rho, k), weights) if s[1] is not None]
+    for name, x, w in sets:
+        if w is not None:
+            if not norm:
+                raise ValueError(f"{name}_weight needs norm=True")
+            _check_shape(name + "_weight", w, (d,))
+        _check_device(device, ((name, x, q.dtype), (name + "_weight", w, q.dtype)))
+    _check_device(device, (("cos", cos, torch.float32), ("sin", sin, torch.float32),
+                           ("positions", positions, torch.int32)))
+    p = NormRopeParams(B, T, d, rot, max_pos, 1 if interleaved else 0, 1 if norm else 0, _dtype_code(q.dtype),
+                       eps, pos_stride)
+    return sets, p, device, batched
+
+
+def norm_rope(q, rho, k, cos, sin, positions=None, *, q_weight=None, rho_weight=None, k_weight=None, eps=1e-6,
+              norm=True, interleaved=False, out=None):
+    """RMS norm of every query, probe and key head with the position rotation, in one pass.
+
+    q, rho: [B, H, T, d], or packed [N, H, d]; k: the same with its own heads
+    (rho and k may be None).  Any strides with a contiguous last dimension (16-byte
+    aligned rows), so that slices of one fused projection need no copy.
+    cos, sin: float32 [max_pos, rot_dim / 2] (None: no rotation), for pairs
+    (f, f + rot_dim / 2), or (2f, 2f + 1) with ``interleaved``.  positions:
+    int32 [T], [B, T] or packed [N] (None: row t has position t); rows at
+    position -1 are skipped.  Weights [d] of q's dtype, or None for ones;
+    norm=False only rotates.  ``out``: a tuple of tensors to write (an entry
+    may be the input itself: in place).  Returns (q, rho, k), None where the
+    input is.
+    """
+    sets, p, device, batched = _norm_rope_call(q, rho, k, cos, sin, positions, (q_weight, rho_weight, k_weight),
+                                               eps, norm, interleaved)
+    if out is not None:
+        given = dict(zip(("q", "rho", "k"), out))
+        ys = [given[name] for name, _, _ in sets]
+        for (name, x, _), y in zip(sets, ys):
+            if y is None or y.shape != x.shape:
+                raise ValueError(f"out's {name} must have shape {tuple(x.shape)}")
+            _check_device(device, (("out's " + name, y, x.dtype),))
+    else:
+        ys = [_head_like(x) for _, x, _ in sets]
+    rows = (HeadRows * len(sets))()
+    for r, (name, x, w), y in zip(rows, sets, ys):
+        r.x, r.y, r.w, r.heads = x.data_ptr(), y.data_ptr(), _raw(w), x.shape[1]
+        r.x_stride[:] = _head_strides(name, x, batched)
+        r.y_stride[:] = _head_strides("out's " + name, y, batched)
+    with _device_guard(device):
+        st = lib.parallax_norm_rope(rows, len(sets), _raw(positions), _raw(cos), _raw(sin), ctypes.byref(p),
+                                    _raw_stream(device))
+    if st != 0:
+        raise ParallaxError(st, "parallax_norm_rope")
+    done = {name: y for (name, _, _), y in zip(sets, ys)}
+    return tuple(done.get(name) for name in ("q", "rho", "k"))
+
+
+def norm_rope_backward(dq, drho, dk, q, rho, k, cos, sin, positions=None, *, q_weight=None, rho_weight=None,
+                       k_weight=None, eps=1e-6, norm=True, interleaved=False):
+    """Gradients of norm_rope: (dq, drho, dk, dq_weight, drho_weight, dk_weight).
+
+    dq, drho, dk: the gradients of norm_rope's results, shaped and typed like
+    q, rho, k (the forward's inputs).  Weight gradients are float32 [d], summed
+    over all rows; None without norm, and everything is None for a set that is.
+    Without given weights, the gradients of weights of one are returned.
+    """
+    sets, p, device, batched = _norm_rope_call(q, rho, k, cos, sin, positions, (q_weight, rho_weight, k_weight),
+                                               eps, norm, interleaved)
+    incoming = {"q": dq, "rho": drho, "k": dk}
+    rows, grads = (HeadRows * len(sets))(), (HeadGrads * len(sets))()
+    d = q.shape[-1]
+    dws = torch.empty(len(sets), d, dtype=torch.float32, device=device) if norm else None
+    dxs = {}
+    for i, (name, x, w) in enumerate(sets):
+        dy = incoming[name]
+        if dy is None or dy.shape != x.shape:
+            raise ValueError(f"d{name} must have shape {tuple(x.shape)}")
+        _check_device(device, (("d" + name, dy, x.dtype),))
+        dx = dxs[name] = _head_like(x)
+        r, g = rows[i], grads[i]
+        r.x, r.w, r.heads = x.data_ptr(), _raw(w), x.shape[1]
+        r.x_stride[:] = _head_strides(name, x, batched)
+        g.dy, g.dx, g.dw = dy.data_ptr(), dx.data_ptr(), _raw(dws[i]) if norm else None
+        g.dy_stride[:] = _head_strides("d" + name, dy, batched)
+        g.dx_stride[:] = _head_strides("d" + name, dx, batched)
+    with _device_guard(device):
+        ws = None
+        if norm:
+            nbytes = lib.parallax_norm_rope_backward_workspace_size(ctypes.byref(p), len(sets))
+            if nbytes == SIZE_MAX:
+                raise ParallaxError(2, "parallax_norm_rope_backward_workspace_size")
+            ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        st = lib.parallax_norm_rope_backward(rows, grads, len(sets), _raw(positions), _raw(cos), _raw(sin), _raw(ws),
+                                             0 if ws is None else ws.numel(), ctypes.byref(p), _raw_stream(device))
+    if st != 0:
+        raise ParallaxError(st, "parallax_norm_rope_backward")
+    at = {name: dws[i] for i, (name, _, _) in enumerate(sets)} if norm else {}
+    return tuple(dxs.get(n) for n in ("q", "rho", "k")) + tuple(at.get(n) for n in ("q", "rho", "k"))
+
+
+class NormRope(torch.autograd.Function):
+    """torch autograd node over norm_rope / norm_rope_backward:
+    apply(q, rho, k, q_weight, rho_weight, k_weight, cos, sin, positions, eps, norm, interleaved)
+    returns (q, rho, k).  cos and sin get no gradient."""
+
+    @staticmethod
+    def forward(ctx, q, rho, k, q_weight, rho_weight, k_weight, cos, sin, positions=None, eps=1e-6, norm=True,
+                interleaved=False):
+        # padding rows are not written: they are zero here
+        out = None if positions is None else tuple(None if x is None else torch.zeros(x.shape, dtype=x.dtype,
+                                                                                      device=x.device)
+                                                   for x in (q, rho, k))
+        out = norm_rope(q, rho, k, cos, sin, positions, q_weight=q_weight, rho_weight=rho_weight, k_weight=k_weight,
+                        eps=eps, norm=norm, interleaved=interleaved, out=out)
+        ctx.save_for_backward(q, rho, k, q_weight, rho_weight, k_weight, cos, sin, positions)
+        ctx.options = dict(eps=eps, norm=norm, interleaved=interleaved)
+        return out
+
+    @staticmethod
+    def backward(ctx, dq, drho, dk):
+        q, rho, k, qw, rw, kw, cos, sin, positions = ctx.saved_tensors
+        grads = [None if x is None else (torch.zeros_like(x) if g is None else _dense_rows(g.to(x.dtype)))
+                 for x, g in ((q, dq), (rho, drho), (k, dk))]
+        dx = norm_rope_backward(*grads, q, rho, k, cos, sin, positions, q_weight=qw, rho_weight=rw, k_weight=kw,
+                                **ctx.options)
+        dw = tuple(None if w is None else g.to(w.dtype) for w, g in zip((qw, rw, kw), dx[3:]))
+        return dx[:3] + dw + (None,) * 6
+
+
+def _dense_rows(g):
+    """g itself where the library can read its rows (broadcast and unaligned gradients are copied)."""
+    unit = 16 // g.element_size()
+    ok = g.stride(-1) == 1 and g.data_ptr() % 16 == 0 and all(s % unit == 0 for s in g.stride()[:-1])
+    return g if ok else g.contiguous()
+
+
+def _append_params(k, v, slot_map, num_pages, num_kv_heads, head_dim, dtype):
+    for name, t in (("k", k), ("v", v)):
+        if t.dim() != 3 or t.shape[1] != num_kv_heads or t.shape[2] != head_dim:
+            raise ValueError(f"{name} must be [N, {num_kv_heads}, {head_dim}], got {tuple(t.shape)}")
+        if t.numel() > 0 and t.stride(2) != 1:
+            raise ValueError(f"{name}'s last dimension must be contiguous")
+    if v.shape[0] != k.shape[0]:
+        raise ValueError(f"k has {k.shape[0]} rows and v {v.shape[0]}")
+    _check_shape("slot_map", slot_map, (k.shape[0],))
+    p = AppendParams(k.shape[0], num_kv_heads, head_dim, PAGE_SIZE, num_pages, dtype)
+    p.k_stride[:] = k.stride()[:2]
+    p.v_stride[:] = v.stride()[:2]
+    return p
+
+
+def cache_append(k, v, slot_map, k_cache, v_cache):
+    """Writes a step's keys and values into the paged pools, in place.
+
+    k, v: [N, Hkv, d] (row and head strides are free, rows 16-byte aligned), of
+    the pools' dtype (bfloat16 or float32); slot_map: int64 [N], row r goes to
+    row slot % 64 of page slot // 64 (page_plan's map; -1 skips); pools
+    [P, Hkv, 64, d] as decode and prefill_paged read them.  Slots are distinct.
+    """
+    if k_cache.dim() != 4 or k_cache.shape != v_cache.shape or k_cache.shape[2] != PAGE_SIZE:
+        raise ValueError(f"pools must be [P, Hkv, {PAGE_SIZE}, d] and alike, got {tuple(k_cache.shape)} and "
+                         f"{tuple(v_cache.shape)}")
+    P, Hkv, _, d = k_cache.shape
+    _check_shape("k_cache", k_cache, k_cache.shape)
+    _check_shape("v_cache", v_cache, v_cache.shape)
+    p = _append_params(k, v, slot_map, P, Hkv, d, _dtype_code(k_cache.dtype))
+    device = k_cache.device
+    _check_device(device, (("k", k, k_cache.dtype), ("v", v, k_cache.dtype), ("slot_map", slot_map, torch.int64),
+                           ("k_cache", k_cache, None), ("v_cache", v_cache, k_cache.dtype)))
+    with _device_guard(device):
+        st = lib.parallax_cache_append(_raw(k), _raw(v), _raw(slot_map), _raw(k_cache), _raw(v_cache),
+                                       ctypes.byref(p), _raw_stream(device))
+    if st != 0:
+        raise ParallaxError(st, "parallax_cache_append")
+
+
+def q4_block_bytes(head_dim: int) -> int:
+    """Bytes of one (page, KV head) block of the 4-bit cache."""
+    n = lib.parallax_q4_block_bytes(int(head_dim))
+    if n == 0:
+        raise ParallaxError(2, "parallax_q4_block_bytes")
+    return n
+
+
+def _q4_head_dim(kv_cache):
+    """The head_dim that a 4-bit cache's block size says."""
+    if kv_cache.dtype != torch.uint8:
+        raise TypeError(f"a 4-bit cache is a uint8 tensor, got {kv_cache.dtype}")
+    for d in (64, 128):
+        if kv_cache.shape[-1] == 72 * d:
+            return d
+    raise ValueError(f"a 4-bit cache's blocks have {q4_block_bytes(64)} or {q4_block_bytes(128)} bytes, "
+                     f"got {kv_cache.shape[-1]}")
+
+
+def q4_cache(num_pages, num_kv_heads, head_dim, device="cuda"):
+    """An empty 4-bit pool [num_pages, num_kv_heads, q4_block_bytes(head_dim)] (uint8)."""
+    return torch.zeros(num_pages, num_kv_heads, q4_block_bytes(head_dim), dtype=torch.uint8, device=device)
+
+
+def _q4_pool(kv_cache):
+    if kv_cache.dim() != 3:
+        raise ValueError(f"a 4-bit pool is [P, Hkv, block bytes], got {tuple(kv_cache.shape)}")
+    _check_shape("kv_cache", kv_cache, kv_cache.shape)
+    return kv_cache.shape[0], kv_cache.shape[1], _q4_head_dim(kv_cache)
+
+
+def cache_append_q4(k, v, slot_map, kv_cache):
+    """Quantises a step's keys and values to 4 bits into the pool, in place.
+
+    k, v: [N, Hkv, d] bfloat16; slot_map as for cache_append; kv_cache: uint8
+    [P, Hkv, q4_block_bytes(d)] (see q4_cache; parallax.h has the layout).
+    Each 64 columns of a row share a scale and a minimum.
+    """
+    P, Hkv, d = _q4_pool(kv_cache)
+    p = _append_params(k, v, slot_map, P, Hkv, d, PLX_BF16)
+    device = kv_cache.device
+    _check_device(device, (("k", k, torch.bfloat16), ("v", v, torch.bfloat16), ("slot_map", slot_map, torch.int64),
+                           ("kv_cache", kv_cache, None)))
+    with _device_guard(device):
+        st = lib.parallax_cache_append_q4(_raw(k), _raw(v), _raw(slot_map), _raw(kv_cache), ctypes.byref(p),
+                                          _raw_stream(device))
+    if st != 0:
+        raise ParallaxError(st, "parallax_cache_append_q4")
+
+
+def cache_gather_q4(kv_cache, slot_map, *, out_dtype=torch.bfloat16, out=None):
+    """The keys and values at the slots, dequantised: (k, v), each [N, Hkv, d]
+    of ``out_dtype`` (bfloat16 or float32).  Rows at slot -1 are left as
+    allocated (``out``: the two tensors to write)."""
+    P, Hkv, d = _q4_pool(kv_cache)
+    device = kv_cache.device
+    if out is None:
+        shape = (2, slot_map.shape[0], Hkv, d) if slot_map.dim() == 1 else (2, 0, Hkv, d)
+        k, v = torch.empty(shape, dtype=out_dtype, device=device)
+    else:
+        k, v = out
+    p = _append_params(k, v, slot_map, P, Hkv, d, _dtype_code(k.dtype))
+    _check_device(device, (("k", k, None), ("v", v, k.dtype), ("slot_map", slot_map, torch.int64),
+                           ("kv_cache", kv_cache, None)))
+    with _device_guard(device):
+        st = lib.parallax_cache_gather_q4(_raw(kv_cache), _raw(slot_map), _raw(k), _raw(v), ctypes.byref(p),
+                                          _raw_stream(device))
+    if st != 0:
+        raise ParallaxError(st, "parallax_cache_gather_q4")
+    return k, v
+
+
+_q4_workspaces = {}
+
+
+def _q4_workspace(device, nbytes):
+    """The 4-bit decode's workspace: one per device and stream, since calls on
+    different streams may overlap; zeroed when allocated, and every call leaves
+    its counters zero.  A captured graph gets one of its own (zeroed in the
+    graph), so that graphs replayed at once do not share it."""
+    if torch.cuda.is_current_stream_capturing():
+        return torch.zeros(nbytes, dtype=torch.uint8, device=device)
+    key = (device.index, _raw_stream(device))
+    with _ws_lock:
+        ws = _q4_workspaces.get(key)
+        if ws is None or ws.numel() < nbytes:
+            ws = _q4_workspaces[key] = torch.zeros(max(nbytes, 1 << 20), dtype=torch.uint8, device=device)
+        return ws
+
+
+def decode_q4(q, rho, kv_cache, scale=None, *, seq_lens=None, page_table=None, out=None, out_dtype=None, num_ctas=0,
+              kv_len=None):
+    """Parallax decode over the 4-bit cache.
+
+    q, rho: [B, Hq, d] bfloat16.  Paged: kv_cache uint8 [P, Hkv, block bytes],
+    page_table int32 [B, max_pages] and seq_lens int32 [B].  Contiguous:
+    kv_cache [B, Hkv, ceil(kv_len / 64), block bytes] with ``kv_len`` (default:
+    all of its pages' tokens) and optional seq_lens.  Returns out [B, Hq, d] in
+    ``out_dtype`` (default bfloat16).
+    """
+    if q.dim() != 3 or tuple(rho.shape) != tuple(q.shape):
+        raise ValueError(f"q and rho must be [B, Hq, d] and alike, got {tuple(q.shape)} and {tuple(rho.shape)}")
+    B, Hq, d = q.shape
+    paged = page_table is not None
+    if kv_cache.dim() != (3 if paged else 4):
+        raise ValueError("a paged 4-bit cache is [P, Hkv, block bytes] and a contiguous one "
+                         f"[B, Hkv, pages, block bytes], got {tuple(kv_cache.shape)}")
+    if _q4_head_dim(kv_cache) != d:
+        raise ValueError(f"the cache's head_dim {_q4_head_dim(kv_cache)} differs from the queries' {d}")
+    Hkv = kv_cache.shape[1]
+    if Hkv < 1 or Hq % Hkv:
+        raise ValueError(f"{Hq} query heads do not split into {Hkv} KV heads")
+    if paged:
+        most = page_table.shape[-1] * PAGE_SIZE
+        kv_len = most if kv_len is None else int(kv_len)
+        if kv_len > most:
+            raise ValueError(f"kv_len {kv_len} exceeds the page table's {page_table.shape[-1]} pages")
+        if seq_lens is None:
+            raise ValueError("a paged cache needs seq_lens")
+        _check_shape("page_table", page_table, (B, page_table.shape[-1]))
+    else:
+        if kv_cache.shape[0] != B:
+            raise ValueError(f"a contiguous cache holds one sequence per row: {kv_cache.shape[0]} != {B}")
+        pages = kv_cache.shape[2]
+        kv_len = pages * PAGE_SIZE if kv_len is None else int(kv_len)
+        if (kv_len + PAGE_SIZE - 1) // PAGE_SIZE != pages:
+            raise ValueError(f"kv_len {kv_len} does not fill the cache's {pages} pages of {PAGE_SIZE} tokens "
+                             "(use seq_lens for shorter sequences)")
+    if seq_lens is not None:
+        _check_shape("seq_lens", seq_lens, (B,))
+    for name, t in (("q", q), ("rho", rho), ("kv_cache", kv_cache)):
+        _check_shape(name, t, t.shape)
+    device = q.device
+    _check_device(device, (("q", q, torch.bfloat16), ("rho", rho, torch.bfloat16), ("kv_cache", kv_cache, None),
+                           ("page_table", page_table, torch.int32), ("seq_lens", seq_lens, torch.int32)))
+    out, out_dtype = _output(out, out_dtype, q.shape, torch.bfloat16, device)
+    _check_device(device, (("out", out, None),))
+    p = DecodeParams(B, Hq, Hkv, d, kv_len, PAGE_SIZE if paged else 0, kv_cache.shape[0] if paged else 0,
+                     page_table.shape[1] if paged else 0, PLX_BF16, _dtype_code(out_dtype),
+                     (1.0 / d ** 0.5) if scale is None else float(scale), int(num_ctas))
+    with _device_guard(device):
+        nbytes = lib.parallax_decode_q4_workspace_size(ctypes.byref(p), 0)
+        if nbytes == SIZE_MAX:
+            raise ParallaxError(1, "parallax_decode_q4_workspace_size")
+        ws = _q4_workspace(device, nbytes)
+        st = lib.parallax_decode_q4(_raw(q), _raw(rho), _raw(kv_cache), _raw(page_table), _raw(seq_lens), _raw(out),
+                                    _raw(ws), ws.numel(), ctypes.byref(p), _raw_stream(device))
+    if st != 0:
+        raise ParallaxError(st, "parallax_decode_q4")
     return out
 
 

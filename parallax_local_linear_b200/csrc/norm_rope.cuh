@@ -1,0 +1,373 @@
+// RMS norm of head rows with the position rotation, forward and backward (the
+// definition is at parallax_norm_rope in parallax.h).
+//
+//     n = x r w,  r = (mean x^2 + eps)^(-1/2),   y = R n
+// with R the rotation of column pairs.  R is orthogonal, so with dn = R^T dy
+// and g = dn w
+//     dx = r (g - x r^2 mean(g x)),   dw = sum over rows dn x r.
+//
+// Both directions read each row once and write one row: HBM bounds them.  A
+// row lies in the 16-byte vectors of LPR neighbouring lanes (16 lanes for 128
+// bf16 columns), so its sums are butterfly shuffles among them and the row
+// never leaves registers.  A lane's rotation partner holds the pair's other
+// column (another lane of the row, or the lane itself when interleaved), and
+// the lane forms only its own column of the pair: the partner's raw vector
+// comes by four shuffles.  A group of lanes takes several heads of one token,
+// so a token's cos and sin are read once for them.
+#pragma once
+
+#include "ptx.cuh"
+
+namespace plx {
+
+constexpr int kNrThreads = 256;
+constexpr int kNrMaxSets = 3;
+
+struct NormRopeSet {
+  const void* x;
+  void* y;                // backward: dx
+  const void* dy;         // backward only
+  const void* w;
+  float* dw;              // backward only
+  int heads, chunks;      // chunks of `hpg` heads
+  long long xs[3], ys[3], ds[3];   // element strides of batch entry, token, head
+};
+
+struct NormRopeArgs {
+  NormRopeSet set[kNrMaxSets];
+  const int32_t* positions;
+  const float* cos;
+  const float* sin;
+  float* partial;         // backward: [sets][gridDim.x][D]
+  long long pos_batch_stride;
+  int sets, B, T, rot, max_pos, norm, hpg;
+  int head_inner;         // consecutive groups take a token's chunks, not consecutive tokens
+  float eps;
+};
+
+// A lane's share of a row: E values from one 16-byte vector.
+template <typename T>
+struct RowVec;
+template <>
+struct RowVec<__nv_bfloat16> {
+  static constexpr int E = 8;
+  static __device__ __forceinline__ void unpack(const uint4& v, float (&f)[E]) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      f[2 * i] = bf16_lo_f(w[i]);
+      f[2 * i + 1] = bf16_hi_f(w[i]);
+    }
+  }
+  static __device__ __forceinline__ uint4 pack(const float (&f)[E]) {
+    return make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7]));
+  }
+};
+template <>
+struct RowVec<float> {
+  static constexpr int E = 4;
+  static __device__ __forceinline__ void unpack(const uint4& v, float (&f)[E]) {
+    f[0] = __uint_as_float(v.x);
+    f[1] = __uint_as_float(v.y);
+    f[2] = __uint_as_float(v.z);
+    f[3] = __uint_as_float(v.w);
+  }
+  static __device__ __forceinline__ uint4 pack(const float (&f)[E]) {
+    return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+  }
+};
+
+// The lane's own columns of the rotation at one position:
+//     y_e = n_e c[e] + partner(n)_e s[e].
+// (c, s) is (cos, -sin) for the first column of a pair, (cos, sin) for the
+// second and (1, 0) past rot.
+template <int E>
+struct Turn {
+  float c[E], s[E];
+};
+
+template <int E, bool kInter>
+__device__ __forceinline__ void load_turn(const NormRopeArgs& a, int pos, int col0, Turn<E>& t) {
+  const int half = a.rot / 2;
+  if (col0 >= a.rot) {
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      t.c[e] = 1.f;
+      t.s[e] = 0.f;
+    }
+    return;
+  }
+  const size_t row = (size_t)pos * half;
+  if (kInter) {
+    const float* cp = a.cos + row + col0 / 2;
+    const float* sp = a.sin + row + col0 / 2;
+#pragma unroll
+    for (int i = 0; i < E / 2; ++i) {
+      const float c = __ldg(cp + i), s = __ldg(sp + i);
+      t.c[2 * i] = t.c[2 * i + 1] = c;
+      t.s[2 * i] = -s;
+      t.s[2 * i + 1] = s;
+    }
+  } else {
+    const bool second = col0 >= half;   // rot is a multiple of 16: a lane's columns lie in one half
+    const int f0 = second ? col0 - half : col0;
+#pragma unroll
+    for (int i = 0; i < E / 4; ++i) {
+      const float4 c = __ldg(reinterpret_cast<const float4*>(a.cos + row + f0) + i);
+      const float4 s = __ldg(reinterpret_cast<const float4*>(a.sin + row + f0) + i);
+      t.c[4 * i] = c.x;
+      t.c[4 * i + 1] = c.y;
+      t.c[4 * i + 2] = c.z;
+      t.c[4 * i + 3] = c.w;
+      t.s[4 * i] = second ? s.x : -s.x;
+      t.s[4 * i + 1] = second ? s.y : -s.y;
+      t.s[4 * i + 2] = second ? s.z : -s.z;
+      t.s[4 * i + 3] = second ? s.w : -s.w;
+    }
+  }
+}
+
+// The partner's vector of the same row.
+template <int E, bool kInter>
+__device__ __forceinline__ uint4 partner_vec(const uint4& v, int src) {
+  if (kInter) return v;
+  return make_uint4(__shfl_sync(0xffffffffu, v.x, src), __shfl_sync(0xffffffffu, v.y, src),
+                    __shfl_sync(0xffffffffu, v.z, src), __shfl_sync(0xffffffffu, v.w, src));
+}
+template <int E, bool kInter>
+__device__ __forceinline__ void swap_pairs(float (&f)[E]) {   // interleaved: the partner of column e is e ^ 1
+  if (!kInter) return;
+#pragma unroll
+  for (int e = 0; e < E; e += 2) {
+    const float t = f[e];
+    f[e] = f[e + 1];
+    f[e + 1] = t;
+  }
+}
+
+template <int LPR>
+__device__ __forceinline__ float row_sum(float v) {
+#pragma unroll
+  for (int o = LPR / 2; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+template <typename T, int D, bool kInter>
+struct NrLane {
+  static constexpr int E = RowVec<T>::E, LPR = D / E, RPW = 32 / LPR;
+  int col0, src;       // first column, lane of the rotation partner
+  bool turned;         // this lane's columns turn
+
+  __device__ __forceinline__ explicit NrLane(const NormRopeArgs& a) {
+    const int lane = threadIdx.x & 31, l = lane % LPR;
+    col0 = l * E;
+    turned = col0 < a.rot;
+    const int shift = a.rot / 2 / E;
+    src = !turned || kInter ? lane : (col0 < a.rot / 2 ? lane + shift : lane - shift);
+  }
+  __device__ __forceinline__ void weights(const void* w, float (&own)[E], float (&other)[E]) const {
+    // the sets of a warp's groups differ, so every lane takes part in the shuffles
+    uint4 v = make_uint4(0, 0, 0, 0);
+    if (w != nullptr) v = __ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(w) + col0));
+    RowVec<T>::unpack(v, own);
+    RowVec<T>::unpack(partner_vec<E, kInter>(v, src), other);
+    swap_pairs<E, kInter>(other);
+    if (w == nullptr) {
+#pragma unroll
+      for (int e = 0; e < E; ++e) own[e] = other[e] = 1.f;
+    }
+  }
+};
+
+// Where group `item` works: its token and its set's heads h0 .. h1 - 1.  Sets
+// and tokens are uniform over a group of LPR lanes, not over the warp.
+struct NrItem {
+  int s, b, t, h0, h1;
+  bool live;
+};
+__device__ __forceinline__ NrItem nr_item(const NormRopeArgs& a, long long item, int chunks, int s_first, int s_last) {
+  const long long tokens = (long long)a.B * a.T;
+  NrItem it;
+  it.live = item < tokens * chunks;
+  if (!it.live) item = 0;
+  const long long tok = a.head_inner ? item / chunks : item % tokens;
+  int c = (int)(a.head_inner ? item % chunks : item / tokens);
+  it.s = s_first;
+  while (it.s < s_last && c >= a.set[it.s].chunks) c -= a.set[it.s++].chunks;
+  it.b = (int)(tok / a.T);
+  it.t = (int)(tok % a.T);
+  it.h0 = c * a.hpg;
+  it.h1 = min(a.set[it.s].heads, it.h0 + a.hpg);
+  return it;
+}
+
+// The position of a token, or -1 for padding (a bad one is reported).
+__device__ __forceinline__ int nr_position(const NormRopeArgs& a, int b, int t) {
+  if (a.positions == nullptr && t < a.max_pos) return t;
+  const int pos = a.positions ? __ldg(a.positions + b * a.pos_batch_stride + t) : t;
+  if (a.rot > 0 && pos >= 0 && pos < a.max_pos) return pos;
+  if (a.rot == 0 && pos >= 0) return pos;
+  if (pos != -1) report_error(32 /* PLX_DEVERR_BAD_POSITION */);
+  return -1;
+}
+
+template <typename T, int D, bool kInter>
+__global__ void __launch_bounds__(kNrThreads) norm_rope_kernel(const NormRopeArgs a) {
+  using L = NrLane<T, D, kInter>;
+  constexpr int E = L::E;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const L ln(a);
+  int chunks = 0;
+  for (int s = 0; s < a.sets; ++s) chunks += a.set[s].chunks;
+  const long long group = ((long long)blockIdx.x * kNrThreads + threadIdx.x) / L::LPR;
+  const NrItem it = nr_item(a, group, chunks, 0, a.sets - 1);
+  const NormRopeSet& set = a.set[it.s];
+  const int pos = it.live ? nr_position(a, it.b, it.t) : -1;
+  const bool live = pos >= 0;
+  Turn<E> tn;
+  load_turn<E, kInter>(a, live ? pos : 0, live ? ln.col0 : D, tn);
+  float w[E], wp[E];
+  ln.weights(set.w, w, wp);
+  const T* x = static_cast<const T*>(set.x) + it.b * set.xs[0] + it.t * set.xs[1] + ln.col0;
+  T* y = static_cast<T*>(set.y) + it.b * set.ys[0] + it.t * set.ys[1] + ln.col0;
+  constexpr int U = 4;   // rows in flight
+  for (int j = 0; j < a.hpg; j += U) {
+    uint4 v[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int h = it.h0 + j + u;
+      v[u] = make_uint4(0, 0, 0, 0);
+      if (live && h < it.h1) v[u] = *reinterpret_cast<const uint4*>(x + h * set.xs[2]);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      float f[E], p[E], o[E];
+      RowVec<T>::unpack(v[u], f);
+      RowVec<T>::unpack(partner_vec<E, kInter>(v[u], ln.src), p);
+      swap_pairs<E, kInter>(p);
+      float r = 1.f;
+      if (a.norm) {
+        float ss = 0.f;
+#pragma unroll
+        for (int e = 0; e < E; ++e) ss = fmaf(f[e] * (1.f / D), f[e], ss);   // overflows only with the mean itself
+        r = rsqrtf(row_sum<L::LPR>(ss) + a.eps);
+      }
+#pragma unroll
+      for (int e = 0; e < E; ++e) o[e] = f[e] * r * w[e] * tn.c[e] + p[e] * r * wp[e] * tn.s[e];
+      const int h = it.h0 + j + u;
+      if (live && h < it.h1) *reinterpret_cast<uint4*>(y + h * set.ys[2]) = RowVec<T>::pack(o);
+    }
+  }
+}
+
+// Backward.  CTAs of blockIdx.y = s walk over set s; each leaves its sum for
+// dw in partial[s][blockIdx.x].
+template <typename T, int D, bool kInter>
+__global__ void __launch_bounds__(kNrThreads) norm_rope_bwd_kernel(const NormRopeArgs a) {
+  using L = NrLane<T, D, kInter>;
+  constexpr int E = L::E;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const L ln(a);
+  const int s = blockIdx.y;
+  const NormRopeSet& set = a.set[s];
+  float w[E], wp[E], acc[E];
+  ln.weights(set.w, w, wp);
+#pragma unroll
+  for (int e = 0; e < E; ++e) acc[e] = 0.f;
+  const long long groups = (long long)gridDim.x * kNrThreads / L::LPR;
+  const long long items = (long long)a.B * a.T * set.chunks;
+  const long long group = ((long long)blockIdx.x * kNrThreads + threadIdx.x) / L::LPR;
+  // Every lane of a warp makes the same number of rounds: the sums' shuffles need all of them.
+  for (long long base = 0; base < items; base += groups) {
+    const NrItem it = nr_item(a, base + group, set.chunks, s, s);
+    const int pos = it.live ? nr_position(a, it.b, it.t) : -1;
+    const bool live = pos >= 0;
+    Turn<E> tn;
+    load_turn<E, kInter>(a, live ? pos : 0, live ? ln.col0 : D, tn);
+    const T* x = static_cast<const T*>(set.x) + it.b * set.xs[0] + it.t * set.xs[1] + ln.col0;
+    const T* dy = static_cast<const T*>(set.dy) + it.b * set.ds[0] + it.t * set.ds[1] + ln.col0;
+    T* dx = static_cast<T*>(set.y) + it.b * set.ys[0] + it.t * set.ys[1] + ln.col0;
+    constexpr int U = 2;
+    for (int j = 0; j < a.hpg; j += U) {
+      uint4 vx[U], vd[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int h = it.h0 + j + u;
+        vx[u] = vd[u] = make_uint4(0, 0, 0, 0);
+        if (live && h < it.h1) {
+          if (a.norm) vx[u] = *reinterpret_cast<const uint4*>(x + h * set.xs[2]);
+          vd[u] = *reinterpret_cast<const uint4*>(dy + h * set.ds[2]);
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        float f[E], d[E], p[E], o[E];
+        RowVec<T>::unpack(vx[u], f);
+        RowVec<T>::unpack(vd[u], d);
+        RowVec<T>::unpack(partner_vec<E, kInter>(vd[u], ln.src), p);
+        swap_pairs<E, kInter>(p);
+        float ss = 0.f, gx = 0.f;
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          d[e] = d[e] * tn.c[e] - p[e] * tn.s[e];   // dn: the transposed rotation
+          const float fd = f[e] * (1.f / D);
+          ss = fmaf(fd, f[e], ss);
+          gx = fmaf(d[e] * w[e], fd, gx);
+        }
+        if (a.norm) {
+          ss = row_sum<L::LPR>(ss);
+          gx = row_sum<L::LPR>(gx);
+          const float r = rsqrtf(ss + a.eps);
+          const float k = r * r * gx;
+#pragma unroll
+          for (int e = 0; e < E; ++e) {
+            o[e] = r * (d[e] * w[e] - f[e] * k);
+            acc[e] = fmaf(d[e], f[e] * r, acc[e]);
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < E; ++e) o[e] = d[e];
+        }
+        const int h = it.h0 + j + u;
+        if (it.live && h < it.h1) *reinterpret_cast<uint4*>(dx + h * set.ys[2]) = RowVec<T>::pack(o);
+      }
+    }
+  }
+  if (set.dw == nullptr) return;
+  __shared__ float part[kNrThreads / L::LPR][D];
+#pragma unroll
+  for (int e = 0; e < E; ++e) part[threadIdx.x / L::LPR][ln.col0 + e] = acc[e];
+  __syncthreads();
+  if (threadIdx.x < D) {
+    float sum = 0.f;
+#pragma unroll
+    for (int g = 0; g < kNrThreads / L::LPR; ++g) sum += part[g][threadIdx.x];
+    a.partial[((size_t)s * gridDim.x + blockIdx.x) * D + threadIdx.x] = sum;
+  }
+}
+
+// dw of set blockIdx.x: the sum of its `n` partial rows, in a fixed order.
+template <int D>
+__global__ void __launch_bounds__(kNrThreads) norm_rope_dw_kernel(const NormRopeArgs a, int n) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  float* dw = a.set[blockIdx.x].dw;
+  if (dw == nullptr) return;
+  constexpr int kWays = kNrThreads / D;
+  __shared__ float part[kWays][D];
+  const int d = threadIdx.x % D, way = threadIdx.x / D;
+  const float* p = a.partial + (size_t)blockIdx.x * n * D + d;
+  float sum = 0.f;
+  for (int i = way; i < n; i += kWays) sum += p[(size_t)i * D];
+  part[way][d] = sum;
+  __syncthreads();
+  if (way == 0) {
+#pragma unroll
+    for (int k = 1; k < kWays; ++k) sum += part[k][d];
+    dw[d] = sum;
+  }
+}
+
+}  // namespace plx

@@ -23,6 +23,10 @@
 #include "prefill_bwd.cuh"
 #include "project.cuh"
 #include "lla.cuh"
+#include "pages.cuh"
+#include "norm_rope.cuh"
+#include "cache_q4.cuh"
+#include "decode_q4.cuh"
 
 namespace {
 
@@ -1030,3 +1034,5 @@ plx_status parallax_last_device_error(cudaStream_t stream, int32_t* code) {
 }
 
 }  // extern "C"
+
+#include "serving_abi.cuh"

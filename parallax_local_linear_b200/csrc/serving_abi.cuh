@@ -1,0 +1,425 @@
+// C entry points of the operators around attention: page plan, head norm with
+// rotation, cache append and gather, and the 4-bit decode.  Included by
+// parallax.cu after its host helpers.
+#pragma once
+
+namespace {
+
+using namespace plx;
+
+// -------------------------------------------------------------- page plan
+plx_status validate_page_plan(const plx_page_plan_params* p) {
+  if (p == nullptr) return PLX_ERR_INVALID_ARG;
+  if (p->batch < 1 || p->num_rows < 0 || p->num_pages < 1 || p->max_pages_per_seq < 1 || p->num_free < 0)
+    return PLX_ERR_INVALID_ARG;
+  if (p->page_size != kPage || p->batch > kPlanMaxBatch) return PLX_ERR_UNSUPPORTED;
+  if ((int64_t)p->max_pages_per_seq * kPage >= (int64_t)INT32_MAX) return PLX_ERR_UNSUPPORTED;
+  return PLX_OK;
+}
+
+// ------------------------------------------------------- norm and rotation
+bool strides_ok(const int64_t* s, int n, int elt) {
+  for (int i = 0; i < n; ++i)
+    if (s[i] % (16 / elt) != 0) return false;
+  return true;
+}
+
+plx_status validate_norm_rope(const plx_head_rows* rows, const plx_head_grads* grads, int32_t num_sets,
+                              const float* cos, const float* sin, const int32_t* positions,
+                              const plx_norm_rope_params* p) {
+  if (p == nullptr || rows == nullptr || num_sets < 1 || num_sets > kNrMaxSets) return PLX_ERR_INVALID_ARG;
+  if (p->batch < 1 || p->tokens < 0 || p->rot_dim < 0 || p->max_pos < 0) return PLX_ERR_INVALID_ARG;
+  if (p->dtype != PLX_F32 && p->dtype != PLX_BF16) return PLX_ERR_INVALID_ARG;
+  if ((p->interleaved != 0 && p->interleaved != 1) || (p->norm != 0 && p->norm != 1)) return PLX_ERR_INVALID_ARG;
+  if (p->norm && !(std::isfinite(p->eps) && p->eps > 0.f)) return PLX_ERR_INVALID_ARG;
+  if (p->head_dim != 64 && p->head_dim != 128) return PLX_ERR_UNSUPPORTED;
+  if (p->rot_dim > p->head_dim || p->rot_dim % 16 != 0) return PLX_ERR_INVALID_ARG;
+  if (p->rot_dim > 0) {
+    if (cos == nullptr || sin == nullptr || !aligned(cos, 16) || !aligned(sin, 16) || p->max_pos < 1)
+      return PLX_ERR_INVALID_ARG;
+    if (positions == nullptr && p->tokens > p->max_pos) return PLX_ERR_INVALID_ARG;
+  }
+  if (positions && (!aligned(positions, 4) || p->pos_batch_stride < 0)) return PLX_ERR_INVALID_ARG;
+  const int elt = p->dtype == PLX_BF16 ? 2 : 4;
+  for (int i = 0; i < num_sets; ++i) {
+    const plx_head_rows& r = rows[i];
+    if (r.heads < 1) return PLX_ERR_INVALID_ARG;
+    if ((int64_t)r.heads * p->batch * p->tokens >= (int64_t)INT32_MAX) return PLX_ERR_UNSUPPORTED;
+    if (r.w && (!p->norm || !aligned(r.w, 16))) return PLX_ERR_INVALID_ARG;
+    if (!aligned(r.x, 16) || !strides_ok(r.x_stride, 3, elt)) return PLX_ERR_INVALID_ARG;
+    if (grads == nullptr) {
+      if (!r.x || !r.y || !aligned(r.y, 16) || !strides_ok(r.y_stride, 3, elt)) return PLX_ERR_INVALID_ARG;
+    } else {
+      const plx_head_grads& g = grads[i];
+      if ((!r.x && p->norm) || !g.dy || !g.dx || !aligned(g.dy, 16) || !aligned(g.dx, 16)) return PLX_ERR_INVALID_ARG;
+      if (!strides_ok(g.dy_stride, 3, elt) || !strides_ok(g.dx_stride, 3, elt)) return PLX_ERR_INVALID_ARG;
+      if (g.dw && (!p->norm || !aligned(g.dw, 4))) return PLX_ERR_INVALID_ARG;
+    }
+  }
+  return PLX_OK;
+}
+
+constexpr int kNrBwdCtasPerSm = 2;
+
+int norm_rope_bwd_ctas(int num_sms, int num_sets) {
+  const int n = num_sms * kNrBwdCtasPerSm / num_sets;
+  return n < 1 ? 1 : n;
+}
+
+NormRopeArgs norm_rope_args(const plx_head_rows* rows, int32_t num_sets, const int32_t* positions, const float* cos,
+                            const float* sin, const plx_norm_rope_params* p, int hpg) {
+  NormRopeArgs a{};
+  a.positions = positions;
+  a.cos = cos;
+  a.sin = sin;
+  a.pos_batch_stride = p->pos_batch_stride;
+  a.sets = num_sets;
+  a.B = p->batch;
+  a.T = p->tokens;
+  a.rot = p->rot_dim;
+  a.max_pos = p->max_pos;
+  a.norm = p->norm;
+  a.eps = p->eps;
+  a.hpg = hpg;
+  // packed rows keep a token's heads together; [B, H, T, d] keeps a head's tokens together
+  a.head_inner = rows[0].x_stride[2] < rows[0].x_stride[1] ? 1 : 0;
+  for (int i = 0; i < num_sets; ++i) {
+    NormRopeSet& s = a.set[i];
+    s.x = rows[i].x;
+    s.y = rows[i].y;
+    s.w = rows[i].w;
+    s.heads = rows[i].heads;
+    s.chunks = (rows[i].heads + hpg - 1) / hpg;
+    for (int k = 0; k < 3; ++k) {
+      s.xs[k] = rows[i].x_stride[k];
+      s.ys[k] = rows[i].y_stride[k];
+    }
+  }
+  return a;
+}
+
+template <typename T, int D, bool kInter>
+plx_status launch_norm_rope(const NormRopeArgs& a, cudaStream_t stream) {
+  constexpr int per_cta = kNrThreads / NrLane<T, D, kInter>::LPR;
+  long long chunks = 0;
+  for (int i = 0; i < a.sets; ++i) chunks += a.set[i].chunks;
+  const long long groups = (long long)a.B * a.T * chunks;
+  return launch_pdl(norm_rope_kernel<T, D, kInter>, dim3((unsigned)((groups + per_cta - 1) / per_cta)),
+                    dim3(kNrThreads), 0, stream, a) == cudaSuccess
+             ? PLX_OK
+             : PLX_ERR_CUDA;
+}
+
+template <typename T, int D, bool kInter>
+plx_status launch_norm_rope_bwd(const NormRopeArgs& a, int ctas, bool dw, cudaStream_t stream) {
+  if (launch_pdl(norm_rope_bwd_kernel<T, D, kInter>, dim3(ctas, a.sets), dim3(kNrThreads), 0, stream, a) !=
+      cudaSuccess)
+    return PLX_ERR_CUDA;
+  if (!dw) return PLX_OK;
+  return launch_pdl(norm_rope_dw_kernel<D>, dim3(a.sets), dim3(kNrThreads), 0, stream, a, ctas) == cudaSuccess
+             ? PLX_OK
+             : PLX_ERR_CUDA;
+}
+
+// Heads that a group of lanes takes for one token: enough to have its cos and
+// sin once for several rows, few enough that every SM has groups.
+int norm_rope_heads_per_group(const plx_head_rows* rows, int32_t num_sets, const plx_norm_rope_params* p) {
+  const int lanes = p->head_dim * (p->dtype == PLX_BF16 ? 2 : 4) / 16;
+  long long heads = 0;
+  for (int i = 0; i < num_sets; ++i) heads += rows[i].heads;
+  const int sms = current_device_sms();
+  const long long fill = (long long)(sms > 0 ? sms : 148) * 4 * kNrThreads / lanes;
+  int hpg = 8;
+  while (hpg > 1 && (long long)p->batch * p->tokens * heads / hpg < fill) hpg /= 2;
+  return hpg;
+}
+
+// ------------------------------------------------------------ cache append
+plx_status validate_append(const plx_append_params* p) {
+  if (p == nullptr) return PLX_ERR_INVALID_ARG;
+  if (p->num_rows < 0 || p->num_kv_heads < 1 || p->num_pages < 1) return PLX_ERR_INVALID_ARG;
+  if (p->dtype != PLX_F32 && p->dtype != PLX_BF16) return PLX_ERR_INVALID_ARG;
+  if (p->head_dim != 64 && p->head_dim != 128) return PLX_ERR_UNSUPPORTED;
+  if (p->page_size != kQ4Page) return PLX_ERR_UNSUPPORTED;
+  if ((int64_t)p->num_rows * p->num_kv_heads * 32 >= (int64_t)INT32_MAX * 128) return PLX_ERR_UNSUPPORTED;
+  const int elt = p->dtype == PLX_BF16 ? 2 : 4;
+  if (!strides_ok(p->k_stride, 2, elt) || !strides_ok(p->v_stride, 2, elt)) return PLX_ERR_INVALID_ARG;
+  return PLX_OK;
+}
+
+AppendArgs append_args(const int64_t* slots, const plx_append_params* p) {
+  AppendArgs a{};
+  a.slots = slots;
+  a.N = p->num_rows;
+  a.Hkv = p->num_kv_heads;
+  a.num_pages = p->num_pages;
+  const int vec = p->dtype == PLX_BF16 ? 8 : 4;   // elements of a 16-byte vector
+  for (int i = 0; i < 2; ++i) {
+    a.ks[i] = p->k_stride[i] / vec;
+    a.vs[i] = p->v_stride[i] / vec;
+  }
+  return a;
+}
+
+template <typename Kernel>
+plx_status launch_rows(Kernel kern, const AppendArgs& a, int lanes, cudaStream_t stream) {
+  const long long threads = (long long)a.N * a.Hkv * lanes;
+  return launch_pdl(kern, dim3((unsigned)((threads + kAppendThreads - 1) / kAppendThreads)), dim3(kAppendThreads), 0,
+                    stream, a) == cudaSuccess
+             ? PLX_OK
+             : PLX_ERR_CUDA;
+}
+
+// -------------------------------------------------------------- 4-bit decode
+plx_status validate_decode_q4(const plx_decode_params* p) {
+  plx_status st = validate_decode(p);
+  if (st != PLX_OK) return st;
+  if (p->in_dtype != PLX_BF16) return PLX_ERR_UNSUPPORTED;
+  return PLX_OK;
+}
+
+size_t decode_q4_workspace(const plx_decode_params* p, int num_sms) {
+  const DecodePlan pl = plan_decode(p, num_sms);
+  return pl.counter_bytes + pl.slot_bytes;
+}
+
+}  // namespace
+
+extern "C" {
+
+plx_status parallax_page_plan(const int32_t* cached_lens, const int32_t* new_lens, int32_t* page_table,
+                              const int32_t* free_pages, const int32_t* free_head, int32_t* seq_lens,
+                              int32_t* cu_seqlens, int64_t* slot_map, int32_t* positions, int32_t* pages_used,
+                              const plx_page_plan_params* p, cudaStream_t stream) {
+  plx_status st = validate_page_plan(p);
+  if (st != PLX_OK) return st;
+  if (!cached_lens || !new_lens || !page_table || !seq_lens || !cu_seqlens || !pages_used) return PLX_ERR_INVALID_ARG;
+  if (p->num_free > 0 && !free_pages) return PLX_ERR_INVALID_ARG;
+  if (p->num_rows > 0 && (!slot_map || !positions)) return PLX_ERR_INVALID_ARG;
+  const size_t B = p->batch, R = p->num_rows;
+  struct Range {
+    const void* p;
+    size_t n, align;
+  };
+  const Range in[] = {{cached_lens, 4 * B, 4}, {new_lens, 4 * B, 4}, {free_pages, 4 * (size_t)p->num_free, 4},
+                      {free_head, (size_t)(free_head ? 4 : 0), 4}};
+  const Range out[] = {{page_table, 4 * B * p->max_pages_per_seq, 4}, {seq_lens, 4 * B, 4}, {cu_seqlens, 4 * B + 4, 4},
+                       {slot_map, 8 * R, 8}, {positions, 4 * R, 4}, {pages_used, 4, 4}};
+  for (const Range& o : out) {
+    if (!aligned(o.p, o.align)) return PLX_ERR_INVALID_ARG;
+    for (const Range& i : in)
+      if (i.n > 0 && o.n > 0 && overlaps(o.p, o.n, i.p, i.n)) return PLX_ERR_INVALID_ARG;
+    for (const Range& q : out)
+      if (&q != &o && q.n > 0 && o.n > 0 && overlaps(o.p, o.n, q.p, q.n)) return PLX_ERR_INVALID_ARG;
+  }
+  for (const Range& i : in)
+    if (!aligned(i.p, i.align)) return PLX_ERR_INVALID_ARG;
+  const int num_sms = current_device_sms();
+  if (num_sms <= 0) return PLX_ERR_CUDA;
+  PagePlanArgs a{};
+  a.cached = cached_lens;
+  a.fresh = new_lens;
+  a.table = page_table;
+  a.free_pages = free_pages;
+  a.free_head = free_head;
+  a.seq_lens = seq_lens;
+  a.cu = cu_seqlens;
+  a.slots = slot_map;
+  a.positions = positions;
+  a.used = pages_used;
+  a.B = p->batch;
+  a.rows = p->num_rows;
+  a.num_pages = p->num_pages;
+  a.max_pages = p->max_pages_per_seq;
+  a.num_free = p->num_free;
+  // one CTA per two rows a thread, and one per 64 requests (a warp takes four)
+  const int64_t by_rows = ((int64_t)p->num_rows + 2 * kPlanThreads - 1) / (2 * kPlanThreads);
+  const int64_t by_requests = ((int64_t)p->batch + 63) / 64;
+  int64_t ctas = by_rows > by_requests ? by_rows : by_requests;
+  if (ctas > num_sms) ctas = num_sms;
+  const int smem = plan_smem_bytes(a.B);
+  if (smem > 48 * 1024 && set_smem(page_plan_kernel, plan_smem_bytes(kPlanMaxBatch)) != cudaSuccess) return PLX_ERR_CUDA;
+  return launch_pdl(page_plan_kernel, dim3((unsigned)ctas), dim3(kPlanThreads), smem, stream, a) == cudaSuccess
+             ? PLX_OK
+             : PLX_ERR_CUDA;
+}
+
+plx_status parallax_norm_rope(const plx_head_rows* rows, int32_t num_sets, const int32_t* positions,
+                              const float* cos, const float* sin, const plx_norm_rope_params* p,
+                              cudaStream_t stream) {
+  plx_status st = validate_norm_rope(rows, nullptr, num_sets, cos, sin, positions, p);
+  if (st != PLX_OK) return st;
+  if (p->tokens == 0) return PLX_OK;
+  const NormRopeArgs a = norm_rope_args(rows, num_sets, positions, cos, sin, p,
+                                        norm_rope_heads_per_group(rows, num_sets, p));
+  const bool il = p->interleaved != 0;
+  if (p->dtype == PLX_BF16) {
+    if (p->head_dim == 64)
+      return il ? launch_norm_rope<__nv_bfloat16, 64, true>(a, stream)
+                : launch_norm_rope<__nv_bfloat16, 64, false>(a, stream);
+    return il ? launch_norm_rope<__nv_bfloat16, 128, true>(a, stream)
+              : launch_norm_rope<__nv_bfloat16, 128, false>(a, stream);
+  }
+  if (p->head_dim == 64)
+    return il ? launch_norm_rope<float, 64, true>(a, stream) : launch_norm_rope<float, 64, false>(a, stream);
+  return il ? launch_norm_rope<float, 128, true>(a, stream) : launch_norm_rope<float, 128, false>(a, stream);
+}
+
+size_t parallax_norm_rope_backward_workspace_size(const plx_norm_rope_params* p, int32_t num_sets) {
+  if (p == nullptr || num_sets < 1 || num_sets > kNrMaxSets) return (size_t)-1;
+  if (p->head_dim != 64 && p->head_dim != 128) return (size_t)-1;
+  const int num_sms = current_device_sms();
+  if (num_sms <= 0) return (size_t)-1;
+  return (size_t)num_sets * norm_rope_bwd_ctas(num_sms, num_sets) * p->head_dim * sizeof(float);
+}
+
+plx_status parallax_norm_rope_backward(const plx_head_rows* rows, const plx_head_grads* grads, int32_t num_sets,
+                                       const int32_t* positions, const float* cos, const float* sin,
+                                       void* workspace, size_t workspace_bytes, const plx_norm_rope_params* p,
+                                       cudaStream_t stream) {
+  if (grads == nullptr) return PLX_ERR_INVALID_ARG;
+  plx_status st = validate_norm_rope(rows, grads, num_sets, cos, sin, positions, p);
+  if (st != PLX_OK) return st;
+  bool dw = false;
+  for (int i = 0; i < num_sets; ++i) dw = dw || grads[i].dw != nullptr;
+  const int num_sms = current_device_sms();
+  if (num_sms <= 0) return PLX_ERR_CUDA;
+  const int ctas = norm_rope_bwd_ctas(num_sms, num_sets);
+  if (dw && (workspace == nullptr || !aligned(workspace, 16) ||
+             workspace_bytes < (size_t)num_sets * ctas * p->head_dim * sizeof(float)))
+    return PLX_ERR_WORKSPACE;
+  NormRopeArgs a = norm_rope_args(rows, num_sets, positions, cos, sin, p, norm_rope_heads_per_group(rows, num_sets, p));
+  a.partial = static_cast<float*>(workspace);
+  a.head_inner = grads[0].dy_stride[2] < grads[0].dy_stride[1] ? 1 : 0;
+  for (int i = 0; i < num_sets; ++i) {
+    NormRopeSet& s = a.set[i];
+    s.dy = grads[i].dy;
+    s.y = grads[i].dx;
+    s.dw = grads[i].dw;
+    for (int k = 0; k < 3; ++k) {
+      s.ds[k] = grads[i].dy_stride[k];
+      s.ys[k] = grads[i].dx_stride[k];
+    }
+  }
+  const bool il = p->interleaved != 0;
+  if (p->dtype == PLX_BF16) {
+    if (p->head_dim == 64)
+      return il ? launch_norm_rope_bwd<__nv_bfloat16, 64, true>(a, ctas, dw, stream)
+                : launch_norm_rope_bwd<__nv_bfloat16, 64, false>(a, ctas, dw, stream);
+    return il ? launch_norm_rope_bwd<__nv_bfloat16, 128, true>(a, ctas, dw, stream)
+              : launch_norm_rope_bwd<__nv_bfloat16, 128, false>(a, ctas, dw, stream);
+  }
+  if (p->head_dim == 64)
+    return il ? launch_norm_rope_bwd<float, 64, true>(a, ctas, dw, stream)
+              : launch_norm_rope_bwd<float, 64, false>(a, ctas, dw, stream);
+  return il ? launch_norm_rope_bwd<float, 128, true>(a, ctas, dw, stream)
+            : launch_norm_rope_bwd<float, 128, false>(a, ctas, dw, stream);
+}
+
+plx_status parallax_cache_append(const void* k, const void* v, const int64_t* slot_map, void* k_cache,
+                                 void* v_cache, const plx_append_params* p, cudaStream_t stream) {
+  plx_status st = validate_append(p);
+  if (st != PLX_OK) return st;
+  if (!k_cache || !v_cache || !aligned(k_cache, 16) || !aligned(v_cache, 16)) return PLX_ERR_INVALID_ARG;
+  if (p->num_rows == 0) return PLX_OK;
+  if (!k || !v || !slot_map || !aligned(k, 16) || !aligned(v, 16) || !aligned(slot_map, 8)) return PLX_ERR_INVALID_ARG;
+  AppendArgs a = append_args(slot_map, p);
+  a.k = k;
+  a.v = v;
+  a.k_pool = k_cache;
+  a.v_pool = v_cache;
+  const int vpr = p->head_dim * (p->dtype == PLX_BF16 ? 2 : 4) / 16;
+  if (vpr == 8) return launch_rows(cache_append_kernel<8>, a, 8, stream);
+  if (vpr == 16) return launch_rows(cache_append_kernel<16>, a, 16, stream);
+  return launch_rows(cache_append_kernel<32>, a, 32, stream);
+}
+
+size_t parallax_q4_block_bytes(int32_t head_dim) {
+  return head_dim == 64 ? Q4Block<64>::kBytes : head_dim == 128 ? Q4Block<128>::kBytes : 0;
+}
+
+plx_status parallax_cache_append_q4(const void* k, const void* v, const int64_t* slot_map, void* kv_cache,
+                                    const plx_append_params* p, cudaStream_t stream) {
+  plx_status st = validate_append(p);
+  if (st != PLX_OK) return st;
+  if (p->dtype != PLX_BF16) return PLX_ERR_UNSUPPORTED;
+  if (!kv_cache || !aligned(kv_cache, 16)) return PLX_ERR_INVALID_ARG;
+  if (p->num_rows == 0) return PLX_OK;
+  if (!k || !v || !slot_map || !aligned(k, 16) || !aligned(v, 16) || !aligned(slot_map, 8)) return PLX_ERR_INVALID_ARG;
+  AppendArgs a = append_args(slot_map, p);
+  a.k = k;
+  a.v = v;
+  a.cache = static_cast<uint8_t*>(kv_cache);
+  return p->head_dim == 64 ? launch_rows(cache_append_q4_kernel<64>, a, 8, stream)
+                           : launch_rows(cache_append_q4_kernel<128>, a, 16, stream);
+}
+
+plx_status parallax_cache_gather_q4(const void* kv_cache, const int64_t* slot_map, void* k, void* v,
+                                    const plx_append_params* p, cudaStream_t stream) {
+  plx_status st = validate_append(p);
+  if (st != PLX_OK) return st;
+  if (!kv_cache || !aligned(kv_cache, 16)) return PLX_ERR_INVALID_ARG;
+  if (p->num_rows == 0) return PLX_OK;
+  if (!k || !v || !slot_map || !aligned(k, 16) || !aligned(v, 16) || !aligned(slot_map, 8)) return PLX_ERR_INVALID_ARG;
+  AppendArgs a = append_args(slot_map, p);
+  a.k_out = k;
+  a.v_out = v;
+  a.cache = const_cast<uint8_t*>(static_cast<const uint8_t*>(kv_cache));
+  const int lanes = p->head_dim / 8;
+  if (p->head_dim == 64)
+    return p->dtype == PLX_BF16 ? launch_rows(cache_gather_q4_kernel<64, true>, a, lanes, stream)
+                                : launch_rows(cache_gather_q4_kernel<64, false>, a, lanes, stream);
+  return p->dtype == PLX_BF16 ? launch_rows(cache_gather_q4_kernel<128, true>, a, lanes, stream)
+                              : launch_rows(cache_gather_q4_kernel<128, false>, a, lanes, stream);
+}
+
+size_t parallax_decode_q4_workspace_size(const plx_decode_params* p, int32_t num_sms) {
+  if (validate_decode_q4(p) != PLX_OK) return (size_t)-1;
+  if (num_sms <= 0) num_sms = current_device_sms();
+  if (num_sms <= 0) return (size_t)-1;
+  return decode_q4_workspace(p, num_sms);
+}
+
+plx_status parallax_decode_q4(const void* q, const void* rho, const void* kv_cache, const int32_t* page_table,
+                              const int32_t* seq_lens, void* out, void* workspace, size_t workspace_bytes,
+                              const plx_decode_params* p, cudaStream_t stream) {
+  plx_status st = validate_decode_q4(p);
+  if (st != PLX_OK) return st;
+  if (!q || !rho || !kv_cache || !out) return PLX_ERR_INVALID_ARG;
+  if (!aligned(q, 16) || !aligned(rho, 16) || !aligned(kv_cache, 16) || !aligned(out, 16)) return PLX_ERR_INVALID_ARG;
+  const bool paged = p->page_size != 0;
+  if (paged && (page_table == nullptr || seq_lens == nullptr)) return PLX_ERR_INVALID_ARG;
+  if (!paged && page_table != nullptr) return PLX_ERR_INVALID_ARG;
+  if ((page_table && !aligned(page_table, 4)) || (seq_lens && !aligned(seq_lens, 4))) return PLX_ERR_INVALID_ARG;
+  const int num_sms = current_device_sms();
+  if (num_sms <= 0) return PLX_ERR_CUDA;
+  if (workspace == nullptr || !aligned(workspace, 256) || workspace_bytes < decode_q4_workspace(p, num_sms))
+    return PLX_ERR_WORKSPACE;
+  if (p->kv_len == 0) {   // every sequence is empty: the output is zero
+    const size_t n = (size_t)p->batch * p->num_q_heads * p->head_dim * (p->out_dtype == PLX_BF16 ? 2 : 4);
+    return note(cudaMemsetAsync(out, 0, n, stream)) == cudaSuccess ? PLX_OK : PLX_ERR_CUDA;
+  }
+  DecodeQ4Args a{};
+  a.q = static_cast<const __nv_bfloat16*>(q);
+  a.rho = static_cast<const __nv_bfloat16*>(rho);
+  a.cache = static_cast<const uint8_t*>(kv_cache);
+  a.page_table = page_table;
+  a.seq_lens = seq_lens;
+  a.out = out;
+  a.B = p->batch;
+  a.Hq = p->num_q_heads;
+  a.Hkv = p->num_kv_heads;
+  a.group = p->num_q_heads / p->num_kv_heads;
+  a.kv_len = p->kv_len;
+  a.paged = paged ? 1 : 0;
+  a.num_pages = paged ? p->num_pages : 0;
+  a.max_pages = paged ? p->max_pages_per_seq : 0;
+  a.scale_log2 = p->scale * 1.4426950408889634f;
+  a.out_bf16 = p->out_dtype == PLX_BF16 ? 1 : 0;
+  const dim3 grid(a.B * a.Hq), block(kQ4Warps * 32);
+  const cudaError_t e = p->head_dim == 64 ? launch_pdl(decode_q4_kernel<64>, grid, block, 0, stream, a)
+                                          : launch_pdl(decode_q4_kernel<128>, grid, block, 0, stream, a);
+  return e == cudaSuccess ? PLX_OK : PLX_ERR_CUDA;
+}
+
+}  // extern "C"
