@@ -623,9 +623,13 @@ plx_status parallax_cache_gather_q4(const void* kv_cache, const int64_t* slot_ma
  *               16-byte aligned.  Rows past a sequence's length may hold
  *               anything.
  *   workspace   device, >= parallax_decode_q4_workspace_size() bytes, 256-byte
- *               aligned, with parallax_decode's rule: the counter region at its
- *               front (4 bytes per (sequence, KV head), padded to 256) is zero
- *               before the first use, and every call leaves it zero.
+ *               aligned, workspace_bytes a multiple of 256.  Its last 4 bytes
+ *               per (sequence, KV head), padded to 256, count the pieces of
+ *               each unit: they are zero before the first use, and every call
+ *               leaves them zero.  One workspace serves calls of any
+ *               parameters with the same workspace_bytes as long as the
+ *               partials (the rest of what a call needs, from the front)
+ *               never reach another call's counters.
  *   the rest    as parallax_decode.  Hq / Hkv <= 8.
  * One launch. */
 size_t parallax_decode_q4_workspace_size(const plx_decode_params* p, int32_t num_sms);

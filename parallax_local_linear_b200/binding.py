@@ -1059,18 +1059,23 @@ def cache_gather_q4(kv_cache, slot_map, *, out_dtype=torch.bfloat16, out=None):
 _q4_workspaces = {}
 
 
-def _q4_workspace(device, nbytes):
+def _q4_workspace(device, nbytes, units):
     """The 4-bit decode's workspace: one per device and stream, since calls on
-    different streams may overlap; zeroed when allocated, and every call leaves
-    its counters zero.  A captured graph gets one of its own (zeroed in the
-    graph), so that graphs replayed at once do not share it."""
+    different streams may overlap.  Partials are at its front and the counters
+    (4 bytes a unit) at its end; it is large enough for the most of either that
+    a call has needed, so that one call's partials never reach another's
+    counters, and zeroed when allocated.  A captured graph gets one of its own
+    (zeroed in the graph), so that graphs replayed at once do not share it."""
     if torch.cuda.is_current_stream_capturing():
         return torch.zeros(nbytes, dtype=torch.uint8, device=device)
+    counters = (4 * units + 255) & ~255
     key = (device.index, _raw_stream(device))
     with _ws_lock:
-        ws = _q4_workspaces.get(key)
-        if ws is None or ws.numel() < nbytes:
-            ws = _q4_workspaces[key] = torch.zeros(max(nbytes, 1 << 20), dtype=torch.uint8, device=device)
+        ws, most_slots, most_counters = _q4_workspaces.get(key, (None, 1 << 20, 1 << 14))
+        if ws is None or nbytes - counters > most_slots or counters > most_counters:
+            most_slots, most_counters = max(most_slots, nbytes - counters), max(most_counters, counters)
+            ws = torch.zeros(most_slots + most_counters, dtype=torch.uint8, device=device)
+            _q4_workspaces[key] = ws, most_slots, most_counters
         return ws
 
 
@@ -1128,7 +1133,7 @@ def decode_q4(q, rho, kv_cache, scale=None, *, seq_lens=None, page_table=None, o
         nbytes = lib.parallax_decode_q4_workspace_size(ctypes.byref(p), 0)
         if nbytes == SIZE_MAX:
             raise ParallaxError(1, "parallax_decode_q4_workspace_size")
-        ws = _q4_workspace(device, nbytes)
+        ws = _q4_workspace(device, nbytes, B * Hkv)
         st = lib.parallax_decode_q4(_raw(q), _raw(rho), _raw(kv_cache), _raw(page_table), _raw(seq_lens), _raw(out),
                                     _raw(ws), ws.numel(), ctypes.byref(p), _raw_stream(device))
     if st != 0:

@@ -1,9 +1,50 @@
-// Parallax decode over the 4-bit cache.
+// Parallax decode over the 4-bit cache (bound: HBM; 144 bytes a token and KV
+// head at d = 128, so the arithmetic per byte is 3.6 times the bf16 decode's
+// and issue slots come next).
 //
-// One query head per CTA; each warp takes 32-token chunks, a lane per token
-// for the scores and probe values and a lane per D/32 columns for the value
-// sums, as the single-pass form of decode.cuh.
+// The sums are those of the single-pass form in decode.cuh,
+//     l = sum e_i,  c = sum e_i a_i,  O1 = sum e_i v_i,  O2 = sum e_i a_i v_i,
+// on k = s n + m and v = s n + m (codes n, scales s and minima m, one pair per
+// token and group of 64 columns).  Scales and minima stay out of the products:
+//     q.k   = sum_g s_g (q_g . n_g) + m_g (sum of q_g)
+//     O1_d  = sum_i (e_i s_i) n_id + sum_i e_i m_i        (d in group g of i's row)
+// so the tensor cores multiply bare codes.  A code masked out of its word is
+// already an fp16 number: bits 0..3 of a half are the subnormal n 2^-24 and bits
+// 4..7 are n 2^-20.  One AND makes two operands; the powers of two are taken
+// out of the queries on one side and of the results on the other.
+//
+// Operands (mma.sync m16n8k16, fp16 in, fp32 sums; the contraction has 8 columns
+// for 4 heads, far below what a tcgen05 tile needs, and its operands would have
+// to be written back to shared memory):
+//     [S A] (16 tokens x 8) = K (16 x d) . [q_0 rho_0 q_1 rho_1 ..] (d x 8)
+//     [O1 O2] (16 columns x 8) += V^T (16 x 16 tokens) . [p_0 pa_0 p_1 pa_1 ..] (16 x 8)
+// Codes are the A operand both times, read from shared memory with one 16-byte
+// load per row and lane in the block's own layout.  A lane's accumulators
+// belong to one head (lane % 4) throughout: scores and probes of tokens r and
+// r + 8, r = lane / 4, then O1 and O2 of d/8 columns.  The weights change
+// from accumulator to operand by a transposing move (movmatrix).
+//
+// Ranges.  q and rho are scaled by a power of two to at most 2^14 per row
+// (exact: they are bf16).  e s and e a s have to fit fp16, whatever the size of
+// s and a: the running reference is not the largest score alone but
+//     M = max_i (x_i + log2(max_g s_ig max(1, |a_i|))),      p_i = 2^(x_i - M + 14)
+// with x_i the score in powers of two, so every product is at most 2^14.  Each
+// enters as hi + lo halves (22 bits, and nothing above 2^-38 of the largest is
+// lost), since a rounding to fp16 alone would show in rows of a few keys.
+// a_i is taken relative to the probe value of the first token the warp sees of
+// a unit; any constant leaves the output unchanged, and merging pieces shifts
+// c and O2 to a common one.
+//
+// Work.  The pages of every (sequence, KV head) unit are laid end to end and
+// cut into equal runs, one per warp: no warp waits for another until its run
+// is done.  A warp keeps its own ring of bulk copies (one page and head is one
+// contiguous block) and refills a stage as it leaves it.  Units that lie
+// inside a run are finished in registers; pieces of cut units are merged in
+// the CTA after one barrier, and across CTAs in the workspace, by the last CTA
+// that finishes a piece (decode.cuh's rule and counters).
 #pragma once
+
+#include <cuda_fp16.h>
 
 #include "cache_q4.cuh"
 #include "decode.cuh"
@@ -11,129 +52,716 @@
 namespace plx {
 
 constexpr int kQ4Warps = 8;
+constexpr int kQ4Threads = kQ4Warps * 32;
 
 struct DecodeQ4Args {
   const __nv_bfloat16* q;
   const __nv_bfloat16* rho;
   const uint8_t* cache;
-  const int32_t* page_table;
-  const int32_t* seq_lens;
+  const int32_t* page_table;       // [B, max_pages] or null: blocks [B, Hkv, pages of kv_len]
+  const int32_t* seq_lens;         // [B] or null
   void* out;
-  int B, Hq, Hkv, group, kv_len, paged, num_pages, max_pages;
+  float* slots;                    // [2 * gridDim.x][group][2 D + 4]
+  int32_t* counters;               // [B * Hkv]
+  int B, Hq, Hkv, group, kv_len, num_pages, max_pages;
   float scale_log2;
   int out_bf16;
+  int min_pages;                   // a CTA takes at least this many pages
+  unsigned long long wait_ns;
 };
 
-template <int D>
-__global__ void __launch_bounds__(kQ4Warps * 32) decode_q4_kernel(const DecodeQ4Args a) {
-  using B = Q4Block<D>;
-  constexpr int C = D / 32;
-  __shared__ float s_q[2][D];
-  __shared__ float s_m[kQ4Warps], s_l[kQ4Warps], s_c[kQ4Warps];
-  __shared__ float s_o[kQ4Warps][2][D];
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int b = blockIdx.x / a.Hq, hq = blockIdx.x % a.Hq, kvh = hq / a.group;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  int len = a.seq_lens ? __ldg(a.seq_lens + b) : a.kv_len;
-  if (len < 0 || len > a.kv_len) {
-    if (tid == 0) report_error(4 /* PLX_DEVERR_BAD_LENGTH */);
-    len = len < 0 ? 0 : a.kv_len;
+template <int D, int NT>
+struct Q4Smem {
+  static constexpr int kStages = D == 64 ? 4 : 2;                  // per warp
+  static constexpr int kRing = kStages * Q4Block<D>::kBytes;       // per warp
+  static constexpr int kRow = 2 * D + 4;                           // a head's state: m l c aref O1 O2
+  static constexpr int kState = 4 * NT * kRow * 4;                 // bytes of a piece
+  static constexpr int kStateOff = kQ4Warps * kRing;
+  static constexpr int kBarOff = kStateOff + kQ4Warps * kState;
+  static constexpr int kMetaOff = kBarOff + kQ4Warps * kStages * 8;
+  static constexpr int kPreOff = kMetaOff + kQ4Warps * 8 * 4;
+  static constexpr int kBytes = kPreOff + (kQ4Threads + 4) * 4 + 64;
+  static_assert(kState <= kRing, "a warp's last piece fits in its ring");
+};
+
+// D += A * B, m16n8k16, fp16 inputs, fp32 accumulate.
+__device__ __forceinline__ void mma_f16_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                              uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// The transpose of the 8 x 8 matrix of halves that the warp holds two to a lane.
+__device__ __forceinline__ uint32_t transpose_8x8(uint32_t v) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
+}
+
+__device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ float2 unpack_half(uint32_t v) {
+  return __half22float2(*reinterpret_cast<const __half2*>(&v));
+}
+
+__device__ __forceinline__ float lg2(float x) {
+  float y;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// N consecutive words of shared memory.
+template <int N>
+__device__ __forceinline__ void lds_words(const uint8_t* p, uint32_t (&w)[N]) {
+  if constexpr (N == 4) {
+    const uint4 v = *reinterpret_cast<const uint4*>(p);
+    w[0] = v.x;
+    w[1] = v.y;
+    w[2] = v.z;
+    w[3] = v.w;
+  } else if constexpr (N == 2) {
+    const uint2 v = *reinterpret_cast<const uint2*>(p);
+    w[0] = v.x;
+    w[1] = v.y;
+  } else {
+    static_assert(N == 1, "1, 2 or 4 words");
+    w[0] = *reinterpret_cast<const uint32_t*>(p);
   }
-  for (int d = tid; d < D; d += kQ4Warps * 32) {
-    s_q[0][d] = __bfloat162float(a.q[((size_t)b * a.Hq + hq) * D + d]);
-    s_q[1][d] = __bfloat162float(a.rho[((size_t)b * a.Hq + hq) * D + d]);
+}
+
+// ---------------------------------------------------------------- the page space
+// pre[i]: pages (of all heads) of the sequences before thread i's share of
+// `per` sequences; pre[kQ4Threads] = T.
+struct Q4Space {
+  const DecodeQ4Args& a;
+  const int* pre;
+  int per;
+  long long T, G;
+
+  __device__ __forceinline__ int len(int b) const {
+    if (a.seq_lens == nullptr) return a.kv_len;
+    return min(max(__ldg(a.seq_lens + b), 0), a.kv_len);
   }
-  __syncthreads();
-  const int tiles_max = (a.kv_len + kQ4Page - 1) / kQ4Page;
-  auto block_of = [&](int tile) {
-    size_t i = ((size_t)b * a.Hkv + kvh) * tiles_max + tile;
-    if (a.paged) {
-      int p = __ldg(a.page_table + (size_t)b * a.max_pages + tile);
-      if (p < 0 || p >= a.num_pages) {
-        report_error(1 /* PLX_DEVERR_BAD_PAGE */);
-        p = 0;
+  __device__ __forceinline__ int pages(int b) const { return (len(b) + kQ4Page - 1) / kQ4Page; }
+  __device__ __forceinline__ long long start(long long c) const { return c * T / G; }
+  __device__ __forceinline__ long long owner(long long x) const { return ((x + 1) * G + T - 1) / T - 1; }
+};
+
+// A place in the page space: page `local` of unit (b, hu), which starts at page
+// `ua` of the space and has `tiles` pages.
+struct Q4Cursor {
+  int b, hu, local, tiles, len, ua;
+
+  // The whole warp calls this together.
+  __device__ __forceinline__ void seek(const Q4Space& s, int x) {
+    const int lane = threadIdx.x & 31;
+    int base = 0;
+    if (s.a.seq_lens == nullptr) {
+      const int per_seq = s.pages(0) * s.a.Hkv;
+      b = x / per_seq;
+      base = b * per_seq;
+    } else {
+      int lo = 0, hi = kQ4Threads - 1;   // last share with pre <= x that is not empty
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (s.pre[mid] <= x) lo = mid; else hi = mid - 1;
       }
-      i = (size_t)p * a.Hkv + kvh;
-    }
-    return a.cache + i * B::kBytes;
-  };
-  float m = -INFINITY, l = 0.f, c = 0.f, o1[C], o2[C];
+      const int i = lo * s.per + lane;
+      const int n = lane < s.per && i < s.a.B ? s.pages(i) * s.a.Hkv : 0;
+      int inc = n;
 #pragma unroll
-  for (int i = 0; i < C; ++i) o1[i] = o2[i] = 0.f;
-  for (int t0 = warp * 32; t0 < len; t0 += kQ4Warps * 32) {
-    const uint8_t* blk = block_of(t0 / kQ4Page);
-    const int row = t0 % kQ4Page + lane;
-    const bool ok = t0 + lane < len;
-    float s = -INFINITY, av = 0.f;
-    if (ok) {
-      s = 0.f;
-      const uint32_t* kr = reinterpret_cast<const uint32_t*>(blk + row * (D / 2));
-      const uint32_t* kp = reinterpret_cast<const uint32_t*>(blk + B::kKParams) + row * B::kGroups;
-      for (int w = 0; w < D / 8; ++w) {
-        const int col = 32 * (w % B::kWords) + 8 * (w / B::kWords);
-        const uint32_t word = kr[w], par = kp[col / 64];
-        for (int i = 0; i < 8; ++i) {
-          const float x = fmaf(bf16_lo_f(par), (float)((word >> (16 * (i & 1) + 4 * (i >> 1))) & 15u), bf16_hi_f(par));
-          s = fmaf(s_q[0][col + i], x, s);
-          av = fmaf(s_q[1][col + i], x, av);
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += v;
+      }
+      const int first = __ffs(__ballot_sync(0xffffffffu, s.pre[lo] + inc > x)) - 1;
+      b = lo * s.per + first;
+      base = s.pre[lo] + __shfl_sync(0xffffffffu, inc - n, first);
+    }
+    len = s.len(b);
+    tiles = (len + kQ4Page - 1) / kQ4Page;
+    hu = (x - base) / tiles;
+    local = (x - base) % tiles;
+    ua = base + hu * tiles;
+  }
+  __device__ __forceinline__ void next_page(const Q4Space& s) {
+    if (++local < tiles) return;
+    local = 0;
+    ua += tiles;
+    if (++hu < s.a.Hkv) return;
+    hu = 0;
+    tiles = 0;
+    while (++b < s.a.B) {
+      len = s.len(b);
+      tiles = (len + kQ4Page - 1) / kQ4Page;
+      if (tiles > 0) return;
+    }
+  }
+  // The page's entry in the page table, and from it its block.
+  __device__ __forceinline__ int entry(const Q4Space& s) const {
+    return s.a.page_table == nullptr ? 0 : __ldg(s.a.page_table + (size_t)b * s.a.max_pages + local);
+  }
+  __device__ __forceinline__ size_t block(const Q4Space& s, int page) const {
+    const DecodeQ4Args& a = s.a;
+    if (a.page_table == nullptr)
+      return ((size_t)b * a.Hkv + hu) * (size_t)((a.kv_len + kQ4Page - 1) / kQ4Page) + local;
+    if (page < 0 || page >= a.num_pages) {
+      report_error(1 /* PLX_DEVERR_BAD_PAGE */);
+      page = 0;
+    }
+    return (size_t)page * a.Hkv + hu;
+  }
+};
+
+// Writes four neighbouring columns of one output row.
+__device__ __forceinline__ void store_out4(const DecodeQ4Args& a, size_t idx, float v0, float v1, float v2, float v3) {
+  if (a.out_bf16)
+    *reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(a.out) + idx) =
+        make_uint2(pack_bf16(v0, v1), pack_bf16(v2, v3));
+  else
+    *reinterpret_cast<float4*>(reinterpret_cast<float*>(a.out) + idx) = make_float4(v0, v1, v2, v3);
+}
+
+// The running state of a warp for one unit, in registers: lane (r, c) =
+// (lane / 4, lane % 4) holds heads c + 4 t and of each the columns 32 j + 4 r
+// + 0 .. 3.
+template <int D, int NT>
+struct Q4WarpState {
+  static constexpr int G = D / 64, J = D / 32;
+  float o[NT][2 * J][4];       // codes' sums: [2 j + h]: columns +2 h, +2 h + 1 (O1, O2 each)
+  float pm[NT][G][2];          // sum p m, sum pa m of the lane's tokens
+  float m[NT], l[NT], c[NT], aref[NT];
+
+  __device__ __forceinline__ void reset() {
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+#pragma unroll
+      for (int i = 0; i < 2 * J; ++i) o[t][i][0] = o[t][i][1] = o[t][i][2] = o[t][i][3] = 0.f;
+#pragma unroll
+      for (int g = 0; g < G; ++g) pm[t][g][0] = pm[t][g][1] = 0.f;
+      m[t] = -INFINITY;
+      l[t] = c[t] = aref[t] = 0.f;
+    }
+  }
+  // Sums over the lanes that hold other tokens of the same heads; the codes'
+  // powers of two and the minima's sums go into o.
+  __device__ __forceinline__ void close() {
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+#pragma unroll
+      for (int off = 4; off < 32; off <<= 1) {
+        l[t] += __shfl_xor_sync(0xffffffffu, l[t], off);
+        c[t] += __shfl_xor_sync(0xffffffffu, c[t], off);
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+          pm[t][g][0] += __shfl_xor_sync(0xffffffffu, pm[t][g][0], off);
+          pm[t][g][1] += __shfl_xor_sync(0xffffffffu, pm[t][g][1], off);
         }
       }
-      s *= a.scale_log2;
-    }
-    const float m_new = fmaxf(m, warp_max(s));
-    const float alpha = ex2(m - m_new), p = ex2(s - m_new), pa = p * av;
-    m = m_new;
-    l = l * alpha + p;
-    c = c * alpha + pa;
 #pragma unroll
-    for (int i = 0; i < C; ++i) {
-      o1[i] *= alpha;
-      o2[i] *= alpha;
-    }
-    for (int j = 0; j < min(32, len - t0); ++j) {
-      const float pj = __shfl_sync(0xffffffffu, p, j), paj = __shfl_sync(0xffffffffu, pa, j);
-      const int r = t0 % kQ4Page + j;
-#pragma unroll
-      for (int i = 0; i < C; ++i) {
-        const int col = lane + 32 * i;
-        const uint32_t word = reinterpret_cast<const uint32_t*>(blk + B::kV + (r / 2) * D)[B::kWords * (lane / 4) + i];
-        const uint32_t par = reinterpret_cast<const uint32_t*>(blk + B::kVParams)[r * B::kGroups + col / 64];
-        const float x = fmaf(bf16_lo_f(par), (float)((word >> (16 * (r & 1) + 4 * (lane % 4))) & 15u), bf16_hi_f(par));
-        o1[i] = fmaf(pj, x, o1[i]);
-        o2[i] = fmaf(paj, x, o2[i]);
+      for (int i = 0; i < 2 * J; ++i) {
+        o[t][i][0] = fmaf(o[t][i][0], 16777216.f, pm[t][i / 4][0]);
+        o[t][i][1] = fmaf(o[t][i][1], 16777216.f, pm[t][i / 4][1]);
+        o[t][i][2] = fmaf(o[t][i][2], 1048576.f, pm[t][i / 4][0]);
+        o[t][i][3] = fmaf(o[t][i][3], 1048576.f, pm[t][i / 4][1]);
       }
     }
   }
-  l = warp_sum(l);
-  c = warp_sum(c);
-  if (lane == 0) {
-    s_m[warp] = m;
-    s_l[warp] = l;
-    s_c[warp] = c;
-  }
+  // After close(): the finished output rows.
+  __device__ __forceinline__ void write_out(const DecodeQ4Args& a, int b, int hu) const {
+    const int r = (threadIdx.x & 31) >> 2, hc = threadIdx.x & 3;
 #pragma unroll
-  for (int i = 0; i < C; ++i) {
-    s_o[warp][0][lane + 32 * i] = o1[i];
-    s_o[warp][1][lane + 32 * i] = o2[i];
+    for (int t = 0; t < NT; ++t) {
+      const int h = 4 * t + hc;
+      if (h >= a.group) continue;
+      const size_t row = ((size_t)b * a.Hq + (size_t)hu * a.group + h) * D;
+#pragma unroll
+      for (int j = 0; j < J; ++j)
+        store_out4(a, row + 32 * j + 4 * r, finalize(o[t][2 * j][0], o[t][2 * j][1], l[t], c[t]),
+                   finalize(o[t][2 * j][2], o[t][2 * j][3], l[t], c[t]),
+                   finalize(o[t][2 * j + 1][0], o[t][2 * j + 1][1], l[t], c[t]),
+                   finalize(o[t][2 * j + 1][2], o[t][2 * j + 1][3], l[t], c[t]));
+    }
+  }
+  // After close(): the piece, as [head][m l c aref O1 O2].
+  __device__ __forceinline__ void deposit(float* dst) const {
+    const int r = (threadIdx.x & 31) >> 2, hc = threadIdx.x & 3;
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      float* row = dst + (4 * t + hc) * (2 * D + 4);
+      if (r == 0) *reinterpret_cast<float4*>(row) = make_float4(m[t], l[t], c[t], aref[t]);
+#pragma unroll
+      for (int j = 0; j < J; ++j) {
+        *reinterpret_cast<float4*>(row + 4 + 32 * j + 4 * r) =
+            make_float4(o[t][2 * j][0], o[t][2 * j][2], o[t][2 * j + 1][0], o[t][2 * j + 1][2]);
+        *reinterpret_cast<float4*>(row + 4 + D + 32 * j + 4 * r) =
+            make_float4(o[t][2 * j][1], o[t][2 * j][3], o[t][2 * j + 1][1], o[t][2 * j + 1][3]);
+      }
+    }
+  }
+};
+
+// The sum of pieces of one unit for one head and column.
+struct Q4Merged {
+  float M, L, C, aref, O1, O2;
+};
+// `first`, `next(i)` walk the pieces' numbers, up to `end`; `piece(i)` points
+// to piece i's row of the head.
+template <int D, typename Next, typename Piece, typename Load>
+__device__ __forceinline__ Q4Merged merge_pieces(int first, int end, int d, Next next, Piece piece, Load load) {
+  Q4Merged s;
+  s.M = -INFINITY;
+  for (int i = first; i < end; i = next(i)) s.M = fmaxf(s.M, load(piece(i)));
+  s.L = s.C = s.O1 = s.O2 = 0.f;
+  s.aref = load(piece(first) + 3);
+  for (int i = first; i < end; i = next(i)) {
+    const float* p = piece(i);
+    const float al = ex2(load(p) - s.M), l = load(p + 1), shift = load(p + 3) - s.aref, o1 = load(p + 4 + d);
+    s.L = fmaf(al, l, s.L);
+    s.C = fmaf(al, fmaf(shift, l, load(p + 2)), s.C);
+    s.O1 = fmaf(al, o1, s.O1);
+    s.O2 = fmaf(al, fmaf(shift, o1, load(p + 4 + D + d)), s.O2);
+  }
+  return s;
+}
+
+template <int D, int NT>
+__global__ void __launch_bounds__(kQ4Threads, 1) decode_q4_kernel(const DecodeQ4Args a) {
+  using SM = Q4Smem<D, NT>;
+  using B = Q4Block<D>;
+  constexpr int S = SM::kStages, G = D / 64, J = D / 32;
+  extern __shared__ __align__(128) uint8_t q4_smem[];
+  uint64_t* bars = reinterpret_cast<uint64_t*>(q4_smem + SM::kBarOff);
+  int* meta = reinterpret_cast<int*>(q4_smem + SM::kMetaOff);   // [warp]: first piece's unit, ua, ub; last piece's
+  int* pre = reinterpret_cast<int*>(q4_smem + SM::kPreOff);
+  __shared__ int s_last;
+  __shared__ int s_part[kQ4Warps];
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int r = lane >> 2, hc = lane & 3;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  uint64_t* full = bars + warp * S;
+  if (lane == 0) {
+#pragma unroll
+    for (int s = 0; s < S; ++s) mbar_init(&full[s], 1);
+    fence_mbarrier_init();
+  }
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+
+  // ---- the page space
+  Q4Space sp{a, pre, (a.B + kQ4Threads - 1) / kQ4Threads, 0, 1};
+  if (a.seq_lens == nullptr) {
+    sp.T = (long long)a.B * a.Hkv * ((a.kv_len + kQ4Page - 1) / kQ4Page);
+  } else {
+    int sum = 0;
+    const int b0 = min(a.B, tid * sp.per), b1 = min(a.B, b0 + sp.per);
+    for (int b = b0; b < b1; ++b) {
+      const int n = __ldg(a.seq_lens + b);
+      if ((n < 0 || n > a.kv_len) && blockIdx.x == 0) report_error(4 /* PLX_DEVERR_BAD_LENGTH */);
+      sum += sp.pages(b) * a.Hkv;
+    }
+    int inc = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += v;
+    }
+    if (lane == 31) s_part[warp] = inc;
+    __syncthreads();
+    int base = 0, total = 0;
+#pragma unroll
+    for (int w = 0; w < kQ4Warps; ++w) {
+      if (w == warp) base = total;
+      total += s_part[w];
+    }
+    pre[tid] = base + inc - sum;
+    sp.T = total;
+    // sequences without tokens have no pages: their rows are zero
+    for (int b = blockIdx.x; b < a.B; b += gridDim.x)
+      if (sp.len(b) == 0)
+        for (int i = tid; i < a.Hq * D / 4; i += kQ4Threads) store_out4(a, (size_t)b * a.Hq * D + 4 * i, 0.f, 0.f, 0.f, 0.f);
   }
   __syncthreads();
-  for (int d = tid; d < D; d += kQ4Warps * 32) {
-    float M = -INFINITY, L = 0.f, Cc = 0.f, O1 = 0.f, O2 = 0.f;
-    for (int w = 0; w < kQ4Warps; ++w) M = fmaxf(M, s_m[w]);
-    for (int w = 0; w < kQ4Warps; ++w) {
-      const float al = s_m[w] == -INFINITY ? 0.f : ex2(s_m[w] - M);
-      L += al * s_l[w];
-      Cc += al * s_c[w];
-      O1 += al * s_o[w][0][d];
-      O2 += al * s_o[w][1][d];
+  const long long most = (sp.T + a.min_pages - 1) / a.min_pages;
+  sp.G = most < (long long)gridDim.x ? most : (long long)gridDim.x;
+  if ((long long)blockIdx.x >= sp.G) return;
+
+  const long long W = sp.G * kQ4Warps, gw = (long long)blockIdx.x * kQ4Warps + warp;
+  const int y0 = (int)(gw * sp.T / W), y1 = (int)((gw + 1) * sp.T / W), n = y1 - y0;
+  uint8_t* ring = q4_smem + warp * SM::kRing;
+  float* first_state = reinterpret_cast<float*>(q4_smem + SM::kStateOff + warp * SM::kState);
+  if (lane < 8) meta[warp * 8 + lane] = -1;
+  __syncwarp();
+
+  if (n > 0) {
+    Q4Cursor cur, ahead;
+    cur.seek(sp, y0);
+    ahead = cur;
+    int issued = 0, entry = ahead.entry(sp);
+    // The next block into stage issued % S.  The entry of the one after it is
+    // read now and looked at when that one is issued, a page later.
+    auto issue = [&] {
+      const size_t blk = ahead.block(sp, entry);
+      if (lane == 0) {
+        uint64_t* bar = &full[issued % S];
+        mbar_arrive_expect_tx(bar, B::kBytes);
+        bulk_load(ring + (issued % S) * B::kBytes, a.cache + blk * B::kBytes, B::kBytes, bar);
+      }
+      ++issued;
+      if (issued < n) {
+        ahead.next_page(sp);
+        entry = ahead.entry(sp);
+      }
+    };
+    for (int i = 0; i < S && i < n; ++i) issue();
+
+    Q4WarpState<D, NT> st;
+    uint32_t qf[NT][D / 16][2];     // [q rho ..] operand
+    float fs[NT], fa[NT];           // factors of a score (in powers of two) and of a probe value
+    float qs[NT][G], rs[NT][G];     // group sums of q (times the scale) and rho
+    bool alive = true, first_done = false;
+    int seg = 0;                    // pages of the current unit done by this warp
+
+    for (int i = 0; i < n; ++i) {
+      if (seg == 0) {
+        st.reset();
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          const int h = 4 * t + (r >> 1);
+          const bool live = h < a.group;
+          const __nv_bfloat16* row = ((r & 1) ? a.rho : a.q) +
+                                     ((size_t)cur.b * a.Hq + (size_t)cur.hu * a.group + (live ? h : 0)) * D + 8 * hc;
+          uint4 v[J];
+#pragma unroll
+          for (int j = 0; j < J; ++j)
+            v[j] = live ? __ldg(reinterpret_cast<const uint4*>(row + 32 * j)) : make_uint4(0, 0, 0, 0);
+          float f[J][8], mx = 0.f, gsum[G];
+#pragma unroll
+          for (int g = 0; g < G; ++g) gsum[g] = 0.f;
+#pragma unroll
+          for (int j = 0; j < J; ++j) {
+            const uint32_t w[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              f[j][2 * e] = bf16_lo_f(w[e]);
+              f[j][2 * e + 1] = bf16_hi_f(w[e]);
+              mx = fmaxf(mx, fmaxf(fabsf(f[j][2 * e]), fabsf(f[j][2 * e + 1])));
+              gsum[j / 2] += f[j][2 * e] + f[j][2 * e + 1];
+            }
+          }
+#pragma unroll
+          for (int off = 1; off < 4; off <<= 1) {
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+#pragma unroll
+            for (int g = 0; g < G; ++g) gsum[g] += __shfl_xor_sync(0xffffffffu, gsum[g], off);
+          }
+          // 2^up takes the row's largest entry into [2^13, 2^14); clamped so
+          // that the power and its inverse times 2^24 are normal numbers
+          const int up = min(120, max(-100, 13 - ((int)(__float_as_uint(mx) >> 23) - 127)));
+          const float sc = __uint_as_float((uint32_t)(up + 127) << 23);
+          const float inv = __uint_as_float((uint32_t)(24 - up + 127) << 23);
+#pragma unroll
+          for (int j = 0; j < J; ++j) {
+            const float lo = sc * 0.0625f;   // the codes of odd pairs are 2^4 larger
+            qf[t][2 * j][0] = pack_half(f[j][0] * sc, f[j][1] * sc);
+            qf[t][2 * j][1] = pack_half(f[j][2] * lo, f[j][3] * lo);
+            qf[t][2 * j + 1][0] = pack_half(f[j][4] * sc, f[j][5] * sc);
+            qf[t][2 * j + 1][1] = pack_half(f[j][6] * lo, f[j][7] * lo);
+          }
+          // rows 2 hc and 2 hc + 1 are this lane's head's q and rho
+          fs[t] = __shfl_sync(0xffffffffu, inv, 8 * hc) * a.scale_log2;
+          fa[t] = __shfl_sync(0xffffffffu, inv, 8 * hc + 4);
+#pragma unroll
+          for (int g = 0; g < G; ++g) {
+            qs[t][g] = __shfl_sync(0xffffffffu, gsum[g], 8 * hc) * a.scale_log2;
+            rs[t][g] = __shfl_sync(0xffffffffu, gsum[g], 8 * hc + 4);
+          }
+        }
+      }
+
+      alive = __all_sync(0xffffffffu, mbar_wait_bounded(a.wait_ns, &full[i % S], (i / S) & 1));
+      if (!alive) {
+        // Abandon the run: wait (bounded) for the copies still in flight, and
+        // go on to the merge, so that every counter is taken back to zero.
+        for (int k = i; k < issued; ++k) mbar_wait_drain(&full[k % S], (k / S) & 1);
+        break;
+      }
+      const uint8_t* blk = ring + (i % S) * B::kBytes;
+      const int nvalid = cur.len - cur.local * kQ4Page;   // tokens of this page (>= 1; 64 or more: all)
+
+      // ---- scores and probe values of tokens 16 mt + r and + 8
+      float x[NT][8], av[NT][8];
+#pragma unroll
+      for (int mt = 0; mt < 4; ++mt) {
+        uint32_t w0[J], w1[J];
+        lds_words<J>(blk + (16 * mt + r) * (D / 2) + hc * (D / 8), w0);
+        lds_words<J>(blk + (16 * mt + r + 8) * (D / 2) + hc * (D / 8), w1);
+        float acc[NT][G][4];
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int g = 0; g < G; ++g) acc[t][g][0] = acc[t][g][1] = acc[t][g][2] = acc[t][g][3] = 0.f;
+#pragma unroll
+        for (int j = 0; j < J; ++j)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t u0 = w0[j] >> (8 * h), u1 = w1[j] >> (8 * h);
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+              mma_f16_16816(acc[t][j / 2], u0 & 0x000f000fu, u1 & 0x000f000fu, u0 & 0x00f000f0u, u1 & 0x00f000f0u,
+                            qf[t][2 * j + h][0], qf[t][2 * j + h][1]);
+          }
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          uint32_t kp[G];
+          lds_words<G>(blk + B::kKParams + (16 * mt + r + 8 * half) * (4 * G), kp);
+#pragma unroll
+          for (int t = 0; t < NT; ++t) {
+            float s = 0.f, p = 0.f, sm = 0.f, pmn = 0.f;
+#pragma unroll
+            for (int g = 0; g < G; ++g) {
+              s = fmaf(bf16_lo_f(kp[g]), acc[t][g][2 * half], s);
+              p = fmaf(bf16_lo_f(kp[g]), acc[t][g][2 * half + 1], p);
+              sm = fmaf(bf16_hi_f(kp[g]), qs[t][g], sm);
+              pmn = fmaf(bf16_hi_f(kp[g]), rs[t][g], pmn);
+            }
+            x[t][2 * mt + half] = fmaf(fs[t], s, sm);
+            av[t][2 * mt + half] = fmaf(fa[t], p, pmn);
+          }
+        }
+      }
+      if (seg == 0) {   // the lane with token 0 (always valid) of the head
+#pragma unroll
+        for (int t = 0; t < NT; ++t) st.aref[t] = __shfl_sync(0xffffffffu, av[t][0], hc);
+      }
+
+      // ---- the running reference
+      float mx[NT];
+#pragma unroll
+      for (int t = 0; t < NT; ++t) mx[t] = -INFINITY;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int tok = 16 * (e >> 1) + r + 8 * (e & 1);
+        const bool ok = tok < nvalid;
+        uint32_t vp[G];
+        lds_words<G>(blk + B::kVParams + tok * (4 * G), vp);
+        float smax = 0.f;
+#pragma unroll
+        for (int g = 0; g < G; ++g) smax = fmaxf(smax, fabsf(bf16_lo_f(vp[g])));
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          x[t][e] = ok ? x[t][e] : -INFINITY;
+          av[t][e] = ok ? av[t][e] - st.aref[t] : 0.f;
+          const float big = fminf(fmaxf(smax * fmaxf(1.f, fabsf(av[t][e])), 0x1p-60f), 0x1p60f);
+          mx[t] = fmaxf(mx[t], x[t][e] + lg2(big));
+        }
+      }
+      bool moved = false;
+      float alpha[NT];
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+#pragma unroll
+        for (int off = 4; off < 32; off <<= 1) mx[t] = fmaxf(mx[t], __shfl_xor_sync(0xffffffffu, mx[t], off));
+        const float m_new = fmaxf(st.m[t], mx[t]);
+        alpha[t] = ex2(st.m[t] - m_new);
+        moved = moved || m_new != st.m[t];
+        st.m[t] = m_new;
+      }
+      if (__any_sync(0xffffffffu, moved)) {
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+#pragma unroll
+          for (int k = 0; k < 2 * J; ++k) {
+            st.o[t][k][0] *= alpha[t];
+            st.o[t][k][1] *= alpha[t];
+            st.o[t][k][2] *= alpha[t];
+            st.o[t][k][3] *= alpha[t];
+          }
+#pragma unroll
+          for (int g = 0; g < G; ++g) {
+            st.pm[t][g][0] *= alpha[t];
+            st.pm[t][g][1] *= alpha[t];
+          }
+          st.l[t] *= alpha[t];
+          st.c[t] *= alpha[t];
+        }
+      }
+
+      // ---- weights and value sums, 16 tokens at a time
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk) {
+        uint32_t bh[NT][G][2], bl[NT][G][2];
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          const int e = 2 * kk + half, tok = 16 * kk + r + 8 * half;
+          const bool ok = tok < nvalid;
+          uint32_t vp[G];
+          lds_words<G>(blk + B::kVParams + tok * (4 * G), vp);
+#pragma unroll
+          for (int t = 0; t < NT; ++t) {
+            const float p = ex2(x[t][e] - (st.m[t] - 14.f)), pa = p * av[t][e];
+            st.l[t] += p;
+            st.c[t] += pa;
+#pragma unroll
+            for (int g = 0; g < G; ++g) {
+              const float s = ok ? bf16_lo_f(vp[g]) : 0.f, mn = ok ? bf16_hi_f(vp[g]) : 0.f;
+              st.pm[t][g][0] = fmaf(p, mn, st.pm[t][g][0]);
+              st.pm[t][g][1] = fmaf(pa, mn, st.pm[t][g][1]);
+              const float ps = p * s, pas = pa * s;
+              const uint32_t hi = pack_half(ps, pas);
+              const float2 hf = unpack_half(hi);
+              bh[t][g][half] = transpose_8x8(hi);
+              bl[t][g][half] = transpose_8x8(pack_half(ps - hf.x, pas - hf.y));
+            }
+          }
+        }
+        uint32_t w0[J], w1[J];
+        lds_words<J>(blk + B::kV + (8 * kk + hc) * D + r * (D / 8), w0);
+        lds_words<J>(blk + B::kV + (8 * kk + hc + 4) * D + r * (D / 8), w1);
+#pragma unroll
+        for (int j = 0; j < J; ++j)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t u0 = w0[j] >> (8 * h), u1 = w1[j] >> (8 * h);
+            const uint32_t a0 = u0 & 0x000f000fu, a1 = u0 & 0x00f000f0u, a2 = u1 & 0x000f000fu, a3 = u1 & 0x00f000f0u;
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+              mma_f16_16816(st.o[t][2 * j + h], a0, a1, a2, a3, bh[t][j / 2][0], bh[t][j / 2][1]);
+              mma_f16_16816(st.o[t][2 * j + h], a0, a1, a2, a3, bl[t][j / 2][0], bl[t][j / 2][1]);
+            }
+          }
+      }
+      __syncwarp();   // every lane has read the stage
+      if (issued < n) issue();
+      ++seg;
+
+      if (cur.local + 1 == cur.tiles && (i + 1 < n || seg == cur.tiles)) {
+        // the unit ends here: finish it, or leave the run's first piece
+        st.close();
+        if (seg == cur.tiles) {
+          st.write_out(a, cur.b, cur.hu);
+        } else {
+          st.deposit(first_state);
+          if (lane == 0) {
+            meta[warp * 8 + 0] = cur.b * a.Hkv + cur.hu;
+            meta[warp * 8 + 1] = cur.ua;
+            meta[warp * 8 + 2] = cur.ua + cur.tiles;
+          }
+          first_done = true;
+        }
+        seg = 0;
+      }
+      if (i + 1 < n) cur.next_page(sp);
     }
-    const float val = len == 0 ? 0.f : finalize(O1, O2, L, Cc);
-    const size_t idx = ((size_t)b * a.Hq + hq) * D + d;
-    if (a.out_bf16)
-      reinterpret_cast<__nv_bfloat16*>(a.out)[idx] = __float2bfloat16_rn(val);
-    else
-      reinterpret_cast<float*>(a.out)[idx] = val;
+    if (!alive) {   // leave the pieces that the merge expects, whatever they hold
+      st.reset();
+      cur.seek(sp, y0);
+      if (!first_done && cur.ua < y0 && cur.ua + cur.tiles < y1) {
+        st.deposit(first_state);
+        if (lane == 0) {
+          meta[warp * 8 + 0] = cur.b * a.Hkv + cur.hu;
+          meta[warp * 8 + 1] = cur.ua;
+          meta[warp * 8 + 2] = cur.ua + cur.tiles;
+        }
+      }
+      cur.seek(sp, y1 - 1);
+      seg = cur.ua < y0 || cur.ua + cur.tiles > y1 ? 1 : 0;
+    }
+    if (seg > 0) {   // the run's last piece, into the ring, which holds no copy any more
+      st.close();
+      st.deposit(reinterpret_cast<float*>(ring));
+      if (lane == 0) {
+        meta[warp * 8 + 3] = cur.b * a.Hkv + cur.hu;
+        meta[warp * 8 + 4] = cur.ua;
+        meta[warp * 8 + 5] = cur.ua + cur.tiles;
+      }
+    }
+  }
+  __syncthreads();
+
+  // ---- merge the CTA's pieces, unit by unit (pieces of a unit are neighbours)
+  const long long x0 = sp.start(blockIdx.x), x1 = sp.start(blockIdx.x + 1);
+  const int rows = a.group;
+  auto piece_ptr = [&](int k) {   // piece k: warp k / 2, its first (even) or last one
+    return reinterpret_cast<const float*>((k & 1) ? q4_smem + (k >> 1) * SM::kRing
+                                                  : q4_smem + SM::kStateOff + (k >> 1) * SM::kState);
+  };
+  auto unit_of = [&](int k) { return meta[(k >> 1) * 8 + 3 * (k & 1)]; };
+  for (int k0 = 0; k0 < 2 * kQ4Warps;) {
+    const int unit = unit_of(k0);
+    if (unit < 0) {
+      ++k0;
+      continue;
+    }
+    uint32_t list = 0;   // the pieces of the unit, as a bit set
+    int k1 = k0;
+    for (; k1 < 2 * kQ4Warps; ++k1) {
+      const int u = unit_of(k1);
+      if (u >= 0 && u != unit) break;
+      if (u == unit) list |= 1u << k1;
+    }
+    const int ua = meta[(k0 >> 1) * 8 + 3 * (k0 & 1) + 1], ub = meta[(k0 >> 1) * 8 + 3 * (k0 & 1) + 2];
+    const bool whole = ua >= x0 && ub <= x1;
+    const long long c0 = sp.owner(ua), c1 = sp.owner(ub - 1);
+    const size_t slot_stride = (size_t)rows * SM::kRow;
+    auto slot_of = [&](long long cc) { return a.slots + (2 * cc + (sp.start(cc) >= ua ? 0 : 1)) * slot_stride; };
+    float* mine = whole ? nullptr : slot_of(blockIdx.x);
+    const size_t out_row = ((size_t)(unit / a.Hkv) * a.Hq + (size_t)(unit % a.Hkv) * rows) * D;
+    for (int i = tid; i < rows * D; i += kQ4Threads) {
+      const int h = i / D, d = i % D;
+      const Q4Merged s = merge_pieces<D>(
+          k0, 32, d, [&](int k) { return k < 31 && (list >> (k + 1)) != 0 ? k + __ffs(list >> (k + 1)) : 32; },
+          [&](int k) { return piece_ptr(k) + h * SM::kRow; }, [](const float* p) { return *p; });
+      if (whole) {
+        const float v = finalize(s.O1, s.O2, s.L, s.C);
+        if (a.out_bf16)
+          reinterpret_cast<__nv_bfloat16*>(a.out)[out_row + i] = __float2bfloat16_rn(v);
+        else
+          reinterpret_cast<float*>(a.out)[out_row + i] = v;
+      } else {
+        float* row = mine + h * SM::kRow;
+        row[4 + d] = s.O1;
+        row[4 + D + d] = s.O2;
+        if (d == 0) {
+          row[0] = s.M;
+          row[1] = s.L;
+          row[2] = s.C;
+          row[3] = s.aref;
+        }
+      }
+    }
+    if (!whole) {
+      __threadfence();
+      __syncthreads();
+      if (tid == 0) {
+        const int prev = atomicAdd(a.counters + unit, 1);
+        s_last = prev == (int)(c1 - c0);
+        if (s_last) atomicExch(a.counters + unit, 0);
+      }
+      __syncthreads();
+      const bool last = s_last != 0;
+      __syncthreads();
+      if (last) {
+        __threadfence();
+        for (int i = tid; i < rows * D; i += kQ4Threads) {
+          const int h = i / D, d = i % D;
+          const Q4Merged s = merge_pieces<D>(
+              0, (int)(c1 - c0 + 1), d, [](int k) { return k + 1; },
+              [&](int k) { return slot_of(c0 + k) + h * SM::kRow; }, [](const float* p) { return __ldcg(p); });
+          const float v = finalize(s.O1, s.O2, s.L, s.C);
+          if (a.out_bf16)
+            reinterpret_cast<__nv_bfloat16*>(a.out)[out_row + i] = __float2bfloat16_rn(v);
+          else
+            reinterpret_cast<float*>(a.out)[out_row + i] = v;
+        }
+      }
+    }
+    k0 = k1;
   }
 }
 

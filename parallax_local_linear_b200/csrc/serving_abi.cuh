@@ -178,9 +178,34 @@ plx_status validate_decode_q4(const plx_decode_params* p) {
   return PLX_OK;
 }
 
-size_t decode_q4_workspace(const plx_decode_params* p, int num_sms) {
-  const DecodePlan pl = plan_decode(p, num_sms);
-  return pl.counter_bytes + pl.slot_bytes;
+// A default grid gives every CTA at least this many pages.
+constexpr int kQ4MinPages = 4;
+
+struct DecodeQ4Plan {
+  int ctas;
+  size_t counter_bytes, slot_bytes;
+};
+
+DecodeQ4Plan plan_decode_q4(const plx_decode_params* p, int num_sms) {
+  DecodeQ4Plan pl{};
+  const int64_t units = (int64_t)p->batch * p->num_kv_heads;
+  const int64_t pages = units * ((p->kv_len + kQ4Page - 1) / kQ4Page);
+  const int64_t least = p->num_ctas > 0 ? 1 : kQ4MinPages;
+  int64_t ctas = p->num_ctas > 0 ? p->num_ctas : num_sms;
+  if (ctas > (pages + least - 1) / least) ctas = (pages + least - 1) / least;
+  if (ctas < 1) ctas = 1;
+  pl.ctas = (int)ctas;
+  pl.counter_bytes = ((size_t)units * 4 + 255) & ~size_t(255);
+  pl.slot_bytes = ((size_t)2 * pl.ctas * (p->num_q_heads / p->num_kv_heads) * (2 * p->head_dim + 4) * 4 + 255) &
+                  ~size_t(255);
+  return pl;
+}
+
+template <int D, int NT>
+cudaError_t launch_decode_q4(const DecodeQ4Args& a, int ctas, cudaStream_t stream) {
+  auto kern = decode_q4_kernel<D, NT>;
+  const cudaError_t e = set_smem(kern, Q4Smem<D, NT>::kBytes);
+  return e != cudaSuccess ? e : launch_pdl(kern, dim3(ctas), dim3(kQ4Threads), Q4Smem<D, NT>::kBytes, stream, a);
 }
 
 }  // namespace
@@ -377,7 +402,8 @@ size_t parallax_decode_q4_workspace_size(const plx_decode_params* p, int32_t num
   if (validate_decode_q4(p) != PLX_OK) return (size_t)-1;
   if (num_sms <= 0) num_sms = current_device_sms();
   if (num_sms <= 0) return (size_t)-1;
-  return decode_q4_workspace(p, num_sms);
+  const DecodeQ4Plan pl = plan_decode_q4(p, num_sms);
+  return pl.counter_bytes + pl.slot_bytes;
 }
 
 plx_status parallax_decode_q4(const void* q, const void* rho, const void* kv_cache, const int32_t* page_table,
@@ -393,7 +419,9 @@ plx_status parallax_decode_q4(const void* q, const void* rho, const void* kv_cac
   if ((page_table && !aligned(page_table, 4)) || (seq_lens && !aligned(seq_lens, 4))) return PLX_ERR_INVALID_ARG;
   const int num_sms = current_device_sms();
   if (num_sms <= 0) return PLX_ERR_CUDA;
-  if (workspace == nullptr || !aligned(workspace, 256) || workspace_bytes < decode_q4_workspace(p, num_sms))
+  const DecodeQ4Plan pl = plan_decode_q4(p, num_sms);
+  if (workspace == nullptr || !aligned(workspace, 256) || workspace_bytes % 256 != 0 ||
+      workspace_bytes < pl.counter_bytes + pl.slot_bytes)
     return PLX_ERR_WORKSPACE;
   if (p->kv_len == 0) {   // every sequence is empty: the output is zero
     const size_t n = (size_t)p->batch * p->num_q_heads * p->head_dim * (p->out_dtype == PLX_BF16 ? 2 : 4);
@@ -411,14 +439,19 @@ plx_status parallax_decode_q4(const void* q, const void* rho, const void* kv_cac
   a.Hkv = p->num_kv_heads;
   a.group = p->num_q_heads / p->num_kv_heads;
   a.kv_len = p->kv_len;
-  a.paged = paged ? 1 : 0;
   a.num_pages = paged ? p->num_pages : 0;
   a.max_pages = paged ? p->max_pages_per_seq : 0;
   a.scale_log2 = p->scale * 1.4426950408889634f;
   a.out_bf16 = p->out_dtype == PLX_BF16 ? 1 : 0;
-  const dim3 grid(a.B * a.Hq), block(kQ4Warps * 32);
-  const cudaError_t e = p->head_dim == 64 ? launch_pdl(decode_q4_kernel<64>, grid, block, 0, stream, a)
-                                          : launch_pdl(decode_q4_kernel<128>, grid, block, 0, stream, a);
+  a.slots = static_cast<float*>(workspace);
+  a.counters = reinterpret_cast<int32_t*>(static_cast<uint8_t*>(workspace) + workspace_bytes - pl.counter_bytes);
+  a.min_pages = p->num_ctas > 0 ? 1 : kQ4MinPages;
+  a.wait_ns = current_wait_ns();
+  const bool one = a.group <= 4;   // four heads fill the 8 columns of a product
+  const cudaError_t e = p->head_dim == 64 ? (one ? launch_decode_q4<64, 1>(a, pl.ctas, stream)
+                                                 : launch_decode_q4<64, 2>(a, pl.ctas, stream))
+                                          : (one ? launch_decode_q4<128, 1>(a, pl.ctas, stream)
+                                                 : launch_decode_q4<128, 2>(a, pl.ctas, stream));
   return e == cudaSuccess ? PLX_OK : PLX_ERR_CUDA;
 }
 
