@@ -27,8 +27,9 @@
 // Ranges.  q and rho are scaled by a power of two to at most 2^14 per row
 // (exact: they are bf16).  e s and e a s have to fit fp16, whatever the size of
 // s and a: the running reference is not the largest score alone but
-//     M = max_i (x_i + log2(max_g s_ig max(1, |a_i|))),      p_i = 2^(x_i - M + 14)
-// with x_i the score in powers of two, so every product is at most 2^14.  Each
+//     M = max_i x_i + log2(max_i,g s_ig max(1, |a_i|)),      p_i = 2^(x_i - M + 14)
+// with x_i the score in powers of two (maxima of a page; M never falls), so
+// every product is at most 2^14.  Each
 // enters as hi + lo halves (22 bits, and nothing above 2^-38 of the largest is
 // lost), since a rounding to fp16 alone would show in rows of a few keys.
 // a_i is taken relative to the probe value of the first token the warp sees of
@@ -37,8 +38,10 @@
 //
 // Work.  The pages of every (sequence, KV head) unit are laid end to end and
 // cut into equal runs, one per warp: no warp waits for another until its run
-// is done.  A warp keeps its own ring of bulk copies (one page and head is one
-// contiguous block) and refills a stage as it leaves it.  Units that lie
+// is done.  A warp keeps its own ring of asynchronous copies (one page and head
+// is one contiguous block) and refills a slot as it leaves it; copies by all
+// lanes cost it 9 issue slots a slot, where a bulk copy from one lane held it up
+// for about 450 cycles.  Units that lie
 // inside a run are finished in registers; pieces of cut units are merged in
 // the CTA after one barrier, and across CTAs in the workspace, by the last CTA
 // that finishes a piece (decode.cuh's rule and counters).
@@ -50,9 +53,6 @@
 #include "decode.cuh"
 
 namespace plx {
-
-constexpr int kQ4Warps = 8;
-constexpr int kQ4Threads = kQ4Warps * 32;
 
 struct DecodeQ4Args {
   const __nv_bfloat16* q;
@@ -67,27 +67,33 @@ struct DecodeQ4Args {
   float scale_log2;
   int out_bf16;
   int min_pages;                   // a CTA takes at least this many pages
-  unsigned long long wait_ns;
 };
 
+// Warps of a CTA (one CTA per SM) and its shared memory.  A ring slot holds
+// one half of a block, K's or V's codes and parameters.
 template <int D, int NT>
 struct Q4Smem {
-  static constexpr int kStages = D == 64 ? 4 : 2;                  // per warp
-  static constexpr int kRing = kStages * Q4Block<D>::kBytes;       // per warp
+  static constexpr int kWarps = NT == 1 ? 12 : 8;                  // 168 and 255 registers a thread
+  static constexpr int kThreads = 32 * kWarps;
+  static constexpr int kCodes = kQ4Page * D / 2;
+  static constexpr int kPart = kCodes + Q4Block<D>::kParamBytes;
+  static constexpr int kSlots = (NT == 1 ? 3 : 4) * (128 / D);     // per warp
+  static constexpr int kRing = kSlots * kPart;                     // per warp
   static constexpr int kRow = 2 * D + 4;                           // a head's state: m l c aref O1 O2
   static constexpr int kState = 4 * NT * kRow * 4;                 // bytes of a piece
-  static constexpr int kStateOff = kQ4Warps * kRing;
-  static constexpr int kBarOff = kStateOff + kQ4Warps * kState;
-  static constexpr int kMetaOff = kBarOff + kQ4Warps * kStages * 8;
-  static constexpr int kPreOff = kMetaOff + kQ4Warps * 8 * 4;
-  static constexpr int kBytes = kPreOff + (kQ4Threads + 4) * 4 + 64;
+  static constexpr int kStateOff = kWarps * kRing;
+  static constexpr int kMetaOff = kStateOff + kWarps * kState;
+  static constexpr int kPreOff = kMetaOff + kWarps * 8 * 4;
+  static constexpr int kBytes = kPreOff + (kThreads + 4) * 4;
   static_assert(kState <= kRing, "a warp's last piece fits in its ring");
+  static_assert(2 * kWarps <= 31, "the pieces of a CTA are a bit set");
+  static_assert(kMaxBatch <= 32 * kThreads, "a lane for every sequence of a share");
 };
 
 // D += A * B, m16n8k16, fp16 inputs, fp32 accumulate.
 __device__ __forceinline__ void mma_f16_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                               uint32_t b0, uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
       "{%0, %1, %2, %3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
@@ -97,7 +103,7 @@ __device__ __forceinline__ void mma_f16_16816(float (&d)[4], uint32_t a0, uint32
 // The transpose of the 8 x 8 matrix of halves that the warp holds two to a lane.
 __device__ __forceinline__ uint32_t transpose_8x8(uint32_t v) {
   uint32_t r;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
   return r;
 }
 
@@ -107,6 +113,16 @@ __device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
 }
 __device__ __forceinline__ float2 unpack_half(uint32_t v) {
   return __half22float2(*reinterpret_cast<const __half2*>(&v));
+}
+
+// 16 bytes from global to shared memory, not through L1.
+__device__ __forceinline__ void q4_copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(reinterpret_cast<uint64_t>(src)) : "memory");
+}
+__device__ __forceinline__ void q4_copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void q4_copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 __device__ __forceinline__ float lg2(float x) {
@@ -136,11 +152,11 @@ __device__ __forceinline__ void lds_words(const uint8_t* p, uint32_t (&w)[N]) {
 
 // ---------------------------------------------------------------- the page space
 // pre[i]: pages (of all heads) of the sequences before thread i's share of
-// `per` sequences; pre[kQ4Threads] = T.
+// `per` sequences.
 struct Q4Space {
   const DecodeQ4Args& a;
   const int* pre;
-  int per;
+  int shares, per;
   long long T, G;
 
   __device__ __forceinline__ int len(int b) const {
@@ -166,7 +182,7 @@ struct Q4Cursor {
       b = x / per_seq;
       base = b * per_seq;
     } else {
-      int lo = 0, hi = kQ4Threads - 1;   // last share with pre <= x that is not empty
+      int lo = 0, hi = s.shares - 1;   // last share with pre <= x that is not empty
       while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
         if (s.pre[mid] <= x) lo = mid; else hi = mid - 1;
@@ -331,30 +347,23 @@ __device__ __forceinline__ Q4Merged merge_pieces(int first, int end, int d, Next
 }
 
 template <int D, int NT>
-__global__ void __launch_bounds__(kQ4Threads, 1) decode_q4_kernel(const DecodeQ4Args a) {
+__global__ void __launch_bounds__(Q4Smem<D, NT>::kThreads, 1) decode_q4_kernel(const DecodeQ4Args a) {
   using SM = Q4Smem<D, NT>;
   using B = Q4Block<D>;
-  constexpr int S = SM::kStages, G = D / 64, J = D / 32;
+  constexpr int S = SM::kSlots, G = D / 64, J = D / 32, kWarps = SM::kWarps, kThreads = SM::kThreads;
   extern __shared__ __align__(128) uint8_t q4_smem[];
-  uint64_t* bars = reinterpret_cast<uint64_t*>(q4_smem + SM::kBarOff);
   int* meta = reinterpret_cast<int*>(q4_smem + SM::kMetaOff);   // [warp]: first piece's unit, ua, ub; last piece's
   int* pre = reinterpret_cast<int*>(q4_smem + SM::kPreOff);
   __shared__ int s_last;
-  __shared__ int s_part[kQ4Warps];
+  __shared__ int s_part[kWarps];
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int r = lane >> 2, hc = lane & 3;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  uint64_t* full = bars + warp * S;
-  if (lane == 0) {
-#pragma unroll
-    for (int s = 0; s < S; ++s) mbar_init(&full[s], 1);
-    fence_mbarrier_init();
-  }
   asm volatile("griddepcontrol.wait;" ::: "memory");
 
   // ---- the page space
-  Q4Space sp{a, pre, (a.B + kQ4Threads - 1) / kQ4Threads, 0, 1};
+  Q4Space sp{a, pre, kThreads, (a.B + kThreads - 1) / kThreads, 0, 1};
   if (a.seq_lens == nullptr) {
     sp.T = (long long)a.B * a.Hkv * ((a.kv_len + kQ4Page - 1) / kQ4Page);
   } else {
@@ -375,7 +384,7 @@ __global__ void __launch_bounds__(kQ4Threads, 1) decode_q4_kernel(const DecodeQ4
     __syncthreads();
     int base = 0, total = 0;
 #pragma unroll
-    for (int w = 0; w < kQ4Warps; ++w) {
+    for (int w = 0; w < kWarps; ++w) {
       if (w == warp) base = total;
       total += s_part[w];
     }
@@ -384,14 +393,14 @@ __global__ void __launch_bounds__(kQ4Threads, 1) decode_q4_kernel(const DecodeQ4
     // sequences without tokens have no pages: their rows are zero
     for (int b = blockIdx.x; b < a.B; b += gridDim.x)
       if (sp.len(b) == 0)
-        for (int i = tid; i < a.Hq * D / 4; i += kQ4Threads) store_out4(a, (size_t)b * a.Hq * D + 4 * i, 0.f, 0.f, 0.f, 0.f);
+        for (int i = tid; i < a.Hq * D / 4; i += kThreads) store_out4(a, (size_t)b * a.Hq * D + 4 * i, 0.f, 0.f, 0.f, 0.f);
   }
   __syncthreads();
   const long long most = (sp.T + a.min_pages - 1) / a.min_pages;
   sp.G = most < (long long)gridDim.x ? most : (long long)gridDim.x;
   if ((long long)blockIdx.x >= sp.G) return;
 
-  const long long W = sp.G * kQ4Warps, gw = (long long)blockIdx.x * kQ4Warps + warp;
+  const long long W = sp.G * kWarps, gw = (long long)blockIdx.x * kWarps + warp;
   const int y0 = (int)(gw * sp.T / W), y1 = (int)((gw + 1) * sp.T / W), n = y1 - y0;
   uint8_t* ring = q4_smem + warp * SM::kRing;
   float* first_state = reinterpret_cast<float*>(q4_smem + SM::kStateOff + warp * SM::kState);
@@ -402,30 +411,60 @@ __global__ void __launch_bounds__(kQ4Threads, 1) decode_q4_kernel(const DecodeQ4
     Q4Cursor cur, ahead;
     cur.seek(sp, y0);
     ahead = cur;
+    // Part 2 i is the keys of the run's page i, part 2 i + 1 its values; part k
+    // goes to slot k % S.  A page's entry in the page table is read when the
+    // part before it is issued and looked at when its own keys are.  Every
+    // part is one group of 16-byte asynchronous copies, 512 bytes a step of
+    // the warp (past the run's end the groups are empty), so that part k has
+    // landed once at most S - 1 groups are on their way.
     int issued = 0, entry = ahead.entry(sp);
-    // The next block into stage issued % S.  The entry of the one after it is
-    // read now and looked at when that one is issued, a page later.
+    const uint8_t* src = nullptr;
+    const uint32_t ring_lane = smem_u32(ring) + 16 * lane;
+    uint32_t fill = ring_lane;        // where the next part goes
     auto issue = [&] {
-      const size_t blk = ahead.block(sp, entry);
-      if (lane == 0) {
-        uint64_t* bar = &full[issued % S];
-        mbar_arrive_expect_tx(bar, B::kBytes);
-        bulk_load(ring + (issued % S) * B::kBytes, a.cache + blk * B::kBytes, B::kBytes, bar);
+      if (issued < 2 * n) {
+        const bool values = issued & 1;
+        if (!values) src = a.cache + ahead.block(sp, entry) * B::kBytes + 16 * lane;
+        const uint8_t* codes = src + (values ? B::kV : 0);
+        const uint8_t* params = src + (values ? B::kVParams : B::kKParams);
+#pragma unroll
+        for (int c = 0; c < SM::kCodes; c += 512) q4_copy16(fill + c, codes + c);
+        if (B::kParamBytes == 512 || lane < B::kParamBytes / 16) q4_copy16(fill + SM::kCodes, params);
+        ++issued;
+        fill = fill == ring_lane + (S - 1) * SM::kPart ? ring_lane : fill + SM::kPart;
+        if (values && issued < 2 * n) {
+          ahead.next_page(sp);
+          entry = ahead.entry(sp);
+        }
       }
-      ++issued;
-      if (issued < n) {
-        ahead.next_page(sp);
-        entry = ahead.entry(sp);
-      }
+      q4_copy_commit();
     };
-    for (int i = 0; i < S && i < n; ++i) issue();
+#pragma unroll 1
+    for (int k = 0; k < S; ++k) issue();
 
     Q4WarpState<D, NT> st;
     uint32_t qf[NT][D / 16][2];     // [q rho ..] operand
     float fs[NT], fa[NT];           // factors of a score (in powers of two) and of a probe value
     float qs[NT][G], rs[NT][G];     // group sums of q (times the scale) and rho
-    bool alive = true, first_done = false;
     int seg = 0;                    // pages of the current unit done by this warp
+    uint8_t* slot = ring;
+    auto landed = [&] {             // the slot's part is there, for every lane
+      q4_copy_wait<S - 1>();
+      __syncwarp();
+    };
+    auto leave = [&] {              // done with the slot: refill it, go to the next one
+      __syncwarp();
+      issue();
+      slot = slot == ring + (S - 1) * SM::kPart ? ring : slot + SM::kPart;
+    };
+    // Parameters of tokens past the sequence's end become zero (they may be
+    // NaN).
+    auto clear_tail = [&](int nvalid) {
+      for (int tok = nvalid + lane; tok < kQ4Page; tok += 32)
+#pragma unroll
+        for (int g = 0; g < G; ++g) reinterpret_cast<uint32_t*>(slot + SM::kCodes)[tok * G + g] = 0;
+      __syncwarp();
+    };
 
     for (int i = 0; i < n; ++i) {
       if (seg == 0) {
@@ -484,23 +523,17 @@ __global__ void __launch_bounds__(kQ4Threads, 1) decode_q4_kernel(const DecodeQ4
         }
       }
 
-      alive = __all_sync(0xffffffffu, mbar_wait_bounded(a.wait_ns, &full[i % S], (i / S) & 1));
-      if (!alive) {
-        // Abandon the run: wait (bounded) for the copies still in flight, and
-        // go on to the merge, so that every counter is taken back to zero.
-        for (int k = i; k < issued; ++k) mbar_wait_drain(&full[k % S], (k / S) & 1);
-        break;
-      }
-      const uint8_t* blk = ring + (i % S) * B::kBytes;
+      landed();
       const int nvalid = cur.len - cur.local * kQ4Page;   // tokens of this page (>= 1; 64 or more: all)
+      if (nvalid < kQ4Page) clear_tail(nvalid);
 
       // ---- scores and probe values of tokens 16 mt + r and + 8
       float x[NT][8], av[NT][8];
 #pragma unroll
       for (int mt = 0; mt < 4; ++mt) {
         uint32_t w0[J], w1[J];
-        lds_words<J>(blk + (16 * mt + r) * (D / 2) + hc * (D / 8), w0);
-        lds_words<J>(blk + (16 * mt + r + 8) * (D / 2) + hc * (D / 8), w1);
+        lds_words<J>(slot + (16 * mt + r) * (D / 2) + hc * (D / 8), w0);
+        lds_words<J>(slot + (16 * mt + r + 8) * (D / 2) + hc * (D / 8), w1);
         float acc[NT][G][4];
 #pragma unroll
         for (int t = 0; t < NT; ++t)
@@ -519,7 +552,7 @@ __global__ void __launch_bounds__(kQ4Threads, 1) decode_q4_kernel(const DecodeQ4
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
           uint32_t kp[G];
-          lds_words<G>(blk + B::kKParams + (16 * mt + r + 8 * half) * (4 * G), kp);
+          lds_words<G>(slot + SM::kCodes + (16 * mt + r + 8 * half) * (4 * G), kp);
 #pragma unroll
           for (int t = 0; t < NT; ++t) {
             float s = 0.f, p = 0.f, sm = 0.f, pmn = 0.f;
@@ -535,30 +568,42 @@ __global__ void __launch_bounds__(kQ4Threads, 1) decode_q4_kernel(const DecodeQ4
           }
         }
       }
+      leave();
       if (seg == 0) {   // the lane with token 0 (always valid) of the head
 #pragma unroll
         for (int t = 0; t < NT; ++t) st.aref[t] = __shfl_sync(0xffffffffu, av[t][0], hc);
       }
-
-      // ---- the running reference
-      float mx[NT];
+      if (nvalid < kQ4Page) {
 #pragma unroll
-      for (int t = 0; t < NT; ++t) mx[t] = -INFINITY;
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if (16 * (e >> 1) + r + 8 * (e & 1) >= nvalid) x[t][e] = -INFINITY;
+      }
+
+      landed();
+      if (nvalid < kQ4Page) clear_tail(nvalid);
+
+      // ---- the running reference: the page's largest score and its largest
+      // scale times probe value
+      float mx[NT], big[NT];
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        mx[t] = -INFINITY;
+        big[t] = 0.f;
+      }
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const int tok = 16 * (e >> 1) + r + 8 * (e & 1);
-        const bool ok = tok < nvalid;
         uint32_t vp[G];
-        lds_words<G>(blk + B::kVParams + tok * (4 * G), vp);
+        lds_words<G>(slot + SM::kCodes + (16 * (e >> 1) + r + 8 * (e & 1)) * (4 * G), vp);
         float smax = 0.f;
 #pragma unroll
         for (int g = 0; g < G; ++g) smax = fmaxf(smax, fabsf(bf16_lo_f(vp[g])));
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
-          x[t][e] = ok ? x[t][e] : -INFINITY;
-          av[t][e] = ok ? av[t][e] - st.aref[t] : 0.f;
-          const float big = fminf(fmaxf(smax * fmaxf(1.f, fabsf(av[t][e])), 0x1p-60f), 0x1p60f);
-          mx[t] = fmaxf(mx[t], x[t][e] + lg2(big));
+          av[t][e] -= st.aref[t];
+          big[t] = fmaxf(big[t], smax * fmaxf(1.f, fabsf(av[t][e])));
+          mx[t] = fmaxf(mx[t], x[t][e]);
         }
       }
       bool moved = false;
@@ -566,8 +611,11 @@ __global__ void __launch_bounds__(kQ4Threads, 1) decode_q4_kernel(const DecodeQ4
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
 #pragma unroll
-        for (int off = 4; off < 32; off <<= 1) mx[t] = fmaxf(mx[t], __shfl_xor_sync(0xffffffffu, mx[t], off));
-        const float m_new = fmaxf(st.m[t], mx[t]);
+        for (int off = 4; off < 32; off <<= 1) {
+          mx[t] = fmaxf(mx[t], __shfl_xor_sync(0xffffffffu, mx[t], off));
+          big[t] = fmaxf(big[t], __shfl_xor_sync(0xffffffffu, big[t], off));
+        }
+        const float m_new = fmaxf(st.m[t], mx[t] + lg2(fminf(fmaxf(big[t], 0x1p-60f), 0x1p60f)));
         alpha[t] = ex2(st.m[t] - m_new);
         moved = moved || m_new != st.m[t];
         st.m[t] = m_new;
@@ -598,10 +646,9 @@ __global__ void __launch_bounds__(kQ4Threads, 1) decode_q4_kernel(const DecodeQ4
         uint32_t bh[NT][G][2], bl[NT][G][2];
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
-          const int e = 2 * kk + half, tok = 16 * kk + r + 8 * half;
-          const bool ok = tok < nvalid;
+          const int e = 2 * kk + half;
           uint32_t vp[G];
-          lds_words<G>(blk + B::kVParams + tok * (4 * G), vp);
+          lds_words<G>(slot + SM::kCodes + (16 * kk + r + 8 * half) * (4 * G), vp);
 #pragma unroll
           for (int t = 0; t < NT; ++t) {
             const float p = ex2(x[t][e] - (st.m[t] - 14.f)), pa = p * av[t][e];
@@ -609,7 +656,7 @@ __global__ void __launch_bounds__(kQ4Threads, 1) decode_q4_kernel(const DecodeQ4
             st.c[t] += pa;
 #pragma unroll
             for (int g = 0; g < G; ++g) {
-              const float s = ok ? bf16_lo_f(vp[g]) : 0.f, mn = ok ? bf16_hi_f(vp[g]) : 0.f;
+              const float s = bf16_lo_f(vp[g]), mn = bf16_hi_f(vp[g]);
               st.pm[t][g][0] = fmaf(p, mn, st.pm[t][g][0]);
               st.pm[t][g][1] = fmaf(pa, mn, st.pm[t][g][1]);
               const float ps = p * s, pas = pa * s;
@@ -621,23 +668,31 @@ __global__ void __launch_bounds__(kQ4Threads, 1) decode_q4_kernel(const DecodeQ4
           }
         }
         uint32_t w0[J], w1[J];
-        lds_words<J>(blk + B::kV + (8 * kk + hc) * D + r * (D / 8), w0);
-        lds_words<J>(blk + B::kV + (8 * kk + hc + 4) * D + r * (D / 8), w1);
+        lds_words<J>(slot + (8 * kk + hc) * D + r * (D / 8), w0);
+        lds_words<J>(slot + (8 * kk + hc + 4) * D + r * (D / 8), w1);
 #pragma unroll
-        for (int j = 0; j < J; ++j)
+        for (int j = 0; j < J; j += 2) {   // the two words of a group: four products, then their low halves
+          uint32_t av4[4][4];
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const uint32_t u0 = w0[j] >> (8 * h), u1 = w1[j] >> (8 * h);
-            const uint32_t a0 = u0 & 0x000f000fu, a1 = u0 & 0x00f000f0u, a2 = u1 & 0x000f000fu, a3 = u1 & 0x00f000f0u;
-#pragma unroll
-            for (int t = 0; t < NT; ++t) {
-              mma_f16_16816(st.o[t][2 * j + h], a0, a1, a2, a3, bh[t][j / 2][0], bh[t][j / 2][1]);
-              mma_f16_16816(st.o[t][2 * j + h], a0, a1, a2, a3, bl[t][j / 2][0], bl[t][j / 2][1]);
-            }
+          for (int q = 0; q < 4; ++q) {
+            const uint32_t u0 = w0[j + q / 2] >> (8 * (q & 1)), u1 = w1[j + q / 2] >> (8 * (q & 1));
+            av4[q][0] = u0 & 0x000f000fu;
+            av4[q][1] = u0 & 0x00f000f0u;
+            av4[q][2] = u1 & 0x000f000fu;
+            av4[q][3] = u1 & 0x00f000f0u;
           }
+#pragma unroll
+          for (int t = 0; t < NT; ++t) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              mma_f16_16816(st.o[t][2 * j + q], av4[q][0], av4[q][1], av4[q][2], av4[q][3], bh[t][j / 2][0], bh[t][j / 2][1]);
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              mma_f16_16816(st.o[t][2 * j + q], av4[q][0], av4[q][1], av4[q][2], av4[q][3], bl[t][j / 2][0], bl[t][j / 2][1]);
+          }
+        }
       }
-      __syncwarp();   // every lane has read the stage
-      if (issued < n) issue();
+      leave();
       ++seg;
 
       if (cur.local + 1 == cur.tiles && (i + 1 < n || seg == cur.tiles)) {
@@ -652,25 +707,10 @@ __global__ void __launch_bounds__(kQ4Threads, 1) decode_q4_kernel(const DecodeQ4
             meta[warp * 8 + 1] = cur.ua;
             meta[warp * 8 + 2] = cur.ua + cur.tiles;
           }
-          first_done = true;
         }
         seg = 0;
       }
       if (i + 1 < n) cur.next_page(sp);
-    }
-    if (!alive) {   // leave the pieces that the merge expects, whatever they hold
-      st.reset();
-      cur.seek(sp, y0);
-      if (!first_done && cur.ua < y0 && cur.ua + cur.tiles < y1) {
-        st.deposit(first_state);
-        if (lane == 0) {
-          meta[warp * 8 + 0] = cur.b * a.Hkv + cur.hu;
-          meta[warp * 8 + 1] = cur.ua;
-          meta[warp * 8 + 2] = cur.ua + cur.tiles;
-        }
-      }
-      cur.seek(sp, y1 - 1);
-      seg = cur.ua < y0 || cur.ua + cur.tiles > y1 ? 1 : 0;
     }
     if (seg > 0) {   // the run's last piece, into the ring, which holds no copy any more
       st.close();
@@ -692,7 +732,7 @@ __global__ void __launch_bounds__(kQ4Threads, 1) decode_q4_kernel(const DecodeQ4
                                                   : q4_smem + SM::kStateOff + (k >> 1) * SM::kState);
   };
   auto unit_of = [&](int k) { return meta[(k >> 1) * 8 + 3 * (k & 1)]; };
-  for (int k0 = 0; k0 < 2 * kQ4Warps;) {
+  for (int k0 = 0; k0 < 2 * kWarps;) {
     const int unit = unit_of(k0);
     if (unit < 0) {
       ++k0;
@@ -700,7 +740,7 @@ __global__ void __launch_bounds__(kQ4Threads, 1) decode_q4_kernel(const DecodeQ4
     }
     uint32_t list = 0;   // the pieces of the unit, as a bit set
     int k1 = k0;
-    for (; k1 < 2 * kQ4Warps; ++k1) {
+    for (; k1 < 2 * kWarps; ++k1) {
       const int u = unit_of(k1);
       if (u >= 0 && u != unit) break;
       if (u == unit) list |= 1u << k1;
@@ -712,7 +752,7 @@ __global__ void __launch_bounds__(kQ4Threads, 1) decode_q4_kernel(const DecodeQ4
     auto slot_of = [&](long long cc) { return a.slots + (2 * cc + (sp.start(cc) >= ua ? 0 : 1)) * slot_stride; };
     float* mine = whole ? nullptr : slot_of(blockIdx.x);
     const size_t out_row = ((size_t)(unit / a.Hkv) * a.Hq + (size_t)(unit % a.Hkv) * rows) * D;
-    for (int i = tid; i < rows * D; i += kQ4Threads) {
+    for (int i = tid; i < rows * D; i += kThreads) {
       const int h = i / D, d = i % D;
       const Q4Merged s = merge_pieces<D>(
           k0, 32, d, [&](int k) { return k < 31 && (list >> (k + 1)) != 0 ? k + __ffs(list >> (k + 1)) : 32; },
@@ -748,7 +788,7 @@ __global__ void __launch_bounds__(kQ4Threads, 1) decode_q4_kernel(const DecodeQ4
       __syncthreads();
       if (last) {
         __threadfence();
-        for (int i = tid; i < rows * D; i += kQ4Threads) {
+        for (int i = tid; i < rows * D; i += kThreads) {
           const int h = i / D, d = i % D;
           const Q4Merged s = merge_pieces<D>(
               0, (int)(c1 - c0 + 1), d, [](int k) { return k + 1; },

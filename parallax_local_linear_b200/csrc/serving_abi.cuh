@@ -205,7 +205,8 @@ template <int D, int NT>
 cudaError_t launch_decode_q4(const DecodeQ4Args& a, int ctas, cudaStream_t stream) {
   auto kern = decode_q4_kernel<D, NT>;
   const cudaError_t e = set_smem(kern, Q4Smem<D, NT>::kBytes);
-  return e != cudaSuccess ? e : launch_pdl(kern, dim3(ctas), dim3(kQ4Threads), Q4Smem<D, NT>::kBytes, stream, a);
+  return e != cudaSuccess ? e : launch_pdl(kern, dim3(ctas), dim3(Q4Smem<D, NT>::kThreads),
+                                               Q4Smem<D, NT>::kBytes, stream, a);
 }
 
 }  // namespace
@@ -446,7 +447,6 @@ plx_status parallax_decode_q4(const void* q, const void* rho, const void* kv_cac
   a.slots = static_cast<float*>(workspace);
   a.counters = reinterpret_cast<int32_t*>(static_cast<uint8_t*>(workspace) + workspace_bytes - pl.counter_bytes);
   a.min_pages = p->num_ctas > 0 ? 1 : kQ4MinPages;
-  a.wait_ns = current_wait_ns();
   const bool one = a.group <= 4;   // four heads fill the 8 columns of a product
   const cudaError_t e = p->head_dim == 64 ? (one ? launch_decode_q4<64, 1>(a, pl.ctas, stream)
                                                  : launch_decode_q4<64, 2>(a, pl.ctas, stream))
