@@ -9,12 +9,13 @@ more: off by at most ds_i = scale (d + 16) 2u sum |q_c| (s n + |m|)_c (2u,
 since the tensor cores may truncate), and a probe value by da_i = (d + 16) 2u
 sum |rho_c| (s n + |m|)_c.  A weight is then off by at most 2 max ds of
 itself, plus 2^-21 for the exponential and the 22 bits in which e and e a
-enter the value product, plus (n + 64) 2u for the sums over n keys.  With
+enter the value product (fp16's half step, 2^-11, from 128 keys on), plus
+(n + 64) 2u for the sums over n keys.  With
 out = sum_i w_i (1 + abar - a_i) v_i, formed from two sums of size
 sum w_i (1 + |a_i - a_ref|) |v_i| each at a common offset a_ref of the
 probes, the error is at most
     sum_i w_i (1 + |abar| + |a_i| + 2 A) |V_i| e  +  sum_i w_i (da_i + sum_j w_j da_j) |V_i|
-with e = 4 max ds + 2^-20 + (n + 64) 4u, |V_i| = (s n + |m|) of the value and
+with e = 4 max ds + 2^-20 (or 2^-11) + (n + 64) 4u, |V_i| = (s n + |m|) of the value and
 A = max |a_i| >= |a_ref|.  The output's own rounding (half a step) is added.
 """
 
@@ -112,7 +113,7 @@ def _reference(x, scale):
                 a = k @ rho[b, h]
                 ds = abs(scale) * (d + 16) * 2 * U * (ka @ np.abs(q[b, h])).max()
                 da = (d + 16) * 2 * U * (ka @ np.abs(rho[b, h]))
-                e = 4 * ds + 2.0 ** -20 + (n + 64) * 4 * U
+                e = 4 * ds + (2.0 ** -20 if n < 128 else 2.0 ** -11) + (n + 64) * 4 * U
                 coef = w * (1 + abs(w @ a) + np.abs(a) + 2 * np.abs(a).max()) * e + w * (da + w @ da)
                 bound[b, h] = coef @ va
     return out, bound
