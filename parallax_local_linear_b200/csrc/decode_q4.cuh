@@ -47,8 +47,10 @@
 // for about 450 cycles.  Units that lie
 // inside a run are finished in registers; pieces of cut units are merged in
 // the CTA after one barrier, and across CTAs in the workspace, by the last CTA
-// that finishes a piece (decode.cuh's rule and counters).
+// that finishes a piece (a counter per unit, which that CTA takes back to zero).
 #pragma once
+
+#include <type_traits>
 
 #include <cuda_fp16.h>
 
@@ -92,7 +94,7 @@ struct Q4Smem {
   static constexpr int kPreOff = kMetaOff + kWarps * 8 * 4;
   static constexpr int kBytes = kPreOff + (kThreads + 4) * 4;
   static_assert(kState <= kRing, "a warp's last piece fits in its ring");
-  static_assert(2 * kWarps <= 31, "the pieces of a CTA are a bit set");
+  static_assert(2 * kWarps <= 32 && kWarps % 4 == 0, "a lane for every piece of a CTA");
   static_assert(kMaxBatch <= 32 * kThreads, "a lane for every sequence of a share");
 };
 
@@ -169,15 +171,20 @@ struct Q4Space {
   const DecodeQ4Args& a;
   const int* pre;
   int shares, per;
-  long long T, G;
+  uint32_t T, G, W;      // pages, CTAs with work, warps of those
+  uint32_t quot, rem;    // T / W, T % W
 
   __device__ __forceinline__ int len(int b) const {
     if (a.seq_lens == nullptr) return a.kv_len;
     return min(max(__ldg(a.seq_lens + b), 0), a.kv_len);
   }
   __device__ __forceinline__ int pages(int b) const { return (len(b) + kQ4Page - 1) / kQ4Page; }
-  __device__ __forceinline__ long long start(long long c) const { return c * T / G; }
-  __device__ __forceinline__ long long owner(long long x) const { return ((x + 1) * G + T - 1) / T - 1; }
+  // First page of warp w's run, floor(w T / W): W < 2^16, so 32 bits are enough.
+  __device__ __forceinline__ uint32_t start(uint32_t w) const { return w * quot + w * rem / W; }
+  // The CTA whose runs hold page x.
+  __device__ __forceinline__ uint32_t owner(uint32_t x) const {
+    return (uint32_t)(((uint64_t)(x + 1) * G - 1) / T);
+  }
 };
 
 // A place in the page space: page `local` of unit (b, hu), which starts at page
@@ -334,29 +341,102 @@ struct Q4WarpState {
   }
 };
 
-// The sum of pieces of one unit for one head and column.
-struct Q4Merged {
-  float M, L, C, aref, O1, O2;
-};
-// `first`, `next(i)` walk the pieces' numbers, up to `end`; `piece(i)` points
-// to piece i's row of the head.
-template <int D, typename Next, typename Piece, typename Load>
-__device__ __forceinline__ Q4Merged merge_pieces(int first, int end, int d, Next next, Piece piece, Load load) {
-  Q4Merged s;
-  s.M = -INFINITY;
-  for (int i = first; i < end; i = next(i)) s.M = fmaxf(s.M, load(piece(i)));
-  s.L = s.C = s.O1 = s.O2 = 0.f;
-  s.aref = load(piece(first) + 3);
-  for (int i = first; i < end; i = next(i)) {
-    const float* p = piece(i);
-    const float al = ex2(load(p) - s.M), l = load(p + 1), shift = load(p + 3) - s.aref, o1 = load(p + 4 + d);
-    s.L = fmaf(al, l, s.L);
-    s.C = fmaf(al, fmaf(shift, l, load(p + 2)), s.C);
-    s.O1 = fmaf(al, o1, s.O1);
-    s.O2 = fmaf(al, fmaf(shift, o1, load(p + 4 + D + d)), s.O2);
+// Adds a page's tokens to the sums: weights from the scores x and probe values
+// av against the reference st.m, 16 tokens at a time.  `slot`: the page's value
+// codes and parameters.  kFine: with the weights' low halves.
+template <int D, int NT, bool kFine>
+__device__ __forceinline__ void q4_value_sums(Q4WarpState<D, NT>& st, const uint8_t* slot, const float (&x)[NT][8],
+                                              const float (&av)[NT][8]) {
+  using SM = Q4Smem<D, NT>;
+  constexpr int G = D / 64, J = D / 32;
+  const int lane = threadIdx.x & 31, r = lane >> 2, hc = lane & 3;
+#pragma unroll
+  for (int kk = 0; kk < 4; ++kk) {
+    uint32_t bh[NT][G][2], bl[NT][G][2];
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      const int e = 2 * kk + half;
+      uint32_t vp[G];
+      lds_words<G>(slot + SM::kCodes + (16 * kk + r + 8 * half) * (4 * G), vp);
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        const float p = ex2(x[t][e] - (st.m[t] - 14.f)), pa = p * av[t][e];
+        st.l[t] += p;
+        st.c[t] += pa;
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+          const float s = bf16_lo_f(vp[g]), mn = bf16_hi_f(vp[g]);
+          st.pm[t][g][0] = fmaf(p, mn, st.pm[t][g][0]);
+          st.pm[t][g][1] = fmaf(pa, mn, st.pm[t][g][1]);
+          const float ps = p * s, pas = pa * s;
+          const uint32_t hi = pack_half(ps, pas);
+          bh[t][g][half] = transpose_8x8(hi);
+          if constexpr (kFine) {
+            const float2 hf = unpack_half(hi);
+            bl[t][g][half] = transpose_8x8(pack_half(ps - hf.x, pas - hf.y));
+          }
+        }
+      }
+    }
+    uint32_t w0[J], w1[J];
+    lds_words<J>(slot + (8 * kk + hc) * D + r * (D / 8), w0);
+    lds_words<J>(slot + (8 * kk + hc + 4) * D + r * (D / 8), w1);
+#pragma unroll
+    for (int j = 0; j < J; j += 2) {   // the two words of a group: four products, then their low halves
+      uint32_t av4[4][4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const uint32_t u0 = w0[j + q / 2] >> (8 * (q & 1)), u1 = w1[j + q / 2] >> (8 * (q & 1));
+        av4[q][0] = u0 & 0x000f000fu;
+        av4[q][1] = u0 & 0x00f000f0u;
+        av4[q][2] = u1 & 0x000f000fu;
+        av4[q][3] = u1 & 0x00f000f0u;
+      }
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          mma_f16_16816(st.o[t][2 * j + q], av4[q][0], av4[q][1], av4[q][2], av4[q][3], bh[t][j / 2][0], bh[t][j / 2][1]);
+        if constexpr (kFine) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            mma_f16_16816(st.o[t][2 * j + q], av4[q][0], av4[q][1], av4[q][2], av4[q][3], bl[t][j / 2][0],
+                          bl[t][j / 2][1]);
+        }
+      }
+    }
   }
-  return s;
 }
+
+// The running sum of a unit's pieces for four columns of one head.
+struct Q4Merged {
+  float m = -INFINITY, l = 0.f, c = 0.f, aref = 0.f;
+  float4 o1 = make_float4(0.f, 0.f, 0.f, 0.f), o2 = make_float4(0.f, 0.f, 0.f, 0.f);
+
+  // Adds the piece (head = m, l, c, aref; p1, p2 its columns): both sides at
+  // the larger reference, the piece's probe values from this sum's offset.
+  __device__ __forceinline__ void add(const float4& head, const float4& p1, const float4& p2) {
+    const bool first = l == 0.f && m == -INFINITY;
+    const float mx = fmaxf(m, head.x), al = first ? 0.f : ex2(m - mx), be = ex2(head.x - mx);
+    if (first) aref = head.w;
+    const float shift = head.w - aref;
+    m = mx;
+    l = fmaf(be, head.y, al * l);
+    c = fmaf(be, fmaf(shift, head.y, head.z), al * c);
+    o1.x = fmaf(be, p1.x, al * o1.x);
+    o1.y = fmaf(be, p1.y, al * o1.y);
+    o1.z = fmaf(be, p1.z, al * o1.z);
+    o1.w = fmaf(be, p1.w, al * o1.w);
+    o2.x = fmaf(be, fmaf(shift, p1.x, p2.x), al * o2.x);
+    o2.y = fmaf(be, fmaf(shift, p1.y, p2.y), al * o2.y);
+    o2.z = fmaf(be, fmaf(shift, p1.z, p2.z), al * o2.z);
+    o2.w = fmaf(be, fmaf(shift, p1.w, p2.w), al * o2.w);
+  }
+  __device__ __forceinline__ void write_out(const DecodeQ4Args& a, size_t idx) const {
+    store_out4(a, idx, finalize(o1.x, o2.x, l, c), finalize(o1.y, o2.y, l, c), finalize(o1.z, o2.z, l, c),
+               finalize(o1.w, o2.w, l, c));
+  }
+};
 
 template <int D, int NT>
 __global__ void __launch_bounds__(Q4Smem<D, NT>::kThreads, 1) decode_q4_kernel(const DecodeQ4Args a) {
@@ -366,7 +446,7 @@ __global__ void __launch_bounds__(Q4Smem<D, NT>::kThreads, 1) decode_q4_kernel(c
   extern __shared__ __align__(128) uint8_t q4_smem[];
   int* meta = reinterpret_cast<int*>(q4_smem + SM::kMetaOff);   // [warp]: first piece's unit, ua, ub; last piece's
   int* pre = reinterpret_cast<int*>(q4_smem + SM::kPreOff);
-  __shared__ int s_last;
+  __shared__ int s_last[kWarps / 4];
   __shared__ int s_part[kWarps];
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -375,9 +455,9 @@ __global__ void __launch_bounds__(Q4Smem<D, NT>::kThreads, 1) decode_q4_kernel(c
   asm volatile("griddepcontrol.wait;" ::: "memory");
 
   // ---- the page space
-  Q4Space sp{a, pre, kThreads, (a.B + kThreads - 1) / kThreads, 0, 1};
+  Q4Space sp{a, pre, kThreads, (a.B + kThreads - 1) / kThreads};
   if (a.seq_lens == nullptr) {
-    sp.T = (long long)a.B * a.Hkv * ((a.kv_len + kQ4Page - 1) / kQ4Page);
+    sp.T = (uint32_t)a.B * a.Hkv * ((a.kv_len + kQ4Page - 1) / kQ4Page);
   } else {
     int sum = 0;
     const int b0 = min(a.B, tid * sp.per), b1 = min(a.B, b0 + sp.per);
@@ -408,12 +488,14 @@ __global__ void __launch_bounds__(Q4Smem<D, NT>::kThreads, 1) decode_q4_kernel(c
         for (int i = tid; i < a.Hq * D / 4; i += kThreads) store_out4(a, (size_t)b * a.Hq * D + 4 * i, 0.f, 0.f, 0.f, 0.f);
   }
   __syncthreads();
-  const long long most = (sp.T + a.min_pages - 1) / a.min_pages;
-  sp.G = most < (long long)gridDim.x ? most : (long long)gridDim.x;
-  if ((long long)blockIdx.x >= sp.G) return;
+  sp.G = min((uint32_t)gridDim.x, (sp.T + a.min_pages - 1) / a.min_pages);
+  if (blockIdx.x >= sp.G) return;
+  sp.W = sp.G * kWarps;
+  sp.quot = sp.T / sp.W;
+  sp.rem = sp.T % sp.W;
 
-  const long long W = sp.G * kWarps, gw = (long long)blockIdx.x * kWarps + warp;
-  const int y0 = (int)(gw * sp.T / W), y1 = (int)((gw + 1) * sp.T / W), n = y1 - y0;
+  const uint32_t gw = blockIdx.x * kWarps + warp;
+  const int y0 = (int)sp.start(gw), y1 = (int)sp.start(gw + 1), n = y1 - y0;
   uint8_t* ring = q4_smem + warp * SM::kRing;
   float* first_state = reinterpret_cast<float*>(q4_smem + SM::kStateOff + warp * SM::kState);
   if (lane < 8) meta[warp * 8 + lane] = -1;
@@ -433,26 +515,29 @@ __global__ void __launch_bounds__(Q4Smem<D, NT>::kThreads, 1) decode_q4_kernel(c
     const uint8_t* src = nullptr;
     const uint32_t ring_lane = smem_u32(ring) + 16 * lane;
     uint32_t fill = ring_lane;        // where the next part goes
-    auto issue = [&] {
+    auto issue = [&](auto part) {     // part: 0 for keys, 1 for values (of the page that is due)
+      constexpr bool kValues = decltype(part)::value;
       if (issued < 2 * n) {
-        const bool values = issued & 1;
-        if (!values) src = a.cache + ahead.block(sp, entry) * B::kBytes + 16 * lane;
-        const uint8_t* codes = src + (values ? B::kV : 0);
-        const uint8_t* params = src + (values ? B::kVParams : B::kKParams);
+        if (!kValues) src = a.cache + ahead.block(sp, entry) * B::kBytes + 16 * lane;
+        constexpr int kFrom = kValues ? B::kV : 0, kParams = kValues ? B::kVParams : B::kKParams;
 #pragma unroll
-        for (int c = 0; c < SM::kCodes; c += 512) q4_copy16(fill + c, codes + c);
-        if (B::kParamBytes == 512 || lane < B::kParamBytes / 16) q4_copy16(fill + SM::kCodes, params);
+        for (int c = 0; c < SM::kCodes; c += 512) q4_copy16(fill + c, src + kFrom + c);
+        if (B::kParamBytes == 512 || lane < B::kParamBytes / 16) q4_copy16(fill + SM::kCodes, src + kParams);
         ++issued;
         fill = fill == ring_lane + (S - 1) * SM::kPart ? ring_lane : fill + SM::kPart;
-        if (values && issued < 2 * n) {
+        if (kValues && issued < 2 * n) {
           ahead.next_page(sp);
           entry = ahead.entry(sp);
         }
       }
       q4_copy_commit();
     };
-#pragma unroll 1
-    for (int k = 0; k < S; ++k) issue();
+    using Keys = std::integral_constant<bool, false>;
+    using Values = std::integral_constant<bool, true>;
+#pragma unroll
+    for (int k = 0; k < S; ++k) {
+      if (k % 2 == 0) issue(Keys{}); else issue(Values{});
+    }
 
     Q4WarpState<D, NT> st;
     uint32_t qf[NT][D / 16][2];     // [q rho ..] operand
@@ -464,9 +549,9 @@ __global__ void __launch_bounds__(Q4Smem<D, NT>::kThreads, 1) decode_q4_kernel(c
       q4_copy_wait<S - 1>();
       __syncwarp();
     };
-    auto leave = [&] {              // done with the slot: refill it, go to the next one
+    auto leave = [&](auto part) {   // done with the slot: refill it, go to the next one
       __syncwarp();
-      issue();
+      issue(part);
       slot = slot == ring + (S - 1) * SM::kPart ? ring : slot + SM::kPart;
     };
     // Parameters of tokens past the sequence's end become zero (they may be
@@ -580,7 +665,7 @@ __global__ void __launch_bounds__(Q4Smem<D, NT>::kThreads, 1) decode_q4_kernel(c
           }
         }
       }
-      leave();
+      leave(std::integral_constant<bool, S % 2 != 0>{});   // part 2 i + S
       if (seg == 0) {   // the lane with token 0 (always valid) of the head
 #pragma unroll
         for (int t = 0; t < NT; ++t) st.aref[t] = __shfl_sync(0xffffffffu, av[t][0], hc);
@@ -651,65 +736,11 @@ __global__ void __launch_bounds__(Q4Smem<D, NT>::kThreads, 1) decode_q4_kernel(c
         }
       }
 
-      // ---- weights and value sums, 16 tokens at a time
-      const bool fine = cur.len < kQ4FineKeys;
-#pragma unroll
-      for (int kk = 0; kk < 4; ++kk) {
-        uint32_t bh[NT][G][2], bl[NT][G][2];
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          const int e = 2 * kk + half;
-          uint32_t vp[G];
-          lds_words<G>(slot + SM::kCodes + (16 * kk + r + 8 * half) * (4 * G), vp);
-#pragma unroll
-          for (int t = 0; t < NT; ++t) {
-            const float p = ex2(x[t][e] - (st.m[t] - 14.f)), pa = p * av[t][e];
-            st.l[t] += p;
-            st.c[t] += pa;
-#pragma unroll
-            for (int g = 0; g < G; ++g) {
-              const float s = bf16_lo_f(vp[g]), mn = bf16_hi_f(vp[g]);
-              st.pm[t][g][0] = fmaf(p, mn, st.pm[t][g][0]);
-              st.pm[t][g][1] = fmaf(pa, mn, st.pm[t][g][1]);
-              const float ps = p * s, pas = pa * s;
-              const uint32_t hi = pack_half(ps, pas);
-              bh[t][g][half] = transpose_8x8(hi);
-              if (fine) {
-                const float2 hf = unpack_half(hi);
-                bl[t][g][half] = transpose_8x8(pack_half(ps - hf.x, pas - hf.y));
-              }
-            }
-          }
-        }
-        uint32_t w0[J], w1[J];
-        lds_words<J>(slot + (8 * kk + hc) * D + r * (D / 8), w0);
-        lds_words<J>(slot + (8 * kk + hc + 4) * D + r * (D / 8), w1);
-#pragma unroll
-        for (int j = 0; j < J; j += 2) {   // the two words of a group: four products, then their low halves
-          uint32_t av4[4][4];
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const uint32_t u0 = w0[j + q / 2] >> (8 * (q & 1)), u1 = w1[j + q / 2] >> (8 * (q & 1));
-            av4[q][0] = u0 & 0x000f000fu;
-            av4[q][1] = u0 & 0x00f000f0u;
-            av4[q][2] = u1 & 0x000f000fu;
-            av4[q][3] = u1 & 0x00f000f0u;
-          }
-#pragma unroll
-          for (int t = 0; t < NT; ++t) {
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-              mma_f16_16816(st.o[t][2 * j + q], av4[q][0], av4[q][1], av4[q][2], av4[q][3], bh[t][j / 2][0], bh[t][j / 2][1]);
-            if (fine) {
-#pragma unroll
-              for (int q = 0; q < 4; ++q)
-                mma_f16_16816(st.o[t][2 * j + q], av4[q][0], av4[q][1], av4[q][2], av4[q][3], bl[t][j / 2][0],
-                              bl[t][j / 2][1]);
-            }
-          }
-        }
-      }
-      leave();
+      if (cur.len < kQ4FineKeys)
+        q4_value_sums<D, NT, true>(st, slot, x, av);
+      else
+        q4_value_sums<D, NT, false>(st, slot, x, av);
+      leave(std::integral_constant<bool, S % 2 == 0>{});
       ++seg;
 
       if (cur.local + 1 == cur.tiles && (i + 1 < n || seg == cur.tiles)) {
@@ -741,84 +772,75 @@ __global__ void __launch_bounds__(Q4Smem<D, NT>::kThreads, 1) decode_q4_kernel(c
   }
   __syncthreads();
 
-  // ---- merge the CTA's pieces, unit by unit (pieces of a unit are neighbours)
-  const long long x0 = sp.start(blockIdx.x), x1 = sp.start(blockIdx.x + 1);
-  const int rows = a.group;
-  auto piece_ptr = [&](int k) {   // piece k: warp k / 2, its first (even) or last one
-    return reinterpret_cast<const float*>((k & 1) ? q4_smem + (k >> 1) * SM::kRing
-                                                  : q4_smem + SM::kStateOff + (k >> 1) * SM::kState);
-  };
-  auto unit_of = [&](int k) { return meta[(k >> 1) * 8 + 3 * (k & 1)]; };
-  for (int k0 = 0; k0 < 2 * kWarps;) {
-    const int unit = unit_of(k0);
-    if (unit < 0) {
-      ++k0;
-      continue;
-    }
-    uint32_t list = 0;   // the pieces of the unit, as a bit set
-    int k1 = k0;
-    for (; k1 < 2 * kWarps; ++k1) {
-      const int u = unit_of(k1);
-      if (u >= 0 && u != unit) break;
-      if (u == unit) list |= 1u << k1;
-    }
-    const int ua = meta[(k0 >> 1) * 8 + 3 * (k0 & 1) + 1], ub = meta[(k0 >> 1) * 8 + 3 * (k0 & 1) + 2];
+  // ---- merge the CTA's pieces.  A team of four warps takes every kTeams-th
+  // unit: a thread four columns of a head.  Lane k knows piece k of the CTA:
+  // warp k / 2's first (even k) or last one; pieces of a unit are in order.
+  constexpr int kTeams = kWarps / 4;
+  const int team = warp / 4, tt = tid % 128;
+  const int x0 = (int)sp.start(blockIdx.x * kWarps), x1 = (int)sp.start((blockIdx.x + 1) * kWarps);
+  const int my_unit = lane < 2 * kWarps ? meta[(lane >> 1) * 8 + 3 * (lane & 1)] : -1;
+  uint32_t todo = __ballot_sync(0xffffffffu, my_unit >= 0);
+  auto team_bar = [&] { asm volatile("bar.sync %0, 128;" ::"r"(1 + team) : "memory"); };
+  for (int k = 0; todo != 0; ++k) {
+    const int first = __ffs(todo) - 1, unit = __shfl_sync(0xffffffffu, my_unit, first);
+    const uint32_t pieces = __ballot_sync(0xffffffffu, my_unit == unit);
+    todo &= ~pieces;
+    if (k % kTeams != team) continue;
+    const int ua = meta[(first >> 1) * 8 + 3 * (first & 1) + 1], ub = meta[(first >> 1) * 8 + 3 * (first & 1) + 2];
     const bool whole = ua >= x0 && ub <= x1;
-    const long long c0 = sp.owner(ua), c1 = sp.owner(ub - 1);
-    const size_t slot_stride = (size_t)rows * SM::kRow;
-    auto slot_of = [&](long long cc) { return a.slots + (2 * cc + (sp.start(cc) >= ua ? 0 : 1)) * slot_stride; };
-    float* mine = whole ? nullptr : slot_of(blockIdx.x);
-    const size_t out_row = ((size_t)(unit / a.Hkv) * a.Hq + (size_t)(unit % a.Hkv) * rows) * D;
-    for (int i = tid; i < rows * D; i += kThreads) {
-      const int h = i / D, d = i % D;
-      const Q4Merged s = merge_pieces<D>(
-          k0, 32, d, [&](int k) { return k < 31 && (list >> (k + 1)) != 0 ? k + __ffs(list >> (k + 1)) : 32; },
-          [&](int k) { return piece_ptr(k) + h * SM::kRow; }, [](const float* p) { return *p; });
+    const size_t out_row = ((size_t)(unit / a.Hkv) * a.Hq + (size_t)(unit % a.Hkv) * a.group) * D;
+    const int items = a.group * (D / 4);
+    const size_t slot_stride = (size_t)a.group * SM::kRow;
+    const uint32_t c0 = whole ? 0 : sp.owner(ua), c1 = whole ? 0 : sp.owner(ub - 1);
+    // Slot 2 c holds a piece of a unit that goes on from CTA c - 1 (or starts
+    // with c), slot 2 c + 1 one that starts inside c; of a unit's CTAs only the
+    // first can hold it in the second.
+    const bool inside = !whole && (int)sp.start(c0 * kWarps) < ua;
+    auto slot_of = [&](uint32_t c) { return a.slots + (2 * c + (c == c0 && inside ? 1 : 0)) * slot_stride; };
+    for (int i = tt; i < items; i += 128) {
+      const int h = i / (D / 4), d = 4 * (i % (D / 4));
+      Q4Merged s;
+      for (uint32_t left = pieces; left; left &= left - 1) {
+        const int q = __ffs(left) - 1;
+        const float* p = reinterpret_cast<const float*>((q & 1) ? q4_smem + (q >> 1) * SM::kRing
+                                                                : q4_smem + SM::kStateOff + (q >> 1) * SM::kState) +
+                         h * SM::kRow;
+        s.add(*reinterpret_cast<const float4*>(p), *reinterpret_cast<const float4*>(p + 4 + d),
+              *reinterpret_cast<const float4*>(p + 4 + D + d));
+      }
       if (whole) {
-        const float v = finalize(s.O1, s.O2, s.L, s.C);
-        if (a.out_bf16)
-          reinterpret_cast<__nv_bfloat16*>(a.out)[out_row + i] = __float2bfloat16_rn(v);
-        else
-          reinterpret_cast<float*>(a.out)[out_row + i] = v;
+        s.write_out(a, out_row + (size_t)h * D + d);
       } else {
-        float* row = mine + h * SM::kRow;
-        row[4 + d] = s.O1;
-        row[4 + D + d] = s.O2;
-        if (d == 0) {
-          row[0] = s.M;
-          row[1] = s.L;
-          row[2] = s.C;
-          row[3] = s.aref;
-        }
+        float* p = slot_of(blockIdx.x) + h * SM::kRow;
+        *reinterpret_cast<float4*>(p + 4 + d) = s.o1;
+        *reinterpret_cast<float4*>(p + 4 + D + d) = s.o2;
+        if (d == 0) *reinterpret_cast<float4*>(p) = make_float4(s.m, s.l, s.c, s.aref);
       }
     }
-    if (!whole) {
+    if (whole) continue;
+    __threadfence();
+    team_bar();
+    if (tt == 0) {
+      const int prev = atomicAdd(a.counters + unit, 1);
+      s_last[team] = prev == (int)(c1 - c0);
+      if (s_last[team]) atomicExch(a.counters + unit, 0);
+    }
+    team_bar();
+    if (s_last[team]) {
       __threadfence();
-      __syncthreads();
-      if (tid == 0) {
-        const int prev = atomicAdd(a.counters + unit, 1);
-        s_last = prev == (int)(c1 - c0);
-        if (s_last) atomicExch(a.counters + unit, 0);
-      }
-      __syncthreads();
-      const bool last = s_last != 0;
-      __syncthreads();
-      if (last) {
-        __threadfence();
-        for (int i = tid; i < rows * D; i += kThreads) {
-          const int h = i / D, d = i % D;
-          const Q4Merged s = merge_pieces<D>(
-              0, (int)(c1 - c0 + 1), d, [](int k) { return k + 1; },
-              [&](int k) { return slot_of(c0 + k) + h * SM::kRow; }, [](const float* p) { return __ldcg(p); });
-          const float v = finalize(s.O1, s.O2, s.L, s.C);
-          if (a.out_bf16)
-            reinterpret_cast<__nv_bfloat16*>(a.out)[out_row + i] = __float2bfloat16_rn(v);
-          else
-            reinterpret_cast<float*>(a.out)[out_row + i] = v;
+      for (int i = tt; i < items; i += 128) {
+        const int h = i / (D / 4), d = 4 * (i % (D / 4));
+        Q4Merged s;
+#pragma unroll 4
+        for (uint32_t c = c0; c <= c1; ++c) {
+          const float* p = slot_of(c) + h * SM::kRow;
+          s.add(__ldcg(reinterpret_cast<const float4*>(p)), __ldcg(reinterpret_cast<const float4*>(p + 4 + d)),
+                __ldcg(reinterpret_cast<const float4*>(p + 4 + D + d)));
         }
+        s.write_out(a, out_row + (size_t)h * D + d);
       }
     }
-    k0 = k1;
+    team_bar();   // s_last can be written again
   }
 }
 

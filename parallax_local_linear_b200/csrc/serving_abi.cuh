@@ -180,6 +180,8 @@ plx_status validate_decode_q4(const plx_decode_params* p) {
 
 // A default grid gives every CTA at least this many pages.
 constexpr int kQ4MinPages = 4;
+// The kernel counts its warps (12 a CTA) in 16 bits.
+constexpr int kQ4MaxCtas = 4096;
 
 struct DecodeQ4Plan {
   int ctas;
@@ -194,6 +196,7 @@ DecodeQ4Plan plan_decode_q4(const plx_decode_params* p, int num_sms) {
   int64_t ctas = p->num_ctas > 0 ? p->num_ctas : num_sms;
   if (ctas > (pages + least - 1) / least) ctas = (pages + least - 1) / least;
   if (ctas < 1) ctas = 1;
+  if (ctas > kQ4MaxCtas) ctas = kQ4MaxCtas;
   pl.ctas = (int)ctas;
   pl.counter_bytes = ((size_t)units * 4 + 255) & ~size_t(255);
   pl.slot_bytes = ((size_t)2 * pl.ctas * (p->num_q_heads / p->num_kv_heads) * (2 * p->head_dim + 4) * 4 + 255) &
