@@ -13,6 +13,7 @@ import collections
 import contextlib
 import ctypes
 import os
+import struct
 import threading
 
 import torch
@@ -141,29 +142,25 @@ lib.parallax_last_device_error.restype = ctypes.c_int
 lib.parallax_last_device_error.argtypes = [_vp, ctypes.POINTER(ctypes.c_int32)]
 
 lib.parallax_page_plan.restype = ctypes.c_int
-lib.parallax_page_plan.argtypes = [_vp] * 10 + [ctypes.POINTER(PagePlanParams), _vp]
+lib.parallax_page_plan.argtypes = [_vp] * 12
 lib.parallax_norm_rope.restype = ctypes.c_int
-lib.parallax_norm_rope.argtypes = [ctypes.POINTER(HeadRows), ctypes.c_int32, _i32p, _vp, _vp,
-                                   ctypes.POINTER(NormRopeParams), _vp]
+lib.parallax_norm_rope.argtypes = [_vp, ctypes.c_int32, _i32p, _vp, _vp, _vp, _vp]
 lib.parallax_norm_rope_backward_workspace_size.restype = ctypes.c_size_t
-lib.parallax_norm_rope_backward_workspace_size.argtypes = [ctypes.POINTER(NormRopeParams), ctypes.c_int32]
+lib.parallax_norm_rope_backward_workspace_size.argtypes = [_vp, ctypes.c_int32]
 lib.parallax_norm_rope_backward.restype = ctypes.c_int
-lib.parallax_norm_rope_backward.argtypes = [ctypes.POINTER(HeadRows), ctypes.POINTER(HeadGrads), ctypes.c_int32,
-                                            _i32p, _vp, _vp, _vp, ctypes.c_size_t, ctypes.POINTER(NormRopeParams),
-                                            _vp]
+lib.parallax_norm_rope_backward.argtypes = [_vp, _vp, ctypes.c_int32, _i32p, _vp, _vp, _vp, ctypes.c_size_t, _vp, _vp]
 lib.parallax_cache_append.restype = ctypes.c_int
-lib.parallax_cache_append.argtypes = [_vp] * 5 + [ctypes.POINTER(AppendParams), _vp]
+lib.parallax_cache_append.argtypes = [_vp] * 7
 lib.parallax_q4_block_bytes.restype = ctypes.c_size_t
 lib.parallax_q4_block_bytes.argtypes = [ctypes.c_int32]
 lib.parallax_cache_append_q4.restype = ctypes.c_int
-lib.parallax_cache_append_q4.argtypes = [_vp] * 4 + [ctypes.POINTER(AppendParams), _vp]
+lib.parallax_cache_append_q4.argtypes = [_vp] * 6
 lib.parallax_cache_gather_q4.restype = ctypes.c_int
-lib.parallax_cache_gather_q4.argtypes = [_vp] * 4 + [ctypes.POINTER(AppendParams), _vp]
+lib.parallax_cache_gather_q4.argtypes = [_vp] * 6
 lib.parallax_decode_q4_workspace_size.restype = ctypes.c_size_t
-lib.parallax_decode_q4_workspace_size.argtypes = [ctypes.POINTER(DecodeParams), ctypes.c_int32]
+lib.parallax_decode_q4_workspace_size.argtypes = [_vp, ctypes.c_int32]
 lib.parallax_decode_q4.restype = ctypes.c_int
-lib.parallax_decode_q4.argtypes = [_vp, _vp, _vp, _i32p, _i32p, _vp, _vp, ctypes.c_size_t,
-                                   ctypes.POINTER(DecodeParams), _vp]
+lib.parallax_decode_q4.argtypes = [_vp, _vp, _vp, _i32p, _i32p, _vp, _vp, ctypes.c_size_t, _vp, _vp]
 
 SIZE_MAX = ctypes.c_size_t(-1).value
 
@@ -679,40 +676,60 @@ def prefill_paged(q, rho, k_cache, v_cache, page_table, cu_seqlens_q, seq_lens, 
 
 # ---------------------------------------------------------------- the step around attention
 
-def _check_device(device, tensors):
-    """Every given (name, tensor, dtype) is a CUDA tensor of ``device`` and dtype (None: any)."""
-    for name, t, dtype in tensors:
-        if t is None:
-            continue
+# These calls are made between small kernels, where the host's time counts: parameter
+# structs are packed in one step (the formats below are the Structures' layouts), and
+# checks read plain integers.
+_PAGE_PLAN = struct.Struct("@6i")
+_NORM_ROPE = struct.Struct("@8if4xq")
+_HEAD_ROWS = struct.Struct("@PPPi4x6q")
+_HEAD_GRADS = struct.Struct("@PPP6q")
+_APPEND = struct.Struct("@6i4q")
+_DECODE = struct.Struct("@10ifi")
+for _fmt, _cls in ((_PAGE_PLAN, PagePlanParams), (_NORM_ROPE, NormRopeParams), (_HEAD_ROWS, HeadRows),
+                   (_HEAD_GRADS, HeadGrads), (_APPEND, AppendParams), (_DECODE, DecodeParams)):
+    assert _fmt.size == ctypes.sizeof(_cls), _cls
+
+
+def _on(index, name, t, dtype=None):
+    """t is a CUDA tensor of device ``index`` and of ``dtype`` (None: any)."""
+    if t.get_device() != index:
         if not t.is_cuda:
             raise ValueError(f"{name} must be a CUDA tensor")
-        if t.device != device:
-            raise ValueError(f"{name} is on {t.device}, not on {device}")
-        if dtype is not None and t.dtype != dtype:
-            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+        raise ValueError(f"{name} is on {t.device}, not on cuda:{index}")
+    if dtype is not None and t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+
+
+def _cuda_index(name, t):
+    index = t.get_device()
+    if index < 0:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return index
 
 
 def _check_shape(name, t, shape):
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
 
 
+_raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
 _no_guard = contextlib.nullcontext()
 
 
-def _device_guard(device):
+def _device_guard(index):
     """The library launches on the current device: make it the tensors' own."""
-    return _no_guard if torch.cuda.current_device() == device.index else torch.cuda.device(device)
-
-
-def _raw_stream(device):
-    return torch.cuda.current_stream(device).cuda_stream
+    return _no_guard if torch.cuda.current_device() == index else torch.cuda.device(index)
 
 
 def _raw(t):
     return None if t is None else t.data_ptr()
+
+
+def _raw0(t):
+    return 0 if t is None else t.data_ptr()
 
 
 PagePlan = collections.namedtuple("PagePlan", "seq_lens cu_seqlens slot_map positions pages_used")
@@ -738,28 +755,29 @@ def page_plan(cached_lens, new_lens, page_table, free_pages, *, num_rows, num_pa
     if cached_lens.dim() != 1 or page_table.dim() != 2 or free_pages.dim() != 1:
         raise ValueError("cached_lens and free_pages must be 1-D and page_table 2-D")
     B, width = cached_lens.shape[0], page_table.shape[1]
-    for name, t, shape in (("cached_lens", cached_lens, (B,)), ("new_lens", new_lens, (B,)),
-                           ("page_table", page_table, (B, width)), ("free_pages", free_pages, free_pages.shape)):
-        _check_shape(name, t, shape)
-    if free_head is not None and (free_head.numel() != 1):
+    _check_shape("cached_lens", cached_lens, (B,))
+    _check_shape("new_lens", new_lens, (B,))
+    _check_shape("page_table", page_table, (B, width))
+    _check_shape("free_pages", free_pages, free_pages.shape)
+    if free_head is not None and free_head.numel() != 1:
         raise ValueError("free_head must hold one element")
-    device = cached_lens.device
-    _check_device(device, (("cached_lens", cached_lens, torch.int32), ("new_lens", new_lens, torch.int32),
-                           ("page_table", page_table, torch.int32), ("free_pages", free_pages, torch.int32),
-                           ("free_head", free_head, torch.int32)))
-    # one allocation: slots first (8-byte entries), every part from a 16-byte boundary
-    n, b = (int(num_rows) + 3) & ~3, (B + 4) & ~3
-    buf = torch.empty(3 * n + 2 * b + 4, dtype=torch.int32, device=device)
-    slots = buf[:2 * n].view(torch.int64)[:num_rows]
-    at = 2 * n
-    positions, seq_lens = buf[at:at + num_rows], buf[at + n:at + n + B]
-    at += n + b
-    cu, used = buf[at:at + B + 1], buf[at + b:at + b + 1]
-    p = PagePlanParams(B, num_rows, PAGE_SIZE, num_pages, width, free_pages.shape[0])
-    with _device_guard(device):
-        st = lib.parallax_page_plan(_raw(cached_lens), _raw(new_lens), _raw(page_table), _raw(free_pages),
-                                    _raw(free_head), _raw(seq_lens), _raw(cu), _raw(slots), _raw(positions),
-                                    _raw(used), ctypes.byref(p), _raw_stream(device))
+    index = _cuda_index("cached_lens", cached_lens)
+    i32 = torch.int32
+    _on(index, "cached_lens", cached_lens, i32)
+    _on(index, "new_lens", new_lens, i32)
+    _on(index, "page_table", page_table, i32)
+    _on(index, "free_pages", free_pages, i32)
+    if free_head is not None:
+        _on(index, "free_head", free_head, i32)
+    num_rows = int(num_rows)
+    slots = torch.empty(num_rows, dtype=torch.int64, device=cached_lens.device)
+    seq_lens, cu, positions, used = cached_lens.new_empty(num_rows + 2 * B + 2).split((B, B + 1, num_rows, 1))
+    with _device_guard(index):
+        st = lib.parallax_page_plan(cached_lens.data_ptr(), new_lens.data_ptr(), page_table.data_ptr(),
+                                    free_pages.data_ptr(), _raw(free_head), seq_lens.data_ptr(), cu.data_ptr(),
+                                    slots.data_ptr(), positions.data_ptr(), used.data_ptr(),
+                                    _PAGE_PLAN.pack(B, num_rows, PAGE_SIZE, num_pages, width, free_pages.shape[0]),
+                                    _raw_stream(index))
     if st != 0:
         raise ParallaxError(st, "parallax_page_plan")
     return PagePlan(seq_lens, cu, slots, positions, used)
@@ -767,20 +785,19 @@ def page_plan(cached_lens, new_lens, page_table, free_pages, *, num_rows, num_pa
 
 def _head_strides(name, t, batched):
     """Element strides (batch entry, token, head) of [B, H, T, d] or packed [N, H, d] rows."""
-    if t.stride(-1) != 1 and t.numel() > 0:
-        raise ValueError(f"{name}'s last dimension must be contiguous")
     s = t.stride()
+    if s[-1] != 1 and t.numel() > 0:
+        raise ValueError(f"{name}'s last dimension must be contiguous")
     return (s[0], s[2], s[1]) if batched else (0, s[0], s[1])
 
 
 def _head_like(x):
-    """A tensor for a row set's results: x's own strides where x is dense, else plain contiguous."""
     return torch.empty_like(x, memory_format=torch.contiguous_format)
 
 
 def _norm_rope_call(q, rho, k, cos, sin, positions, weights, eps, norm, interleaved):
-    """Checks and parameters that the two directions share: (sets, params, device), a set being
-    (name, x, weight)."""
+    """Checks and parameters that the two directions share: (sets, params, device index,
+    batched), a set being (name, x, weight)."""
     batched = q.dim() == 4
     if q.dim() not in (3, 4):
         raise ValueError(f"q must be [B, H, T, d] or packed [N, H, d], got {tuple(q.shape)}")
@@ -810,19 +827,23 @@ def _norm_rope_call(q, rho, k, cos, sin, positions, weights, eps, norm, interlea
         pos_stride = T if positions.dim() == 2 else 0
     elif rot and T > max_pos:
         raise ValueError(f"{T} tokens need as many rows of cos and sin, got {max_pos}")
-    device = q.device
+    index, dtype = _cuda_index("q", q), q.dtype
     sets = [s for s in zip(("q", "rho", "k"), (q, rho, k), weights) if s[1] is not None]
     for name, x, w in sets:
+        _on(index, name, x, dtype)
         if w is not None:
             if not norm:
                 raise ValueError(f"{name}_weight needs norm=True")
             _check_shape(name + "_weight", w, (d,))
-        _check_device(device, ((name, x, q.dtype), (name + "_weight", w, q.dtype)))
-    _check_device(device, (("cos", cos, torch.float32), ("sin", sin, torch.float32),
-                           ("positions", positions, torch.int32)))
-    p = NormRopeParams(B, T, d, rot, max_pos, 1 if interleaved else 0, 1 if norm else 0, _dtype_code(q.dtype),
-                       eps, pos_stride)
-    return sets, p, device, batched
+            _on(index, name + "_weight", w, dtype)
+    if cos is not None:
+        _on(index, "cos", cos, torch.float32)
+        _on(index, "sin", sin, torch.float32)
+    if positions is not None:
+        _on(index, "positions", positions, torch.int32)
+    p = _NORM_ROPE.pack(B, T, d, rot, max_pos, 1 if interleaved else 0, 1 if norm else 0, _dtype_code(dtype), eps,
+                        pos_stride)
+    return sets, p, index, batched
 
 
 def norm_rope(q, rho, k, cos, sin, positions=None, *, q_weight=None, rho_weight=None, k_weight=None, eps=1e-6,
@@ -840,29 +861,27 @@ def norm_rope(q, rho, k, cos, sin, positions=None, *, q_weight=None, rho_weight=
     may be the input itself: in place).  Returns (q, rho, k), None where the
     input is.
     """
-    sets, p, device, batched = _norm_rope_call(q, rho, k, cos, sin, positions, (q_weight, rho_weight, k_weight),
-                                               eps, norm, interleaved)
-    if out is not None:
-        given = dict(zip(("q", "rho", "k"), out))
-        ys = [given[name] for name, _, _ in sets]
-        for (name, x, _), y in zip(sets, ys):
+    sets, p, index, batched = _norm_rope_call(q, rho, k, cos, sin, positions, (q_weight, rho_weight, k_weight), eps,
+                                              norm, interleaved)
+    done, rows = {"q": None, "rho": None, "k": None}, b""
+    given = dict(zip(done, out)) if out is not None else None
+    for name, x, w in sets:
+        strides = _head_strides(name, x, batched)
+        if given is None:
+            y = _head_like(x)
+        else:
+            y = given.get(name)
             if y is None or y.shape != x.shape:
                 raise ValueError(f"out's {name} must have shape {tuple(x.shape)}")
-            _check_device(device, (("out's " + name, y, x.dtype),))
-    else:
-        ys = [_head_like(x) for _, x, _ in sets]
-    rows = (HeadRows * len(sets))()
-    for r, (name, x, w), y in zip(rows, sets, ys):
-        r.x, r.y, r.w, r.heads = x.data_ptr(), y.data_ptr(), _raw(w), x.shape[1]
-        r.x_stride[:] = _head_strides(name, x, batched)
-        r.y_stride[:] = _head_strides("out's " + name, y, batched)
-    with _device_guard(device):
-        st = lib.parallax_norm_rope(rows, len(sets), _raw(positions), _raw(cos), _raw(sin), ctypes.byref(p),
-                                    _raw_stream(device))
+            _on(index, "out's " + name, y, x.dtype)
+        done[name] = y
+        rows += _HEAD_ROWS.pack(x.data_ptr(), y.data_ptr(), _raw0(w), x.shape[1], *strides,
+                                *_head_strides("out's " + name, y, batched))
+    with _device_guard(index):
+        st = lib.parallax_norm_rope(rows, len(sets), _raw(positions), _raw(cos), _raw(sin), p, _raw_stream(index))
     if st != 0:
         raise ParallaxError(st, "parallax_norm_rope")
-    done = {name: y for (name, _, _), y in zip(sets, ys)}
-    return tuple(done.get(name) for name in ("q", "rho", "k"))
+    return tuple(done.values())
 
 
 def norm_rope_backward(dq, drho, dk, q, rho, k, cos, sin, positions=None, *, q_weight=None, rho_weight=None,
@@ -874,38 +893,35 @@ def norm_rope_backward(dq, drho, dk, q, rho, k, cos, sin, positions=None, *, q_w
     over all rows; None without norm, and everything is None for a set that is.
     Without given weights, the gradients of weights of one are returned.
     """
-    sets, p, device, batched = _norm_rope_call(q, rho, k, cos, sin, positions, (q_weight, rho_weight, k_weight),
-                                               eps, norm, interleaved)
-    incoming = {"q": dq, "rho": drho, "k": dk}
-    rows, grads = (HeadRows * len(sets))(), (HeadGrads * len(sets))()
-    d = q.shape[-1]
-    dws = torch.empty(len(sets), d, dtype=torch.float32, device=device) if norm else None
-    dxs = {}
-    for i, (name, x, w) in enumerate(sets):
+    sets, p, index, batched = _norm_rope_call(q, rho, k, cos, sin, positions, (q_weight, rho_weight, k_weight), eps,
+                                              norm, interleaved)
+    names = ("q", "rho", "k")
+    incoming, dxs, dws = dict(zip(names, (dq, drho, dk))), dict.fromkeys(names), dict.fromkeys(names)
+    rows = grads = b""
+    no_strides = (0,) * 3
+    for name, x, w in sets:
         dy = incoming[name]
         if dy is None or dy.shape != x.shape:
             raise ValueError(f"d{name} must have shape {tuple(x.shape)}")
-        _check_device(device, (("d" + name, dy, x.dtype),))
+        _on(index, "d" + name, dy, x.dtype)
         dx = dxs[name] = _head_like(x)
-        r, g = rows[i], grads[i]
-        r.x, r.w, r.heads = x.data_ptr(), _raw(w), x.shape[1]
-        r.x_stride[:] = _head_strides(name, x, batched)
-        g.dy, g.dx, g.dw = dy.data_ptr(), dx.data_ptr(), _raw(dws[i]) if norm else None
-        g.dy_stride[:] = _head_strides("d" + name, dy, batched)
-        g.dx_stride[:] = _head_strides("d" + name, dx, batched)
-    with _device_guard(device):
-        ws = None
         if norm:
-            nbytes = lib.parallax_norm_rope_backward_workspace_size(ctypes.byref(p), len(sets))
+            dws[name] = torch.empty(x.shape[-1], dtype=torch.float32, device=x.device)
+        rows += _HEAD_ROWS.pack(x.data_ptr(), 0, _raw0(w), x.shape[1], *_head_strides(name, x, batched), *no_strides)
+        grads += _HEAD_GRADS.pack(dy.data_ptr(), dx.data_ptr(), _raw0(dws[name]),
+                                  *_head_strides("d" + name, dy, batched), *_head_strides("d" + name, dx, batched))
+    with _device_guard(index):
+        ws, nbytes = None, 0
+        if norm:
+            nbytes = lib.parallax_norm_rope_backward_workspace_size(p, len(sets))
             if nbytes == SIZE_MAX:
                 raise ParallaxError(2, "parallax_norm_rope_backward_workspace_size")
-            ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
+            ws = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
         st = lib.parallax_norm_rope_backward(rows, grads, len(sets), _raw(positions), _raw(cos), _raw(sin), _raw(ws),
-                                             0 if ws is None else ws.numel(), ctypes.byref(p), _raw_stream(device))
+                                             nbytes, p, _raw_stream(index))
     if st != 0:
         raise ParallaxError(st, "parallax_norm_rope_backward")
-    at = {name: dws[i] for i, (name, _, _) in enumerate(sets)} if norm else {}
-    return tuple(dxs.get(n) for n in ("q", "rho", "k")) + tuple(at.get(n) for n in ("q", "rho", "k"))
+    return tuple(dxs.values()) + tuple(dws.values())
 
 
 class NormRope(torch.autograd.Function):
@@ -944,19 +960,22 @@ def _dense_rows(g):
     return g if ok else g.contiguous()
 
 
-def _append_params(k, v, slot_map, num_pages, num_kv_heads, head_dim, dtype):
-    for name, t in (("k", k), ("v", v)):
-        if t.dim() != 3 or t.shape[1] != num_kv_heads or t.shape[2] != head_dim:
-            raise ValueError(f"{name} must be [N, {num_kv_heads}, {head_dim}], got {tuple(t.shape)}")
-        if t.numel() > 0 and t.stride(2) != 1:
-            raise ValueError(f"{name}'s last dimension must be contiguous")
-    if v.shape[0] != k.shape[0]:
-        raise ValueError(f"k has {k.shape[0]} rows and v {v.shape[0]}")
-    _check_shape("slot_map", slot_map, (k.shape[0],))
-    p = AppendParams(k.shape[0], num_kv_heads, head_dim, PAGE_SIZE, num_pages, dtype)
-    p.k_stride[:] = k.stride()[:2]
-    p.v_stride[:] = v.stride()[:2]
-    return p
+def _append_params(k, v, slot_map, num_pages, num_kv_heads, head_dim, dtype, index):
+    """Checks of k, v [N, Hkv, d] and slot_map [N]; the packed parameters."""
+    if k.dim() != 3 or k.shape[1] != num_kv_heads or k.shape[2] != head_dim:
+        raise ValueError(f"k must be [N, {num_kv_heads}, {head_dim}], got {tuple(k.shape)}")
+    n = k.shape[0]
+    if v.shape != k.shape:
+        raise ValueError(f"v must have k's shape {tuple(k.shape)}, got {tuple(v.shape)}")
+    ks, vs = k.stride(), v.stride()
+    if n > 0 and (ks[2] != 1 or vs[2] != 1):
+        raise ValueError("the last dimension of k and v must be contiguous")
+    _check_shape("slot_map", slot_map, (n,))
+    _on(index, "k", k, dtype)
+    _on(index, "v", v, dtype)
+    _on(index, "slot_map", slot_map, torch.int64)
+    return _APPEND.pack(n, num_kv_heads, head_dim, PAGE_SIZE, num_pages, _dtype_code(dtype), ks[0], ks[1], vs[0],
+                        vs[1])
 
 
 def cache_append(k, v, slot_map, k_cache, v_cache):
@@ -973,13 +992,12 @@ def cache_append(k, v, slot_map, k_cache, v_cache):
     P, Hkv, _, d = k_cache.shape
     _check_shape("k_cache", k_cache, k_cache.shape)
     _check_shape("v_cache", v_cache, v_cache.shape)
-    p = _append_params(k, v, slot_map, P, Hkv, d, _dtype_code(k_cache.dtype))
-    device = k_cache.device
-    _check_device(device, (("k", k, k_cache.dtype), ("v", v, k_cache.dtype), ("slot_map", slot_map, torch.int64),
-                           ("k_cache", k_cache, None), ("v_cache", v_cache, k_cache.dtype)))
-    with _device_guard(device):
-        st = lib.parallax_cache_append(_raw(k), _raw(v), _raw(slot_map), _raw(k_cache), _raw(v_cache),
-                                       ctypes.byref(p), _raw_stream(device))
+    index = _cuda_index("k_cache", k_cache)
+    _on(index, "v_cache", v_cache, k_cache.dtype)
+    p = _append_params(k, v, slot_map, P, Hkv, d, k_cache.dtype, index)
+    with _device_guard(index):
+        st = lib.parallax_cache_append(k.data_ptr(), v.data_ptr(), slot_map.data_ptr(), k_cache.data_ptr(),
+                                       v_cache.data_ptr(), p, _raw_stream(index))
     if st != 0:
         raise ParallaxError(st, "parallax_cache_append")
 
@@ -1023,13 +1041,11 @@ def cache_append_q4(k, v, slot_map, kv_cache):
     Each 64 columns of a row share a scale and a minimum.
     """
     P, Hkv, d = _q4_pool(kv_cache)
-    p = _append_params(k, v, slot_map, P, Hkv, d, PLX_BF16)
-    device = kv_cache.device
-    _check_device(device, (("k", k, torch.bfloat16), ("v", v, torch.bfloat16), ("slot_map", slot_map, torch.int64),
-                           ("kv_cache", kv_cache, None)))
-    with _device_guard(device):
-        st = lib.parallax_cache_append_q4(_raw(k), _raw(v), _raw(slot_map), _raw(kv_cache), ctypes.byref(p),
-                                          _raw_stream(device))
+    index = _cuda_index("kv_cache", kv_cache)
+    p = _append_params(k, v, slot_map, P, Hkv, d, torch.bfloat16, index)
+    with _device_guard(index):
+        st = lib.parallax_cache_append_q4(k.data_ptr(), v.data_ptr(), slot_map.data_ptr(), kv_cache.data_ptr(), p,
+                                          _raw_stream(index))
     if st != 0:
         raise ParallaxError(st, "parallax_cache_append_q4")
 
@@ -1039,18 +1055,19 @@ def cache_gather_q4(kv_cache, slot_map, *, out_dtype=torch.bfloat16, out=None):
     of ``out_dtype`` (bfloat16 or float32).  Rows at slot -1 are left as
     allocated (``out``: the two tensors to write)."""
     P, Hkv, d = _q4_pool(kv_cache)
-    device = kv_cache.device
+    index = _cuda_index("kv_cache", kv_cache)
     if out is None:
-        shape = (2, slot_map.shape[0], Hkv, d) if slot_map.dim() == 1 else (2, 0, Hkv, d)
-        k, v = torch.empty(shape, dtype=out_dtype, device=device)
+        if slot_map.dim() != 1:
+            raise ValueError(f"slot_map must be 1-D, got {tuple(slot_map.shape)}")
+        shape = (slot_map.shape[0], Hkv, d)
+        k = torch.empty(shape, dtype=out_dtype, device=kv_cache.device)
+        v = torch.empty(shape, dtype=out_dtype, device=kv_cache.device)
     else:
         k, v = out
-    p = _append_params(k, v, slot_map, P, Hkv, d, _dtype_code(k.dtype))
-    _check_device(device, (("k", k, None), ("v", v, k.dtype), ("slot_map", slot_map, torch.int64),
-                           ("kv_cache", kv_cache, None)))
-    with _device_guard(device):
-        st = lib.parallax_cache_gather_q4(_raw(kv_cache), _raw(slot_map), _raw(k), _raw(v), ctypes.byref(p),
-                                          _raw_stream(device))
+    p = _append_params(k, v, slot_map, P, Hkv, d, k.dtype, index)
+    with _device_guard(index):
+        st = lib.parallax_cache_gather_q4(kv_cache.data_ptr(), slot_map.data_ptr(), k.data_ptr(), v.data_ptr(), p,
+                                          _raw_stream(index))
     if st != 0:
         raise ParallaxError(st, "parallax_cache_gather_q4")
     return k, v
@@ -1059,7 +1076,7 @@ def cache_gather_q4(kv_cache, slot_map, *, out_dtype=torch.bfloat16, out=None):
 _q4_workspaces = {}
 
 
-def _q4_workspace(device, nbytes, units):
+def _q4_workspace(index, nbytes, units):
     """The 4-bit decode's workspace: one per device and stream, since calls on
     different streams may overlap.  Partials are at its front and the counters
     (4 bytes a unit) at its end; it is large enough for the most of either that
@@ -1067,14 +1084,14 @@ def _q4_workspace(device, nbytes, units):
     counters, and zeroed when allocated.  A captured graph gets one of its own
     (zeroed in the graph), so that graphs replayed at once do not share it."""
     if torch.cuda.is_current_stream_capturing():
-        return torch.zeros(nbytes, dtype=torch.uint8, device=device)
+        return torch.zeros(nbytes, dtype=torch.uint8, device=index)
     counters = (4 * units + 255) & ~255
-    key = (device.index, _raw_stream(device))
+    key = (index, _raw_stream(index))
     with _ws_lock:
         ws, most_slots, most_counters = _q4_workspaces.get(key, (None, 1 << 20, 1 << 14))
         if ws is None or nbytes - counters > most_slots or counters > most_counters:
             most_slots, most_counters = max(most_slots, nbytes - counters), max(most_counters, counters)
-            ws = torch.zeros(most_slots + most_counters, dtype=torch.uint8, device=device)
+            ws = torch.zeros(most_slots + most_counters, dtype=torch.uint8, device=index)
             _q4_workspaces[key] = ws, most_slots, most_counters
         return ws
 
@@ -1119,23 +1136,29 @@ def decode_q4(q, rho, kv_cache, scale=None, *, seq_lens=None, page_table=None, o
                              "(use seq_lens for shorter sequences)")
     if seq_lens is not None:
         _check_shape("seq_lens", seq_lens, (B,))
-    for name, t in (("q", q), ("rho", rho), ("kv_cache", kv_cache)):
-        _check_shape(name, t, t.shape)
-    device = q.device
-    _check_device(device, (("q", q, torch.bfloat16), ("rho", rho, torch.bfloat16), ("kv_cache", kv_cache, None),
-                           ("page_table", page_table, torch.int32), ("seq_lens", seq_lens, torch.int32)))
-    out, out_dtype = _output(out, out_dtype, q.shape, torch.bfloat16, device)
-    _check_device(device, (("out", out, None),))
-    p = DecodeParams(B, Hq, Hkv, d, kv_len, PAGE_SIZE if paged else 0, kv_cache.shape[0] if paged else 0,
+    _check_shape("q", q, q.shape)
+    _check_shape("rho", rho, q.shape)
+    _check_shape("kv_cache", kv_cache, kv_cache.shape)
+    index = _cuda_index("q", q)
+    _on(index, "q", q, torch.bfloat16)
+    _on(index, "rho", rho, torch.bfloat16)
+    _on(index, "kv_cache", kv_cache)
+    if page_table is not None:
+        _on(index, "page_table", page_table, torch.int32)
+    if seq_lens is not None:
+        _on(index, "seq_lens", seq_lens, torch.int32)
+    out, out_dtype = _output(out, out_dtype, q.shape, torch.bfloat16, q.device)
+    _on(index, "out", out)
+    p = _DECODE.pack(B, Hq, Hkv, d, kv_len, PAGE_SIZE if paged else 0, kv_cache.shape[0] if paged else 0,
                      page_table.shape[1] if paged else 0, PLX_BF16, _dtype_code(out_dtype),
                      (1.0 / d ** 0.5) if scale is None else float(scale), int(num_ctas))
-    with _device_guard(device):
-        nbytes = lib.parallax_decode_q4_workspace_size(ctypes.byref(p), 0)
+    with _device_guard(index):
+        nbytes = lib.parallax_decode_q4_workspace_size(p, 0)
         if nbytes == SIZE_MAX:
             raise ParallaxError(1, "parallax_decode_q4_workspace_size")
-        ws = _q4_workspace(device, nbytes, B * Hkv)
-        st = lib.parallax_decode_q4(_raw(q), _raw(rho), _raw(kv_cache), _raw(page_table), _raw(seq_lens), _raw(out),
-                                    _raw(ws), ws.numel(), ctypes.byref(p), _raw_stream(device))
+        ws = _q4_workspace(index, nbytes, B * Hkv)
+        st = lib.parallax_decode_q4(q.data_ptr(), rho.data_ptr(), kv_cache.data_ptr(), _raw(page_table),
+                                    _raw(seq_lens), out.data_ptr(), ws.data_ptr(), ws.numel(), p, _raw_stream(index))
     if st != 0:
         raise ParallaxError(st, "parallax_decode_q4")
     return out
