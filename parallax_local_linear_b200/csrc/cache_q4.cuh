@@ -1,8 +1,8 @@
 // The paged cache's writers and the 4-bit cache's reader: cache append (plain
 // pools and 4-bit blocks) and gather.  The block layout is in parallax.h.
 //
-// All three move rows between [N, Hkv, d] tensors and slots of the cache, one
-// 16-byte vector (8 bf16 columns) per lane.  HBM bounds them on long prompts
+// All three move rows between [N, Hkv, d] tensors and slots of the cache.  HBM
+// bounds them on long prompts
 // and launch latency on single tokens: append_q4 reads 4 d bytes of a token
 // and head and writes 72 d / 64.
 #pragma once
@@ -75,51 +75,74 @@ __global__ void __launch_bounds__(kAppendThreads) cache_append_kernel(const Appe
 }
 
 // ------------------------------------------------------------------- quantise
-// Codes of the lane's 8 columns (code i in bits 4 i) and the parameter word of
-// its group, which 8 neighbouring lanes share.
-__device__ __forceinline__ void quantise8(const uint4& vec, uint32_t& codes, uint32_t& param) {
-  float x[8];
-  const uint32_t w[4] = {vec.x, vec.y, vec.z, vec.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    x[2 * i] = bf16_lo_f(w[i]);
-    x[2 * i + 1] = bf16_hi_f(w[i]);
-  }
-  float lo = x[0], hi = x[0];
-  bool finite = true;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    lo = fminf(lo, x[i]);
-    hi = fmaxf(hi, x[i]);
-    finite = finite && fabsf(x[i]) < INFINITY;   // false for NaN too
-  }
-#pragma unroll
-  for (int o = 1; o < 8; o <<= 1) {
-    lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
-    hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
-  }
-  const uint32_t group = 0xffu << (threadIdx.x & 24);
-  const float range = hi - lo;
-  finite = (__ballot_sync(0xffffffffu, finite) & group) == group && range < INFINITY;
-  const uint32_t s16 = pack_bf16(__fdiv_rn(range, 15.f), 0.f) & 0xffffu;
-  const float s = __uint_as_float(s16 << 16);
-  // A group that cannot be held reads back NaN: scale 0, minimum NaN.
-  param = finite ? s16 | (__float_as_uint(lo) & 0xffff0000u) : 0x7fc00000u;
-  codes = 0;
-  if (!finite || !(s > 0.f)) return;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float q = rintf(__fdiv_rn(x[i] - lo, s));
-    codes |= (uint32_t)fminf(q, 15.f) << (4 * i);
-  }
+// The format's own arithmetic for one value: fp32 difference and quotient,
+// rounded to nearest even.
+__device__ __forceinline__ uint32_t q4_code(float x, float lo, float s) {
+  return (uint32_t)fminf(rintf(__fdiv_rn(x - lo, s)), 15.f);
 }
 
-// K's word order: column i of 8 at bits 16 (i % 2) + 4 (i / 2).
-__device__ __forceinline__ uint32_t k_word(uint32_t c) {
-  uint32_t w = 0;
+__device__ __forceinline__ __nv_bfloat162 as_bf162(uint32_t v) { return *reinterpret_cast<__nv_bfloat162*>(&v); }
+__device__ __forceinline__ uint32_t as_u32(__nv_bfloat162 v) { return *reinterpret_cast<uint32_t*>(&v); }
+
+// Codes of the lane's 8 columns and the parameter word of its group, which 8
+// neighbouring lanes share.  kKeys: code i at bits 16 (i % 2) + 4 (i / 2) (a K
+// word), otherwise at bits 4 i (two V half words).
+//
+// Minimum and maximum are taken on packed bf16 pairs, NaN winning, so a group
+// that is not finite ends up with a range that is not.  Quotients are products
+// with 1/s, off by less than 2^-18 here; only a lane that has one within 2^-15
+// of a border between two codes (or a scale so small that 1/s is not safe)
+// divides.  The same holds for range/15 and the border between two bf16
+// values.  Dividing throughout took 764 instructions a vector pair, this
+// takes 280.
+template <bool kKeys>
+__device__ __forceinline__ void quantise8(const uint4& vec, uint32_t& codes, uint32_t& param) {
+  const uint32_t w[4] = {vec.x, vec.y, vec.z, vec.w};
+  __nv_bfloat162 mn = __hmin2_nan(__hmin2_nan(as_bf162(w[0]), as_bf162(w[1])), __hmin2_nan(as_bf162(w[2]), as_bf162(w[3])));
+  __nv_bfloat162 mx = __hmax2_nan(__hmax2_nan(as_bf162(w[0]), as_bf162(w[1])), __hmax2_nan(as_bf162(w[2]), as_bf162(w[3])));
 #pragma unroll
-  for (int i = 0; i < 8; ++i) w |= ((c >> (4 * i)) & 15u) << (16 * (i & 1) + 4 * (i >> 1));
-  return w;
+  for (int o = 1; o < 8; o <<= 1) {
+    mn = __hmin2_nan(mn, as_bf162(__shfl_xor_sync(0xffffffffu, as_u32(mn), o)));
+    mx = __hmax2_nan(mx, as_bf162(__shfl_xor_sync(0xffffffffu, as_u32(mx), o)));
+  }
+  mn = __hmin2_nan(mn, __lowhigh2highlow(mn));
+  mx = __hmax2_nan(mx, __lowhigh2highlow(mx));
+  const float lo = bf16_hi_f(as_u32(mn)), range = bf16_hi_f(as_u32(mx)) - lo;
+  // A group that cannot be held reads back NaN: scale 0, minimum NaN.
+  const bool finite = range < INFINITY;
+  float ratio = range * (1.f / 15.f);
+  if (((__float_as_uint(ratio) + 0x8004u) & 0xffffu) < 8u || ratio < 0x1p-100f) ratio = __fdiv_rn(range, 15.f);
+  const uint32_t s16 = pack_bf16(ratio, 0.f) & 0xffffu;
+  const float s = __uint_as_float(s16 << 16);
+  param = finite ? s16 | (__float_as_uint(lo) & 0xffff0000u) : 0x7fc00000u;
+  const float inv = __frcp_rn(s);
+  // q + 1.5 2^23 holds round(q) in its low bits; the words' sum takes the
+  // constant's own bits out again.
+  constexpr uint32_t kMagicBits = 0x4b400000u;
+  const float2 lo2 = make_float2(-lo, -lo), inv2 = make_float2(inv, inv);
+  const float2 magic = make_float2(12582912.f, 12582912.f), unmagic = make_float2(-12582912.f, -12582912.f);
+  uint32_t sum = 0;
+  float far = 0.f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 q = mul2(add2(make_float2(bf16_lo_f(w[i]), bf16_hi_f(w[i])), lo2), inv2);
+    const float2 t = add2(q, magic);
+    const float2 n = add2(t, unmagic);
+    far = fmaxf(far, fmaxf(fabsf(q.x - n.x), fabsf(q.y - n.y)));
+    const int p0 = kKeys ? 4 * i : 8 * i, p1 = kKeys ? 16 + 4 * i : 8 * i + 4;
+    sum += ((__float_as_uint(t.x) - kMagicBits) << p0) + ((__float_as_uint(t.y) - kMagicBits) << p1);
+  }
+  if (!(far < 0.5f - 0x1p-15f) || s < 0x1p-100f || !finite) {
+    sum = 0;
+    if (s > 0.f && finite) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int p0 = kKeys ? 4 * i : 8 * i, p1 = kKeys ? 16 + 4 * i : 8 * i + 4;
+        sum |= q4_code(bf16_lo_f(w[i]), lo, s) << p0 | q4_code(bf16_hi_f(w[i]), lo, s) << p1;
+      }
+    }
+  }
+  codes = sum;
 }
 
 template <int D>
@@ -133,22 +156,22 @@ __global__ void __launch_bounds__(kAppendThreads) cache_append_q4_kernel(const A
   const int l = (int)(i % LPR);
   const bool in = rh < (long long)a.N * a.Hkv;
   const int r = in ? (int)(rh / a.Hkv) : 0, h = in ? (int)(rh % a.Hkv) : 0;
-  int page = -1, row = 0;
-  if (in) slot_of_row(a, r, page, row);
   uint4 kv = make_uint4(0, 0, 0, 0), vv = kv;
-  if (page >= 0) {
+  if (in) {   // beside the slot's load
     kv = __ldg(static_cast<const uint4*>(a.k) + r * a.ks[0] + h * a.ks[1] + l);
     vv = __ldg(static_cast<const uint4*>(a.v) + r * a.vs[0] + h * a.vs[1] + l);
   }
+  int page = -1, row = 0;
+  if (in) slot_of_row(a, r, page, row);
   uint32_t kc, kp, vc, vp;   // every lane of the warp takes part in the shuffles
-  quantise8(kv, kc, kp);
-  quantise8(vv, vc, vp);
+  quantise8<true>(kv, kc, kp);
+  quantise8<false>(vv, vc, vp);
   if (page < 0) return;
   uint8_t* block = a.cache + ((size_t)page * a.Hkv + h) * B::kBytes;
   // lane l holds columns 8 l ..: word c = l % 4, j = l / 4 of the K row, words
   // r = 2 (l % 4) + {0, 1} of the V row
   uint32_t* krow = reinterpret_cast<uint32_t*>(block + row * (D / 2));
-  krow[B::kWords * (l % 4) + l / 4] = k_word(kc);
+  krow[B::kWords * (l % 4) + l / 4] = kc;
   uint16_t* vrow = reinterpret_cast<uint16_t*>(block + B::kV + (row / 2) * D) + (row & 1);
   vrow[2 * (B::kWords * (2 * (l % 4)) + l / 4)] = (uint16_t)vc;
   vrow[2 * (B::kWords * (2 * (l % 4) + 1) + l / 4)] = (uint16_t)(vc >> 16);
@@ -159,45 +182,63 @@ __global__ void __launch_bounds__(kAppendThreads) cache_append_q4_kernel(const A
 }
 
 // --------------------------------------------------------------------- gather
+// A lane takes four neighbouring columns of a key and a value row, so that a
+// row of results is written without gaps (with eight, an fp32 row is written
+// 16 bytes of every 32 at a time: 38 against 24 us for 134 MB), and kGatherRows
+// rows, so that their loads overlap.
+constexpr int kGatherRows = 4;
+
 template <int D, bool kBf16>
 __global__ void __launch_bounds__(kAppendThreads) cache_gather_q4_kernel(const AppendArgs a) {
   using B = Q4Block<D>;
-  constexpr int LPR = D / 8;
+  constexpr int LPR = D / 4, RPC = kAppendThreads / LPR;   // lanes of a row, rows a CTA takes at once
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const long long i = (long long)blockIdx.x * kAppendThreads + threadIdx.x;
-  const long long rh = i / LPR;
-  if (rh >= (long long)a.N * a.Hkv) return;
-  const int l = (int)(i % LPR), r = (int)(rh / a.Hkv), h = (int)(rh % a.Hkv);
-  int page, row;
-  slot_of_row(a, r, page, row);
-  if (page < 0) return;
-  const uint8_t* block = a.cache + ((size_t)page * a.Hkv + h) * B::kBytes;
-  const uint32_t kw = reinterpret_cast<const uint32_t*>(block + row * (D / 2))[B::kWords * (l % 4) + l / 4];
-  const uint16_t* vrow = reinterpret_cast<const uint16_t*>(block + B::kV + (row / 2) * D) + (row & 1);
-  const uint32_t vw = vrow[2 * (B::kWords * (2 * (l % 4)) + l / 4)] |
-                      (uint32_t)vrow[2 * (B::kWords * (2 * (l % 4) + 1) + l / 4)] << 16;
-  const uint32_t kp = reinterpret_cast<const uint32_t*>(block + B::kKParams)[row * B::kGroups + l / 8];
-  const uint32_t vp = reinterpret_cast<const uint32_t*>(block + B::kVParams)[row * B::kGroups + l / 8];
-  float kx[8], vx[8];
+  const int l = threadIdx.x % LPR;
+  const long long first = (long long)blockIdx.x * (RPC * kGatherRows) + threadIdx.x / LPR;
+  const uint8_t* block[kGatherRows];
+  int r[kGatherRows], h[kGatherRows], row[kGatherRows];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    kx[e] = fmaf(bf16_lo_f(kp), (float)((kw >> (16 * (e & 1) + 4 * (e >> 1))) & 15u), bf16_hi_f(kp));
-    vx[e] = fmaf(bf16_lo_f(vp), (float)((vw >> (4 * e)) & 15u), bf16_hi_f(vp));
+  for (int u = 0; u < kGatherRows; ++u) {
+    const long long rh = first + u * RPC;
+    int page = -1;
+    r[u] = (int)(rh / a.Hkv);
+    h[u] = (int)(rh % a.Hkv);
+    if (rh < (long long)a.N * a.Hkv) slot_of_row(a, r[u], page, row[u]);
+    block[u] = page < 0 ? nullptr : a.cache + ((size_t)page * a.Hkv + h[u]) * B::kBytes;
   }
-  // strides in 16-byte vectors
-  if (kBf16) {
-    static_cast<uint4*>(a.k_out)[r * a.ks[0] + h * a.ks[1] + l] =
-        make_uint4(pack_bf16(kx[0], kx[1]), pack_bf16(kx[2], kx[3]), pack_bf16(kx[4], kx[5]), pack_bf16(kx[6], kx[7]));
-    static_cast<uint4*>(a.v_out)[r * a.vs[0] + h * a.vs[1] + l] =
-        make_uint4(pack_bf16(vx[0], vx[1]), pack_bf16(vx[2], vx[3]), pack_bf16(vx[4], vx[5]), pack_bf16(vx[6], vx[7]));
-  } else {
-    float4* ko = static_cast<float4*>(a.k_out) + r * a.ks[0] + h * a.ks[1] + 2 * l;
-    float4* vo = static_cast<float4*>(a.v_out) + r * a.vs[0] + h * a.vs[1] + 2 * l;
-    ko[0] = make_float4(kx[0], kx[1], kx[2], kx[3]);
-    ko[1] = make_float4(kx[4], kx[5], kx[6], kx[7]);
-    vo[0] = make_float4(vx[0], vx[1], vx[2], vx[3]);
-    vo[1] = make_float4(vx[4], vx[5], vx[6], vx[7]);
+  // columns 4 l .. 4 l + 3: a half of K's word l / 2 (columns 8 (l / 2) ..), and
+  // a half word of V's
+  const int kw = B::kWords * ((l / 2) % 4) + l / 8, kshift = 8 * (l % 2);
+  const int vw = B::kWords * (l % 8) + l / 8;
+  uint32_t kc[kGatherRows], vc[kGatherRows], kp[kGatherRows], vp[kGatherRows];
+#pragma unroll
+  for (int u = 0; u < kGatherRows; ++u) {
+    if (block[u] == nullptr) continue;
+    kc[u] = reinterpret_cast<const uint32_t*>(block[u] + row[u] * (D / 2))[kw] >> kshift;
+    vc[u] = reinterpret_cast<const uint16_t*>(block[u] + B::kV + (row[u] / 2) * D)[2 * vw + (row[u] & 1)];
+    kp[u] = reinterpret_cast<const uint32_t*>(block[u] + B::kKParams)[row[u] * B::kGroups + l / 16];
+    vp[u] = reinterpret_cast<const uint32_t*>(block[u] + B::kVParams)[row[u] * B::kGroups + l / 16];
+  }
+#pragma unroll
+  for (int u = 0; u < kGatherRows; ++u) {
+    if (block[u] == nullptr) continue;
+    float kx[4], vx[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      kx[e] = fmaf(bf16_lo_f(kp[u]), (float)((kc[u] >> (16 * (e & 1) + 4 * (e >> 1))) & 15u), bf16_hi_f(kp[u]));
+      vx[e] = fmaf(bf16_lo_f(vp[u]), (float)((vc[u] >> (4 * e)) & 15u), bf16_hi_f(vp[u]));
+    }
+    // strides in 16-byte vectors
+    uint4* ko = static_cast<uint4*>(a.k_out) + r[u] * a.ks[0] + h[u] * a.ks[1];
+    uint4* vo = static_cast<uint4*>(a.v_out) + r[u] * a.vs[0] + h[u] * a.vs[1];
+    if (kBf16) {
+      reinterpret_cast<uint2*>(ko)[l] = make_uint2(pack_bf16(kx[0], kx[1]), pack_bf16(kx[2], kx[3]));
+      reinterpret_cast<uint2*>(vo)[l] = make_uint2(pack_bf16(vx[0], vx[1]), pack_bf16(vx[2], vx[3]));
+    } else {
+      reinterpret_cast<float4*>(ko)[l] = make_float4(kx[0], kx[1], kx[2], kx[3]);
+      reinterpret_cast<float4*>(vo)[l] = make_float4(vx[0], vx[1], vx[2], vx[3]);
+    }
   }
 }
 

@@ -45,35 +45,33 @@ struct NormRopeArgs {
   float eps;
 };
 
-// A lane's share of a row: E values from one 16-byte vector.
+// A lane's share of a row: E values from one 16-byte vector, in pairs (the
+// packed fp32 arithmetic takes two at an instruction).
 template <typename T>
 struct RowVec;
 template <>
 struct RowVec<__nv_bfloat16> {
   static constexpr int E = 8;
-  static __device__ __forceinline__ void unpack(const uint4& v, float (&f)[E]) {
+  static __device__ __forceinline__ void unpack(const uint4& v, float2 (&f)[4]) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      f[2 * i] = bf16_lo_f(w[i]);
-      f[2 * i + 1] = bf16_hi_f(w[i]);
-    }
+    for (int i = 0; i < 4; ++i) f[i] = make_float2(bf16_lo_f(w[i]), bf16_hi_f(w[i]));
   }
-  static __device__ __forceinline__ uint4 pack(const float (&f)[E]) {
-    return make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7]));
+  static __device__ __forceinline__ uint4 pack(const float2 (&f)[4]) {
+    return make_uint4(pack_bf16(f[0].x, f[0].y), pack_bf16(f[1].x, f[1].y), pack_bf16(f[2].x, f[2].y),
+                      pack_bf16(f[3].x, f[3].y));
   }
 };
 template <>
 struct RowVec<float> {
   static constexpr int E = 4;
-  static __device__ __forceinline__ void unpack(const uint4& v, float (&f)[E]) {
-    f[0] = __uint_as_float(v.x);
-    f[1] = __uint_as_float(v.y);
-    f[2] = __uint_as_float(v.z);
-    f[3] = __uint_as_float(v.w);
+  static __device__ __forceinline__ void unpack(const uint4& v, float2 (&f)[2]) {
+    f[0] = make_float2(__uint_as_float(v.x), __uint_as_float(v.y));
+    f[1] = make_float2(__uint_as_float(v.z), __uint_as_float(v.w));
   }
-  static __device__ __forceinline__ uint4 pack(const float (&f)[E]) {
-    return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+  static __device__ __forceinline__ uint4 pack(const float2 (&f)[2]) {
+    return make_uint4(__float_as_uint(f[0].x), __float_as_uint(f[0].y), __float_as_uint(f[1].x),
+                      __float_as_uint(f[1].y));
   }
 };
 
@@ -81,19 +79,19 @@ struct RowVec<float> {
 //     y_e = n_e c[e] + partner(n)_e s[e].
 // (c, s) is (cos, -sin) for the first column of a pair, (cos, sin) for the
 // second and (1, 0) past rot.
-template <int E>
+template <int P>
 struct Turn {
-  float c[E], s[E];
+  float2 c[P], s[P];
 };
 
-template <int E, bool kInter>
-__device__ __forceinline__ void load_turn(const NormRopeArgs& a, int pos, int col0, Turn<E>& t) {
+template <int P, bool kInter>
+__device__ __forceinline__ void load_turn(const NormRopeArgs& a, int pos, int col0, Turn<P>& t) {
   const int half = a.rot / 2;
   if (col0 >= a.rot) {
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
-      t.c[e] = 1.f;
-      t.s[e] = 0.f;
+    for (int i = 0; i < P; ++i) {
+      t.c[i] = make_float2(1.f, 1.f);
+      t.s[i] = make_float2(0.f, 0.f);
     }
     return;
   }
@@ -102,46 +100,23 @@ __device__ __forceinline__ void load_turn(const NormRopeArgs& a, int pos, int co
     const float* cp = a.cos + row + col0 / 2;
     const float* sp = a.sin + row + col0 / 2;
 #pragma unroll
-    for (int i = 0; i < E / 2; ++i) {
+    for (int i = 0; i < P; ++i) {
       const float c = __ldg(cp + i), s = __ldg(sp + i);
-      t.c[2 * i] = t.c[2 * i + 1] = c;
-      t.s[2 * i] = -s;
-      t.s[2 * i + 1] = s;
+      t.c[i] = make_float2(c, c);
+      t.s[i] = make_float2(-s, s);
     }
   } else {
     const bool second = col0 >= half;   // rot is a multiple of 16: a lane's columns lie in one half
     const int f0 = second ? col0 - half : col0;
 #pragma unroll
-    for (int i = 0; i < E / 4; ++i) {
+    for (int i = 0; i < P / 2; ++i) {
       const float4 c = __ldg(reinterpret_cast<const float4*>(a.cos + row + f0) + i);
       const float4 s = __ldg(reinterpret_cast<const float4*>(a.sin + row + f0) + i);
-      t.c[4 * i] = c.x;
-      t.c[4 * i + 1] = c.y;
-      t.c[4 * i + 2] = c.z;
-      t.c[4 * i + 3] = c.w;
-      t.s[4 * i] = second ? s.x : -s.x;
-      t.s[4 * i + 1] = second ? s.y : -s.y;
-      t.s[4 * i + 2] = second ? s.z : -s.z;
-      t.s[4 * i + 3] = second ? s.w : -s.w;
+      t.c[2 * i] = make_float2(c.x, c.y);
+      t.c[2 * i + 1] = make_float2(c.z, c.w);
+      t.s[2 * i] = second ? make_float2(s.x, s.y) : make_float2(-s.x, -s.y);
+      t.s[2 * i + 1] = second ? make_float2(s.z, s.w) : make_float2(-s.z, -s.w);
     }
-  }
-}
-
-// The partner's vector of the same row.
-template <int E, bool kInter>
-__device__ __forceinline__ uint4 partner_vec(const uint4& v, int src) {
-  if (kInter) return v;
-  return make_uint4(__shfl_sync(0xffffffffu, v.x, src), __shfl_sync(0xffffffffu, v.y, src),
-                    __shfl_sync(0xffffffffu, v.z, src), __shfl_sync(0xffffffffu, v.w, src));
-}
-template <int E, bool kInter>
-__device__ __forceinline__ void swap_pairs(float (&f)[E]) {   // interleaved: the partner of column e is e ^ 1
-  if (!kInter) return;
-#pragma unroll
-  for (int e = 0; e < E; e += 2) {
-    const float t = f[e];
-    f[e] = f[e + 1];
-    f[e + 1] = t;
   }
 }
 
@@ -154,28 +129,30 @@ __device__ __forceinline__ float row_sum(float v) {
 
 template <typename T, int D, bool kInter>
 struct NrLane {
-  static constexpr int E = RowVec<T>::E, LPR = D / E, RPW = 32 / LPR;
+  static constexpr int E = RowVec<T>::E, P = E / 2, LPR = D / E, RPW = 32 / LPR;
   int col0, src;       // first column, lane of the rotation partner
-  bool turned;         // this lane's columns turn
 
   __device__ __forceinline__ explicit NrLane(const NormRopeArgs& a) {
     const int lane = threadIdx.x & 31, l = lane % LPR;
     col0 = l * E;
-    turned = col0 < a.rot;
     const int shift = a.rot / 2 / E;
-    src = !turned || kInter ? lane : (col0 < a.rot / 2 ? lane + shift : lane - shift);
+    src = col0 >= a.rot || kInter ? lane : (col0 < a.rot / 2 ? lane + shift : lane - shift);
   }
-  __device__ __forceinline__ void weights(const void* w, float (&own)[E], float (&other)[E]) const {
-    // the sets of a warp's groups differ, so every lane takes part in the shuffles
-    uint4 v = make_uint4(0, 0, 0, 0);
-    if (w != nullptr) v = __ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(w) + col0));
-    RowVec<T>::unpack(v, own);
-    RowVec<T>::unpack(partner_vec<E, kInter>(v, src), other);
-    swap_pairs<E, kInter>(other);
-    if (w == nullptr) {
+  // The partner columns of a vector of the lane's row.  Every lane takes part.
+  __device__ __forceinline__ void partner(const uint4& v, float2 (&f)[P]) const {
+    if (kInter) {   // the partner of column e is e ^ 1
+      RowVec<T>::unpack(v, f);
 #pragma unroll
-      for (int e = 0; e < E; ++e) own[e] = other[e] = 1.f;
+      for (int i = 0; i < P; ++i) f[i] = make_float2(f[i].y, f[i].x);
+    } else {
+      RowVec<T>::unpack(make_uint4(__shfl_sync(0xffffffffu, v.x, src), __shfl_sync(0xffffffffu, v.y, src),
+                                   __shfl_sync(0xffffffffu, v.z, src), __shfl_sync(0xffffffffu, v.w, src)),
+                        f);
     }
+  }
+  __device__ __forceinline__ uint4 load_weights(const void* w) const {
+    return w == nullptr ? make_uint4(0, 0, 0, 0)
+                        : __ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(w) + col0));
   }
 };
 
@@ -214,7 +191,7 @@ __device__ __forceinline__ int nr_position(const NormRopeArgs& a, int b, int t) 
 template <typename T, int D, bool kInter>
 __global__ void __launch_bounds__(kNrThreads) norm_rope_kernel(const NormRopeArgs a) {
   using L = NrLane<T, D, kInter>;
-  constexpr int E = L::E;
+  constexpr int P = L::P;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const L ln(a);
@@ -225,38 +202,47 @@ __global__ void __launch_bounds__(kNrThreads) norm_rope_kernel(const NormRopeArg
   const NormRopeSet& set = a.set[it.s];
   const int pos = it.live ? nr_position(a, it.b, it.t) : -1;
   const bool live = pos >= 0;
-  Turn<E> tn;
-  load_turn<E, kInter>(a, live ? pos : 0, live ? ln.col0 : D, tn);
-  float w[E], wp[E];
-  ln.weights(set.w, w, wp);
-  const T* x = static_cast<const T*>(set.x) + it.b * set.xs[0] + it.t * set.xs[1] + ln.col0;
-  T* y = static_cast<T*>(set.y) + it.b * set.ys[0] + it.t * set.ys[1] + ln.col0;
+  // y = r (x wc + partner(x) ws) with the weights taken into the rotation
+  float2 wc[P], ws[P];
+  {
+    Turn<P> tn;
+    load_turn<P, kInter>(a, live ? pos : 0, live ? ln.col0 : D, tn);
+    const uint4 wv = ln.load_weights(set.w);
+    float2 w[P], wp[P];
+    RowVec<T>::unpack(wv, w);
+    ln.partner(wv, wp);
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+      wc[i] = set.w == nullptr ? tn.c[i] : mul2(w[i], tn.c[i]);
+      ws[i] = set.w == nullptr ? tn.s[i] : mul2(wp[i], tn.s[i]);
+    }
+  }
+  const T* x = static_cast<const T*>(set.x) + it.b * set.xs[0] + it.t * set.xs[1] + it.h0 * set.xs[2] + ln.col0;
+  T* y = static_cast<T*>(set.y) + it.b * set.ys[0] + it.t * set.ys[1] + it.h0 * set.ys[2] + ln.col0;
+  const int heads = live ? it.h1 - it.h0 : 0;
   constexpr int U = 4;   // rows in flight
   for (int j = 0; j < a.hpg; j += U) {
     uint4 v[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int h = it.h0 + j + u;
       v[u] = make_uint4(0, 0, 0, 0);
-      if (live && h < it.h1) v[u] = *reinterpret_cast<const uint4*>(x + h * set.xs[2]);
+      if (j + u < heads) v[u] = *reinterpret_cast<const uint4*>(x + (j + u) * set.xs[2]);
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      float f[E], p[E], o[E];
+      float2 f[P], p[P], o[P];
       RowVec<T>::unpack(v[u], f);
-      RowVec<T>::unpack(partner_vec<E, kInter>(v[u], ln.src), p);
-      swap_pairs<E, kInter>(p);
+      ln.partner(v[u], p);
       float r = 1.f;
       if (a.norm) {
-        float ss = 0.f;
+        float2 ss = make_float2(0.f, 0.f);
 #pragma unroll
-        for (int e = 0; e < E; ++e) ss = fmaf(f[e] * (1.f / D), f[e], ss);   // overflows only with the mean itself
-        r = rsqrtf(row_sum<L::LPR>(ss) + a.eps);
+        for (int i = 0; i < P; ++i) ss = fma2(mul2(f[i], make_float2(1.f / D, 1.f / D)), f[i], ss);   // (overflows only with the mean itself)
+        r = rsqrtf(row_sum<L::LPR>(ss.x + ss.y) + a.eps);
       }
 #pragma unroll
-      for (int e = 0; e < E; ++e) o[e] = f[e] * r * w[e] * tn.c[e] + p[e] * r * wp[e] * tn.s[e];
-      const int h = it.h0 + j + u;
-      if (live && h < it.h1) *reinterpret_cast<uint4*>(y + h * set.ys[2]) = RowVec<T>::pack(o);
+      for (int i = 0; i < P; ++i) o[i] = mul2(fma2(f[i], wc[i], mul2(p[i], ws[i])), make_float2(r, r));
+      if (j + u < heads) *reinterpret_cast<uint4*>(y + (j + u) * set.ys[2]) = RowVec<T>::pack(o);
     }
   }
 }
@@ -266,16 +252,19 @@ __global__ void __launch_bounds__(kNrThreads) norm_rope_kernel(const NormRopeArg
 template <typename T, int D, bool kInter>
 __global__ void __launch_bounds__(kNrThreads) norm_rope_bwd_kernel(const NormRopeArgs a) {
   using L = NrLane<T, D, kInter>;
-  constexpr int E = L::E;
+  constexpr int P = L::P;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const L ln(a);
   const int s = blockIdx.y;
   const NormRopeSet& set = a.set[s];
-  float w[E], wp[E], acc[E];
-  ln.weights(set.w, w, wp);
+  float2 w[P], acc[P];
+  RowVec<T>::unpack(ln.load_weights(set.w), w);
 #pragma unroll
-  for (int e = 0; e < E; ++e) acc[e] = 0.f;
+  for (int i = 0; i < P; ++i) {
+    if (set.w == nullptr) w[i] = make_float2(1.f, 1.f);
+    acc[i] = make_float2(0.f, 0.f);
+  }
   const long long groups = (long long)gridDim.x * kNrThreads / L::LPR;
   const long long items = (long long)a.B * a.T * set.chunks;
   const long long group = ((long long)blockIdx.x * kNrThreads + threadIdx.x) / L::LPR;
@@ -284,61 +273,59 @@ __global__ void __launch_bounds__(kNrThreads) norm_rope_bwd_kernel(const NormRop
     const NrItem it = nr_item(a, base + group, set.chunks, s, s);
     const int pos = it.live ? nr_position(a, it.b, it.t) : -1;
     const bool live = pos >= 0;
-    Turn<E> tn;
-    load_turn<E, kInter>(a, live ? pos : 0, live ? ln.col0 : D, tn);
-    const T* x = static_cast<const T*>(set.x) + it.b * set.xs[0] + it.t * set.xs[1] + ln.col0;
-    const T* dy = static_cast<const T*>(set.dy) + it.b * set.ds[0] + it.t * set.ds[1] + ln.col0;
-    T* dx = static_cast<T*>(set.y) + it.b * set.ys[0] + it.t * set.ys[1] + ln.col0;
+    Turn<P> tn;
+    load_turn<P, kInter>(a, live ? pos : 0, live ? ln.col0 : D, tn);
+    const T* x = static_cast<const T*>(set.x) + it.b * set.xs[0] + it.t * set.xs[1] + it.h0 * set.xs[2] + ln.col0;
+    const T* dy = static_cast<const T*>(set.dy) + it.b * set.ds[0] + it.t * set.ds[1] + it.h0 * set.ds[2] + ln.col0;
+    T* dx = static_cast<T*>(set.y) + it.b * set.ys[0] + it.t * set.ys[1] + it.h0 * set.ys[2] + ln.col0;
+    const int heads = it.live ? it.h1 - it.h0 : 0;   // (padding rows of a live token read nothing and write zeros)
     constexpr int U = 2;
     for (int j = 0; j < a.hpg; j += U) {
       uint4 vx[U], vd[U];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int h = it.h0 + j + u;
         vx[u] = vd[u] = make_uint4(0, 0, 0, 0);
-        if (live && h < it.h1) {
-          if (a.norm) vx[u] = *reinterpret_cast<const uint4*>(x + h * set.xs[2]);
-          vd[u] = *reinterpret_cast<const uint4*>(dy + h * set.ds[2]);
+        if (live && j + u < heads) {
+          if (a.norm) vx[u] = *reinterpret_cast<const uint4*>(x + (j + u) * set.xs[2]);
+          vd[u] = *reinterpret_cast<const uint4*>(dy + (j + u) * set.ds[2]);
         }
       }
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        float f[E], d[E], p[E], o[E];
+        float2 f[P], d[P], p[P], g[P];
         RowVec<T>::unpack(vx[u], f);
         RowVec<T>::unpack(vd[u], d);
-        RowVec<T>::unpack(partner_vec<E, kInter>(vd[u], ln.src), p);
-        swap_pairs<E, kInter>(p);
-        float ss = 0.f, gx = 0.f;
+        ln.partner(vd[u], p);
+        float2 ss = make_float2(0.f, 0.f), gx = ss;
 #pragma unroll
-        for (int e = 0; e < E; ++e) {
-          d[e] = d[e] * tn.c[e] - p[e] * tn.s[e];   // dn: the transposed rotation
-          const float fd = f[e] * (1.f / D);
-          ss = fmaf(fd, f[e], ss);
-          gx = fmaf(d[e] * w[e], fd, gx);
+        for (int i = 0; i < P; ++i) {
+          // dn: the transposed rotation
+          d[i] = fma2(d[i], tn.c[i], mul2(p[i], make_float2(-tn.s[i].x, -tn.s[i].y)));
+          g[i] = mul2(d[i], w[i]);
+          const float2 fd = mul2(f[i], make_float2(1.f / D, 1.f / D));
+          ss = fma2(fd, f[i], ss);
+          gx = fma2(g[i], fd, gx);
         }
         if (a.norm) {
-          ss = row_sum<L::LPR>(ss);
-          gx = row_sum<L::LPR>(gx);
-          const float r = rsqrtf(ss + a.eps);
-          const float k = r * r * gx;
+          const float r = rsqrtf(row_sum<L::LPR>(ss.x + ss.y) + a.eps);
+          const float k = -r * r * row_sum<L::LPR>(gx.x + gx.y);
 #pragma unroll
-          for (int e = 0; e < E; ++e) {
-            o[e] = r * (d[e] * w[e] - f[e] * k);
-            acc[e] = fmaf(d[e], f[e] * r, acc[e]);
+          for (int i = 0; i < P; ++i) {
+            g[i] = mul2(fma2(f[i], make_float2(k, k), g[i]), make_float2(r, r));
+            acc[i] = fma2(d[i], mul2(f[i], make_float2(r, r)), acc[i]);
           }
         } else {
 #pragma unroll
-          for (int e = 0; e < E; ++e) o[e] = d[e];
+          for (int i = 0; i < P; ++i) g[i] = d[i];
         }
-        const int h = it.h0 + j + u;
-        if (it.live && h < it.h1) *reinterpret_cast<uint4*>(dx + h * set.ys[2]) = RowVec<T>::pack(o);
+        if (j + u < heads) *reinterpret_cast<uint4*>(dx + (j + u) * set.ys[2]) = RowVec<T>::pack(g);
       }
     }
   }
   if (set.dw == nullptr) return;
   __shared__ float part[kNrThreads / L::LPR][D];
 #pragma unroll
-  for (int e = 0; e < E; ++e) part[threadIdx.x / L::LPR][ln.col0 + e] = acc[e];
+  for (int i = 0; i < P; ++i) *reinterpret_cast<float2*>(&part[threadIdx.x / L::LPR][ln.col0 + 2 * i]) = acc[i];
   __syncthreads();
   if (threadIdx.x < D) {
     float sum = 0.f;

@@ -161,11 +161,12 @@ AppendArgs append_args(const int64_t* slots, const plx_append_params* p) {
   return a;
 }
 
+// `lanes` threads for each (row, KV head), or for `rows` of them.
 template <typename Kernel>
-plx_status launch_rows(Kernel kern, const AppendArgs& a, int lanes, cudaStream_t stream) {
-  const long long threads = (long long)a.N * a.Hkv * lanes;
-  return launch_pdl(kern, dim3((unsigned)((threads + kAppendThreads - 1) / kAppendThreads)), dim3(kAppendThreads), 0,
-                    stream, a) == cudaSuccess
+plx_status launch_rows(Kernel kern, const AppendArgs& a, int lanes, cudaStream_t stream, int rows = 1) {
+  const long long per_cta = kAppendThreads / lanes * rows;
+  const long long ctas = ((long long)a.N * a.Hkv + per_cta - 1) / per_cta;
+  return launch_pdl(kern, dim3((unsigned)ctas), dim3(kAppendThreads), 0, stream, a) == cudaSuccess
              ? PLX_OK
              : PLX_ERR_CUDA;
 }
@@ -394,12 +395,11 @@ plx_status parallax_cache_gather_q4(const void* kv_cache, const int64_t* slot_ma
   a.k_out = k;
   a.v_out = v;
   a.cache = const_cast<uint8_t*>(static_cast<const uint8_t*>(kv_cache));
-  const int lanes = p->head_dim / 8;
-  if (p->head_dim == 64)
-    return p->dtype == PLX_BF16 ? launch_rows(cache_gather_q4_kernel<64, true>, a, lanes, stream)
-                                : launch_rows(cache_gather_q4_kernel<64, false>, a, lanes, stream);
-  return p->dtype == PLX_BF16 ? launch_rows(cache_gather_q4_kernel<128, true>, a, lanes, stream)
-                              : launch_rows(cache_gather_q4_kernel<128, false>, a, lanes, stream);
+  const int lanes = p->head_dim / 4;
+  auto kern = p->head_dim == 64 ? (p->dtype == PLX_BF16 ? cache_gather_q4_kernel<64, true> : cache_gather_q4_kernel<64, false>)
+                                : (p->dtype == PLX_BF16 ? cache_gather_q4_kernel<128, true>
+                                                        : cache_gather_q4_kernel<128, false>);
+  return launch_rows(kern, a, lanes, stream, kGatherRows);
 }
 
 size_t parallax_decode_q4_workspace_size(const plx_decode_params* p, int32_t num_sms) {
