@@ -59,10 +59,9 @@ template <int VPR>
 __global__ void __launch_bounds__(kAppendThreads) cache_append_kernel(const AppendArgs a) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const long long i = (long long)blockIdx.x * kAppendThreads + threadIdx.x;
-  const long long rh = i / VPR;
-  if (rh >= (long long)a.N * a.Hkv) return;
-  const int vec = (int)(i % VPR), r = (int)(rh / a.Hkv), h = (int)(rh % a.Hkv);
+  const uint32_t i = blockIdx.x * kAppendThreads + threadIdx.x, rh = i / VPR;
+  if (rh >= (uint32_t)a.N * a.Hkv) return;
+  const int vec = i % VPR, r = rh / (uint32_t)a.Hkv, h = rh - r * a.Hkv;
   int page, row;
   slot_of_row(a, r, page, row);
   if (page < 0) return;
@@ -151,11 +150,10 @@ __global__ void __launch_bounds__(kAppendThreads) cache_append_q4_kernel(const A
   constexpr int LPR = D / 8;   // lanes of a row
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const long long i = (long long)blockIdx.x * kAppendThreads + threadIdx.x;
-  const long long rh = i / LPR;
-  const int l = (int)(i % LPR);
-  const bool in = rh < (long long)a.N * a.Hkv;
-  const int r = in ? (int)(rh / a.Hkv) : 0, h = in ? (int)(rh % a.Hkv) : 0;
+  const uint32_t i = blockIdx.x * kAppendThreads + threadIdx.x, rh = i / LPR;
+  const int l = i % LPR;
+  const bool in = rh < (uint32_t)a.N * a.Hkv;
+  const int r = rh / (uint32_t)a.Hkv, h = rh - r * a.Hkv;
   uint4 kv = make_uint4(0, 0, 0, 0), vv = kv;
   if (in) {   // beside the slot's load
     kv = __ldg(static_cast<const uint4*>(a.k) + r * a.ks[0] + h * a.ks[1] + l);
@@ -195,16 +193,16 @@ __global__ void __launch_bounds__(kAppendThreads) cache_gather_q4_kernel(const A
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int l = threadIdx.x % LPR;
-  const long long first = (long long)blockIdx.x * (RPC * kGatherRows) + threadIdx.x / LPR;
+  const uint32_t first = blockIdx.x * (RPC * kGatherRows) + threadIdx.x / LPR;
   const uint8_t* block[kGatherRows];
   int r[kGatherRows], h[kGatherRows], row[kGatherRows];
 #pragma unroll
   for (int u = 0; u < kGatherRows; ++u) {
-    const long long rh = first + u * RPC;
+    const uint32_t rh = first + u * RPC;
     int page = -1;
-    r[u] = (int)(rh / a.Hkv);
-    h[u] = (int)(rh % a.Hkv);
-    if (rh < (long long)a.N * a.Hkv) slot_of_row(a, r[u], page, row[u]);
+    r[u] = rh / (uint32_t)a.Hkv;
+    h[u] = rh - r[u] * a.Hkv;
+    if (rh < (uint32_t)a.N * a.Hkv) slot_of_row(a, r[u], page, row[u]);
     block[u] = page < 0 ? nullptr : a.cache + ((size_t)page * a.Hkv + h[u]) * B::kBytes;
   }
   // columns 4 l .. 4 l + 3: a half of K's word l / 2 (columns 8 (l / 2) ..), and

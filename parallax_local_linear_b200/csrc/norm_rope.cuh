@@ -22,6 +22,7 @@ namespace plx {
 
 constexpr int kNrThreads = 256;
 constexpr int kNrMaxSets = 3;
+constexpr int kNrBwdCtasPerSm = 3;
 
 struct NormRopeSet {
   const void* x;
@@ -30,6 +31,7 @@ struct NormRopeSet {
   const void* w;
   float* dw;              // backward only
   int heads, chunks;      // chunks of `hpg` heads
+  int ctas, first_cta;    // backward: its share of the grid
   long long xs[3], ys[3], ds[3];   // element strides of batch entry, token, head
 };
 
@@ -38,10 +40,9 @@ struct NormRopeArgs {
   const int32_t* positions;
   const float* cos;
   const float* sin;
-  float* partial;         // backward: [sets][gridDim.x][D]
+  float* partial;         // backward: [gridDim.x][D]
   long long pos_batch_stride;
   int sets, B, T, rot, max_pos, norm, hpg;
-  int head_inner;         // consecutive groups take a token's chunks, not consecutive tokens
   float eps;
 };
 
@@ -156,28 +157,6 @@ struct NrLane {
   }
 };
 
-// Where group `item` works: its token and its set's heads h0 .. h1 - 1.  Sets
-// and tokens are uniform over a group of LPR lanes, not over the warp.
-struct NrItem {
-  int s, b, t, h0, h1;
-  bool live;
-};
-__device__ __forceinline__ NrItem nr_item(const NormRopeArgs& a, long long item, int chunks, int s_first, int s_last) {
-  const long long tokens = (long long)a.B * a.T;
-  NrItem it;
-  it.live = item < tokens * chunks;
-  if (!it.live) item = 0;
-  const long long tok = a.head_inner ? item / chunks : item % tokens;
-  int c = (int)(a.head_inner ? item % chunks : item / tokens);
-  it.s = s_first;
-  while (it.s < s_last && c >= a.set[it.s].chunks) c -= a.set[it.s++].chunks;
-  it.b = (int)(tok / a.T);
-  it.t = (int)(tok % a.T);
-  it.h0 = c * a.hpg;
-  it.h1 = min(a.set[it.s].heads, it.h0 + a.hpg);
-  return it;
-}
-
 // The position of a token, or -1 for padding (a bad one is reported).
 __device__ __forceinline__ int nr_position(const NormRopeArgs& a, int b, int t) {
   if (a.positions == nullptr && t < a.max_pos) return t;
@@ -188,6 +167,8 @@ __device__ __forceinline__ int nr_position(const NormRopeArgs& a, int b, int t) 
   return -1;
 }
 
+// A group of LPR lanes takes the rows of chunk blockIdx.y (a set's next `hpg`
+// heads) of one token; neighbouring groups take neighbouring tokens.
 template <typename T, int D, bool kInter>
 __global__ void __launch_bounds__(kNrThreads) norm_rope_kernel(const NormRopeArgs a) {
   using L = NrLane<T, D, kInter>;
@@ -195,12 +176,13 @@ __global__ void __launch_bounds__(kNrThreads) norm_rope_kernel(const NormRopeArg
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const L ln(a);
-  int chunks = 0;
-  for (int s = 0; s < a.sets; ++s) chunks += a.set[s].chunks;
-  const long long group = ((long long)blockIdx.x * kNrThreads + threadIdx.x) / L::LPR;
-  const NrItem it = nr_item(a, group, chunks, 0, a.sets - 1);
-  const NormRopeSet& set = a.set[it.s];
-  const int pos = it.live ? nr_position(a, it.b, it.t) : -1;
+  int chunk = blockIdx.y, si = 0;
+  while (chunk >= a.set[si].chunks) chunk -= a.set[si++].chunks;
+  const NormRopeSet& set = a.set[si];
+  const int tok = (int)((blockIdx.x * kNrThreads + threadIdx.x) / L::LPR);
+  const int b = a.B == 1 ? 0 : tok / a.T, t = tok - b * a.T;
+  const int h0 = chunk * a.hpg;
+  const int pos = b < a.B && t < a.T ? nr_position(a, b, t) : -1;
   const bool live = pos >= 0;
   // y = r (x wc + partner(x) ws) with the weights taken into the rotation
   float2 wc[P], ws[P];
@@ -217,9 +199,9 @@ __global__ void __launch_bounds__(kNrThreads) norm_rope_kernel(const NormRopeArg
       ws[i] = set.w == nullptr ? tn.s[i] : mul2(wp[i], tn.s[i]);
     }
   }
-  const T* x = static_cast<const T*>(set.x) + it.b * set.xs[0] + it.t * set.xs[1] + it.h0 * set.xs[2] + ln.col0;
-  T* y = static_cast<T*>(set.y) + it.b * set.ys[0] + it.t * set.ys[1] + it.h0 * set.ys[2] + ln.col0;
-  const int heads = live ? it.h1 - it.h0 : 0;
+  const T* x = static_cast<const T*>(set.x) + b * set.xs[0] + t * set.xs[1] + h0 * set.xs[2] + ln.col0;
+  T* y = static_cast<T*>(set.y) + b * set.ys[0] + t * set.ys[1] + h0 * set.ys[2] + ln.col0;
+  const int heads = live ? min(a.hpg, set.heads - h0) : 0;
   constexpr int U = 4;   // rows in flight
   for (int j = 0; j < a.hpg; j += U) {
     uint4 v[U];
@@ -247,17 +229,19 @@ __global__ void __launch_bounds__(kNrThreads) norm_rope_kernel(const NormRopeArg
   }
 }
 
-// Backward.  CTAs of blockIdx.y = s walk over set s; each leaves its sum for
-// dw in partial[s][blockIdx.x].
+// Backward.  Every set has a share of the grid's CTAs by its number of heads;
+// each CTA walks over its set's rows and leaves its sum for dw in
+// partial[blockIdx.x].
 template <typename T, int D, bool kInter>
-__global__ void __launch_bounds__(kNrThreads) norm_rope_bwd_kernel(const NormRopeArgs a) {
+__global__ void __launch_bounds__(kNrThreads, kNrBwdCtasPerSm) norm_rope_bwd_kernel(const NormRopeArgs a) {
   using L = NrLane<T, D, kInter>;
   constexpr int P = L::P;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const L ln(a);
-  const int s = blockIdx.y;
-  const NormRopeSet& set = a.set[s];
+  int si = 0;
+  while (si + 1 < a.sets && (int)blockIdx.x >= a.set[si + 1].first_cta) ++si;
+  const NormRopeSet& set = a.set[si];
   float2 w[P], acc[P];
   RowVec<T>::unpack(ln.load_weights(set.w), w);
 #pragma unroll
@@ -265,20 +249,22 @@ __global__ void __launch_bounds__(kNrThreads) norm_rope_bwd_kernel(const NormRop
     if (set.w == nullptr) w[i] = make_float2(1.f, 1.f);
     acc[i] = make_float2(0.f, 0.f);
   }
-  const long long groups = (long long)gridDim.x * kNrThreads / L::LPR;
-  const long long items = (long long)a.B * a.T * set.chunks;
-  const long long group = ((long long)blockIdx.x * kNrThreads + threadIdx.x) / L::LPR;
+  const uint32_t groups = set.ctas * (kNrThreads / L::LPR), tokens = a.B * a.T, items = tokens * set.chunks;
+  const uint32_t group = (blockIdx.x - set.first_cta) * (kNrThreads / L::LPR) + threadIdx.x / L::LPR;
   // Every lane of a warp makes the same number of rounds: the sums' shuffles need all of them.
-  for (long long base = 0; base < items; base += groups) {
-    const NrItem it = nr_item(a, base + group, set.chunks, s, s);
-    const int pos = it.live ? nr_position(a, it.b, it.t) : -1;
+  for (uint32_t base = 0; base < items; base += groups) {
+    const uint32_t item = base + group;
+    const bool in = item < items;
+    const int chunk = in ? item / tokens : 0, tok = in ? item - chunk * tokens : 0;
+    const int b = a.B == 1 ? 0 : tok / a.T, t = tok - b * a.T, h0 = chunk * a.hpg;
+    const int pos = in ? nr_position(a, b, t) : -1;
     const bool live = pos >= 0;
     Turn<P> tn;
     load_turn<P, kInter>(a, live ? pos : 0, live ? ln.col0 : D, tn);
-    const T* x = static_cast<const T*>(set.x) + it.b * set.xs[0] + it.t * set.xs[1] + it.h0 * set.xs[2] + ln.col0;
-    const T* dy = static_cast<const T*>(set.dy) + it.b * set.ds[0] + it.t * set.ds[1] + it.h0 * set.ds[2] + ln.col0;
-    T* dx = static_cast<T*>(set.y) + it.b * set.ys[0] + it.t * set.ys[1] + it.h0 * set.ys[2] + ln.col0;
-    const int heads = it.live ? it.h1 - it.h0 : 0;   // (padding rows of a live token read nothing and write zeros)
+    const T* x = static_cast<const T*>(set.x) + b * set.xs[0] + t * set.xs[1] + h0 * set.xs[2] + ln.col0;
+    const T* dy = static_cast<const T*>(set.dy) + b * set.ds[0] + t * set.ds[1] + h0 * set.ds[2] + ln.col0;
+    T* dx = static_cast<T*>(set.y) + b * set.ys[0] + t * set.ys[1] + h0 * set.ys[2] + ln.col0;
+    const int heads = in ? min(a.hpg, set.heads - h0) : 0;   // (padding rows of a live token read nothing and write zeros)
     constexpr int U = 2;
     for (int j = 0; j < a.hpg; j += U) {
       uint4 vx[U], vd[U];
@@ -331,22 +317,25 @@ __global__ void __launch_bounds__(kNrThreads) norm_rope_bwd_kernel(const NormRop
     float sum = 0.f;
 #pragma unroll
     for (int g = 0; g < kNrThreads / L::LPR; ++g) sum += part[g][threadIdx.x];
-    a.partial[((size_t)s * gridDim.x + blockIdx.x) * D + threadIdx.x] = sum;
+    a.partial[(size_t)blockIdx.x * D + threadIdx.x] = sum;
   }
 }
 
-// dw of set blockIdx.x: the sum of its `n` partial rows, in a fixed order.
+// dw of set blockIdx.x: the sum of its CTAs' partial rows, in a fixed order.
 template <int D>
-__global__ void __launch_bounds__(kNrThreads) norm_rope_dw_kernel(const NormRopeArgs a, int n) {
+__global__ void __launch_bounds__(kNrThreads) norm_rope_dw_kernel(const NormRopeArgs a) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  float* dw = a.set[blockIdx.x].dw;
+  const NormRopeSet& set = a.set[blockIdx.x];
+  float* dw = set.dw;
   if (dw == nullptr) return;
   constexpr int kWays = kNrThreads / D;
   __shared__ float part[kWays][D];
   const int d = threadIdx.x % D, way = threadIdx.x / D;
-  const float* p = a.partial + (size_t)blockIdx.x * n * D + d;
+  const float* p = a.partial + (size_t)set.first_cta * D + d;
+  const int n = set.ctas;
   float sum = 0.f;
+#pragma unroll 8
   for (int i = way; i < n; i += kWays) sum += p[(size_t)i * D];
   part[way][d] = sum;
   __syncthreads();

@@ -44,7 +44,9 @@ plx_status validate_norm_rope(const plx_head_rows* rows, const plx_head_grads* g
   for (int i = 0; i < num_sets; ++i) {
     const plx_head_rows& r = rows[i];
     if (r.heads < 1) return PLX_ERR_INVALID_ARG;
-    if ((int64_t)r.heads * p->batch * p->tokens >= (int64_t)INT32_MAX) return PLX_ERR_UNSUPPORTED;
+    // a set's rows and the grid's threads are counted in 32 bits; blockIdx.y has 16
+    if ((int64_t)r.heads * p->batch * p->tokens >= (int64_t)INT32_MAX || r.heads > 16384) return PLX_ERR_UNSUPPORTED;
+    if ((int64_t)p->batch * p->tokens >= (int64_t)INT32_MAX / 32) return PLX_ERR_UNSUPPORTED;
     if (r.w && (!p->norm || !aligned(r.w, 16))) return PLX_ERR_INVALID_ARG;
     if (!aligned(r.x, 16) || !strides_ok(r.x_stride, 3, elt)) return PLX_ERR_INVALID_ARG;
     if (grads == nullptr) {
@@ -59,11 +61,26 @@ plx_status validate_norm_rope(const plx_head_rows* rows, const plx_head_grads* g
   return PLX_OK;
 }
 
-constexpr int kNrBwdCtasPerSm = 2;
-
+// The backward's grid: one CTA per set at least.
 int norm_rope_bwd_ctas(int num_sms, int num_sets) {
-  const int n = num_sms * kNrBwdCtasPerSm / num_sets;
-  return n < 1 ? 1 : n;
+  const int n = num_sms * kNrBwdCtasPerSm;
+  return n < num_sets ? num_sets : n;
+}
+
+// Shares it out by the sets' numbers of heads (a set's rows are its work).
+void norm_rope_bwd_shares(NormRopeArgs* a, int ctas) {
+  long long heads = 0, before = 0;
+  for (int i = 0; i < a->sets; ++i) heads += a->set[i].heads;
+  int at = 0;
+  for (int i = 0; i < a->sets; ++i) {
+    before += a->set[i].heads;
+    int end = (int)(before * ctas / heads);
+    if (end < at + 1) end = at + 1;                                   // at least one for this set
+    if (end > ctas - (a->sets - 1 - i)) end = ctas - (a->sets - 1 - i);   // and for each after it
+    a->set[i].first_cta = at;
+    a->set[i].ctas = end - at;
+    at = end;
+  }
 }
 
 NormRopeArgs norm_rope_args(const plx_head_rows* rows, int32_t num_sets, const int32_t* positions, const float* cos,
@@ -81,8 +98,6 @@ NormRopeArgs norm_rope_args(const plx_head_rows* rows, int32_t num_sets, const i
   a.norm = p->norm;
   a.eps = p->eps;
   a.hpg = hpg;
-  // packed rows keep a token's heads together; [B, H, T, d] keeps a head's tokens together
-  a.head_inner = rows[0].x_stride[2] < rows[0].x_stride[1] ? 1 : 0;
   for (int i = 0; i < num_sets; ++i) {
     NormRopeSet& s = a.set[i];
     s.x = rows[i].x;
@@ -103,8 +118,8 @@ plx_status launch_norm_rope(const NormRopeArgs& a, cudaStream_t stream) {
   constexpr int per_cta = kNrThreads / NrLane<T, D, kInter>::LPR;
   long long chunks = 0;
   for (int i = 0; i < a.sets; ++i) chunks += a.set[i].chunks;
-  const long long groups = (long long)a.B * a.T * chunks;
-  return launch_pdl(norm_rope_kernel<T, D, kInter>, dim3((unsigned)((groups + per_cta - 1) / per_cta)),
+  const long long tokens = (long long)a.B * a.T;
+  return launch_pdl(norm_rope_kernel<T, D, kInter>, dim3((unsigned)((tokens + per_cta - 1) / per_cta), (unsigned)chunks),
                     dim3(kNrThreads), 0, stream, a) == cudaSuccess
              ? PLX_OK
              : PLX_ERR_CUDA;
@@ -112,13 +127,11 @@ plx_status launch_norm_rope(const NormRopeArgs& a, cudaStream_t stream) {
 
 template <typename T, int D, bool kInter>
 plx_status launch_norm_rope_bwd(const NormRopeArgs& a, int ctas, bool dw, cudaStream_t stream) {
-  if (launch_pdl(norm_rope_bwd_kernel<T, D, kInter>, dim3(ctas, a.sets), dim3(kNrThreads), 0, stream, a) !=
-      cudaSuccess)
+  if (launch_pdl(norm_rope_bwd_kernel<T, D, kInter>, dim3(ctas), dim3(kNrThreads), 0, stream, a) != cudaSuccess)
     return PLX_ERR_CUDA;
   if (!dw) return PLX_OK;
-  return launch_pdl(norm_rope_dw_kernel<D>, dim3(a.sets), dim3(kNrThreads), 0, stream, a, ctas) == cudaSuccess
-             ? PLX_OK
-             : PLX_ERR_CUDA;
+  return launch_pdl(norm_rope_dw_kernel<D>, dim3(a.sets), dim3(kNrThreads), 0, stream, a) == cudaSuccess ? PLX_OK
+                                                                                                       : PLX_ERR_CUDA;
 }
 
 // Heads that a group of lanes takes for one token: enough to have its cos and
@@ -141,7 +154,7 @@ plx_status validate_append(const plx_append_params* p) {
   if (p->dtype != PLX_F32 && p->dtype != PLX_BF16) return PLX_ERR_INVALID_ARG;
   if (p->head_dim != 64 && p->head_dim != 128) return PLX_ERR_UNSUPPORTED;
   if (p->page_size != kQ4Page) return PLX_ERR_UNSUPPORTED;
-  if ((int64_t)p->num_rows * p->num_kv_heads * 32 >= (int64_t)INT32_MAX * 128) return PLX_ERR_UNSUPPORTED;
+  if ((int64_t)p->num_rows * p->num_kv_heads >= (int64_t)INT32_MAX / 32) return PLX_ERR_UNSUPPORTED;   // threads in 32 bits
   const int elt = p->dtype == PLX_BF16 ? 2 : 4;
   if (!strides_ok(p->k_stride, 2, elt) || !strides_ok(p->v_stride, 2, elt)) return PLX_ERR_INVALID_ARG;
   return PLX_OK;
@@ -300,7 +313,7 @@ size_t parallax_norm_rope_backward_workspace_size(const plx_norm_rope_params* p,
   if (p->head_dim != 64 && p->head_dim != 128) return (size_t)-1;
   const int num_sms = current_device_sms();
   if (num_sms <= 0) return (size_t)-1;
-  return (size_t)num_sets * norm_rope_bwd_ctas(num_sms, num_sets) * p->head_dim * sizeof(float);
+  return (size_t)norm_rope_bwd_ctas(num_sms, num_sets) * p->head_dim * sizeof(float);
 }
 
 plx_status parallax_norm_rope_backward(const plx_head_rows* rows, const plx_head_grads* grads, int32_t num_sets,
@@ -316,11 +329,10 @@ plx_status parallax_norm_rope_backward(const plx_head_rows* rows, const plx_head
   if (num_sms <= 0) return PLX_ERR_CUDA;
   const int ctas = norm_rope_bwd_ctas(num_sms, num_sets);
   if (dw && (workspace == nullptr || !aligned(workspace, 16) ||
-             workspace_bytes < (size_t)num_sets * ctas * p->head_dim * sizeof(float)))
+             workspace_bytes < (size_t)ctas * p->head_dim * sizeof(float)))
     return PLX_ERR_WORKSPACE;
   NormRopeArgs a = norm_rope_args(rows, num_sets, positions, cos, sin, p, norm_rope_heads_per_group(rows, num_sets, p));
   a.partial = static_cast<float*>(workspace);
-  a.head_inner = grads[0].dy_stride[2] < grads[0].dy_stride[1] ? 1 : 0;
   for (int i = 0; i < num_sets; ++i) {
     NormRopeSet& s = a.set[i];
     s.dy = grads[i].dy;
@@ -331,6 +343,7 @@ plx_status parallax_norm_rope_backward(const plx_head_rows* rows, const plx_head
       s.ys[k] = grads[i].dx_stride[k];
     }
   }
+  norm_rope_bwd_shares(&a, ctas);
   const bool il = p->interleaved != 0;
   if (p->dtype == PLX_BF16) {
     if (p->head_dim == 64)
