@@ -23,6 +23,9 @@ namespace plx {
 constexpr int kNrThreads = 256;
 constexpr int kNrMaxSets = 3;
 constexpr int kNrBwdCtasPerSm = 3;
+constexpr int kNrBwdHeads = 4;                                    // rows of an item
+constexpr int kNrBwdSmem = 2 * kNrBwdHeads * 2 * kNrThreads * 16;  // two items' vectors
+constexpr int kNrDwThreads = 1024;
 
 struct NormRopeSet {
   const void* x;
@@ -45,6 +48,25 @@ struct NormRopeArgs {
   int sets, B, T, rot, max_pos, norm, hpg;
   float eps;
 };
+
+// Rows are read once and written once: neither way through L1, and out of L2
+// first (rope_prefill 147 to 133 us).
+__device__ __forceinline__ uint4 load_row(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
+__device__ __forceinline__ void store_row(void* p, const uint4& v) {
+  asm volatile("st.global.cs.v4.u32 [%0], {%1, %2, %3, %4};" ::"l"(p), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+// 16 bytes into shared memory as they arrive; zeros where !read.
+__device__ __forceinline__ void copy_row(uint32_t dst, const void* src, bool read) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(reinterpret_cast<uint64_t>(src)),
+               "r"(read ? 16 : 0)
+               : "memory");
+}
 
 // A lane's share of a row: E values from one 16-byte vector, in pairs (the
 // packed fp32 arithmetic takes two at an instruction).
@@ -208,7 +230,7 @@ __global__ void __launch_bounds__(kNrThreads) norm_rope_kernel(const NormRopeArg
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       v[u] = make_uint4(0, 0, 0, 0);
-      if (j + u < heads) v[u] = *reinterpret_cast<const uint4*>(x + (j + u) * set.xs[2]);
+      if (j + u < heads) v[u] = load_row(x + (j + u) * set.xs[2]);
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
@@ -224,7 +246,7 @@ __global__ void __launch_bounds__(kNrThreads) norm_rope_kernel(const NormRopeArg
       }
 #pragma unroll
       for (int i = 0; i < P; ++i) o[i] = mul2(fma2(f[i], wc[i], mul2(p[i], ws[i])), make_float2(r, r));
-      if (j + u < heads) *reinterpret_cast<uint4*>(y + (j + u) * set.ys[2]) = RowVec<T>::pack(o);
+      if (j + u < heads) store_row(y + (j + u) * set.ys[2], RowVec<T>::pack(o));
     }
   }
 }
@@ -251,65 +273,90 @@ __global__ void __launch_bounds__(kNrThreads, kNrBwdCtasPerSm) norm_rope_bwd_ker
   }
   const uint32_t groups = set.ctas * (kNrThreads / L::LPR), tokens = a.B * a.T, items = tokens * set.chunks;
   const uint32_t group = (blockIdx.x - set.first_cta) * (kNrThreads / L::LPR) + threadIdx.x / L::LPR;
-  // Every lane of a warp makes the same number of rounds: the sums' shuffles need all of them.
-  for (uint32_t base = 0; base < items; base += groups) {
-    const uint32_t item = base + group;
+
+  // An item is kNrBwdHeads heads of a token.  The next item's vectors come into
+  // this thread's own part of shared memory while it works on the current one
+  // (loading two rows at a time into registers left 24 warps waiting: 268
+  // against 231 us for rope_grad at its best chunk).
+  struct Item {
+    const T* x;
+    const T* dy;
+    T* dx;
+    int heads, pos;      // rows to write; position, or -1
+  };
+  auto decode = [&](uint32_t item) {
+    Item it;
     const bool in = item < items;
     const int chunk = in ? item / tokens : 0, tok = in ? item - chunk * tokens : 0;
-    const int b = a.B == 1 ? 0 : tok / a.T, t = tok - b * a.T, h0 = chunk * a.hpg;
-    const int pos = in ? nr_position(a, b, t) : -1;
-    const bool live = pos >= 0;
+    const int b = a.B == 1 ? 0 : tok / a.T, t = tok - b * a.T, h0 = chunk * kNrBwdHeads;
+    it.pos = in ? nr_position(a, b, t) : -1;
+    it.x = static_cast<const T*>(set.x) + b * set.xs[0] + t * set.xs[1] + h0 * set.xs[2] + ln.col0;
+    it.dy = static_cast<const T*>(set.dy) + b * set.ds[0] + t * set.ds[1] + h0 * set.ds[2] + ln.col0;
+    it.dx = static_cast<T*>(set.y) + b * set.ys[0] + t * set.ys[1] + h0 * set.ys[2] + ln.col0;
+    it.heads = in ? min(kNrBwdHeads, set.heads - h0) : 0;   // (padding rows of a token read nothing and write zeros)
+    return it;
+  };
+  extern __shared__ __align__(16) uint8_t nr_smem[];   // [2][kNrBwdHeads][x, dy][thread]
+  auto slot = [&](int buf, int j, int which) {
+    return nr_smem + (((buf * kNrBwdHeads + j) * 2 + which) * kNrThreads + threadIdx.x) * 16;
+  };
+  auto fetch = [&](const Item& it, int buf) {
+#pragma unroll
+    for (int j = 0; j < kNrBwdHeads; ++j) {
+      const bool read = it.pos >= 0 && j < it.heads;
+      copy_row(smem_u32(slot(buf, j, 0)), read && a.norm ? it.x + j * set.xs[2] : static_cast<const T*>(set.dy), read && a.norm);
+      copy_row(smem_u32(slot(buf, j, 1)), read ? it.dy + j * set.ds[2] : static_cast<const T*>(set.dy), read);
+    }
+  };
+  Item next = decode(group);
+  fetch(next, 0);
+  asm volatile("cp.async.commit_group;" ::: "memory");
+  int buf = 0;
+  // Every lane of a warp makes the same number of rounds: the sums' shuffles need all of them.
+  for (uint32_t base = 0; base < items; base += groups, buf ^= 1) {
+    const Item it = next;
+    if (base + groups < items) {
+      next = decode(base + groups + group);
+      fetch(next, buf ^ 1);
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
     Turn<P> tn;
-    load_turn<P, kInter>(a, live ? pos : 0, live ? ln.col0 : D, tn);
-    const T* x = static_cast<const T*>(set.x) + b * set.xs[0] + t * set.xs[1] + h0 * set.xs[2] + ln.col0;
-    const T* dy = static_cast<const T*>(set.dy) + b * set.ds[0] + t * set.ds[1] + h0 * set.ds[2] + ln.col0;
-    T* dx = static_cast<T*>(set.y) + b * set.ys[0] + t * set.ys[1] + h0 * set.ys[2] + ln.col0;
-    const int heads = in ? min(a.hpg, set.heads - h0) : 0;   // (padding rows of a live token read nothing and write zeros)
-    constexpr int U = 2;
-    for (int j = 0; j < a.hpg; j += U) {
-      uint4 vx[U], vd[U];
+    load_turn<P, kInter>(a, max(it.pos, 0), it.pos >= 0 ? ln.col0 : D, tn);
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        vx[u] = vd[u] = make_uint4(0, 0, 0, 0);
-        if (live && j + u < heads) {
-          if (a.norm) vx[u] = *reinterpret_cast<const uint4*>(x + (j + u) * set.xs[2]);
-          vd[u] = *reinterpret_cast<const uint4*>(dy + (j + u) * set.ds[2]);
-        }
+    for (int i = 0; i < P; ++i) tn.s[i] = make_float2(-tn.s[i].x, -tn.s[i].y);   // the transposed rotation
+    asm volatile("cp.async.wait_group 1;" ::: "memory");
+#pragma unroll
+    for (int j = 0; j < kNrBwdHeads; ++j) {
+      const uint4 vd = *reinterpret_cast<const uint4*>(slot(buf, j, 1));
+      float2 f[P], d[P], p[P], g[P];
+      RowVec<T>::unpack(*reinterpret_cast<const uint4*>(slot(buf, j, 0)), f);
+      RowVec<T>::unpack(vd, d);
+      ln.partner(vd, p);
+      float2 ss = make_float2(0.f, 0.f), gx = ss;
+#pragma unroll
+      for (int i = 0; i < P; ++i) {
+        d[i] = fma2(d[i], tn.c[i], mul2(p[i], tn.s[i]));   // dn
+        g[i] = mul2(d[i], w[i]);
+        const float2 fd = mul2(f[i], make_float2(1.f / D, 1.f / D));
+        ss = fma2(fd, f[i], ss);
+        gx = fma2(g[i], fd, gx);
       }
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        float2 f[P], d[P], p[P], g[P];
-        RowVec<T>::unpack(vx[u], f);
-        RowVec<T>::unpack(vd[u], d);
-        ln.partner(vd[u], p);
-        float2 ss = make_float2(0.f, 0.f), gx = ss;
+      if (a.norm) {
+        const float r = rsqrtf(row_sum<L::LPR>(ss.x + ss.y) + a.eps);
+        const float k = -r * r * row_sum<L::LPR>(gx.x + gx.y);
 #pragma unroll
         for (int i = 0; i < P; ++i) {
-          // dn: the transposed rotation
-          d[i] = fma2(d[i], tn.c[i], mul2(p[i], make_float2(-tn.s[i].x, -tn.s[i].y)));
-          g[i] = mul2(d[i], w[i]);
-          const float2 fd = mul2(f[i], make_float2(1.f / D, 1.f / D));
-          ss = fma2(fd, f[i], ss);
-          gx = fma2(g[i], fd, gx);
+          g[i] = mul2(fma2(f[i], make_float2(k, k), g[i]), make_float2(r, r));
+          acc[i] = fma2(d[i], mul2(f[i], make_float2(r, r)), acc[i]);
         }
-        if (a.norm) {
-          const float r = rsqrtf(row_sum<L::LPR>(ss.x + ss.y) + a.eps);
-          const float k = -r * r * row_sum<L::LPR>(gx.x + gx.y);
-#pragma unroll
-          for (int i = 0; i < P; ++i) {
-            g[i] = mul2(fma2(f[i], make_float2(k, k), g[i]), make_float2(r, r));
-            acc[i] = fma2(d[i], mul2(f[i], make_float2(r, r)), acc[i]);
-          }
-        } else {
-#pragma unroll
-          for (int i = 0; i < P; ++i) g[i] = d[i];
-        }
-        if (j + u < heads) *reinterpret_cast<uint4*>(dx + (j + u) * set.ys[2]) = RowVec<T>::pack(g);
       }
+      if (j < it.heads) store_row(it.dx + j * set.ys[2], RowVec<T>::pack(g));
     }
   }
   if (set.dw == nullptr) return;
-  __shared__ float part[kNrThreads / L::LPR][D];
+  float (*part)[D] = reinterpret_cast<float (*)[D]>(nr_smem);   // [kNrThreads / LPR][D]
+  static_assert(kNrThreads / L::LPR * D * 4 <= kNrBwdSmem, "the groups' sums fit");
+  __syncthreads();   // (each thread has read its own vectors)
 #pragma unroll
   for (int i = 0; i < P; ++i) *reinterpret_cast<float2*>(&part[threadIdx.x / L::LPR][ln.col0 + 2 * i]) = acc[i];
   __syncthreads();
@@ -323,13 +370,13 @@ __global__ void __launch_bounds__(kNrThreads, kNrBwdCtasPerSm) norm_rope_bwd_ker
 
 // dw of set blockIdx.x: the sum of its CTAs' partial rows, in a fixed order.
 template <int D>
-__global__ void __launch_bounds__(kNrThreads) norm_rope_dw_kernel(const NormRopeArgs a) {
+__global__ void __launch_bounds__(kNrDwThreads) norm_rope_dw_kernel(const NormRopeArgs a) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const NormRopeSet& set = a.set[blockIdx.x];
   float* dw = set.dw;
   if (dw == nullptr) return;
-  constexpr int kWays = kNrThreads / D;
+  constexpr int kWays = kNrDwThreads / D;
   __shared__ float part[kWays][D];
   const int d = threadIdx.x % D, way = threadIdx.x / D;
   const float* p = a.partial + (size_t)set.first_cta * D + d;

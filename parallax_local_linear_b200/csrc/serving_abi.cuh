@@ -127,10 +127,12 @@ plx_status launch_norm_rope(const NormRopeArgs& a, cudaStream_t stream) {
 
 template <typename T, int D, bool kInter>
 plx_status launch_norm_rope_bwd(const NormRopeArgs& a, int ctas, bool dw, cudaStream_t stream) {
-  if (launch_pdl(norm_rope_bwd_kernel<T, D, kInter>, dim3(ctas), dim3(kNrThreads), 0, stream, a) != cudaSuccess)
+  auto kern = norm_rope_bwd_kernel<T, D, kInter>;
+  if (set_smem(kern, kNrBwdSmem) != cudaSuccess ||
+      launch_pdl(kern, dim3(ctas), dim3(kNrThreads), kNrBwdSmem, stream, a) != cudaSuccess)
     return PLX_ERR_CUDA;
   if (!dw) return PLX_OK;
-  return launch_pdl(norm_rope_dw_kernel<D>, dim3(a.sets), dim3(kNrThreads), 0, stream, a) == cudaSuccess ? PLX_OK
+  return launch_pdl(norm_rope_dw_kernel<D>, dim3(a.sets), dim3(kNrDwThreads), 0, stream, a) == cudaSuccess ? PLX_OK
                                                                                                        : PLX_ERR_CUDA;
 }
 
@@ -142,7 +144,7 @@ int norm_rope_heads_per_group(const plx_head_rows* rows, int32_t num_sets, const
   for (int i = 0; i < num_sets; ++i) heads += rows[i].heads;
   const int sms = current_device_sms();
   const long long fill = (long long)(sms > 0 ? sms : 148) * 4 * kNrThreads / lanes;
-  int hpg = 8;
+  int hpg = 16;   // (128 us for rope_prefill; 133 with 8, 152 with 4, 192 with 2)
   while (hpg > 1 && (long long)p->batch * p->tokens * heads / hpg < fill) hpg /= 2;
   return hpg;
 }
@@ -331,7 +333,7 @@ plx_status parallax_norm_rope_backward(const plx_head_rows* rows, const plx_head
   if (dw && (workspace == nullptr || !aligned(workspace, 16) ||
              workspace_bytes < (size_t)ctas * p->head_dim * sizeof(float)))
     return PLX_ERR_WORKSPACE;
-  NormRopeArgs a = norm_rope_args(rows, num_sets, positions, cos, sin, p, norm_rope_heads_per_group(rows, num_sets, p));
+  NormRopeArgs a = norm_rope_args(rows, num_sets, positions, cos, sin, p, kNrBwdHeads);
   a.partial = static_cast<float*>(workspace);
   for (int i = 0; i < num_sets; ++i) {
     NormRopeSet& s = a.set[i];
