@@ -54,14 +54,15 @@ __device__ __forceinline__ void slot_of_row(const AppendArgs& a, int r, int& pag
 }
 
 // ---------------------------------------------------------------- plain pools
-// A vector per thread: N * Hkv rows of VPR 16-byte vectors, K and V together.
+// A vector per thread: row blockIdx.x.., head blockIdx.y, VPR 16-byte vectors of K
+// and of V.
 template <int VPR>
 __global__ void __launch_bounds__(kAppendThreads) cache_append_kernel(const AppendArgs a) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const uint32_t i = blockIdx.x * kAppendThreads + threadIdx.x, rh = i / VPR;
-  if (rh >= (uint32_t)a.N * a.Hkv) return;
-  const int vec = i % VPR, r = rh / (uint32_t)a.Hkv, h = rh - r * a.Hkv;
+  const uint32_t i = blockIdx.x * kAppendThreads + threadIdx.x;
+  const int vec = i % VPR, r = i / VPR, h = blockIdx.y;
+  if (r >= a.N) return;
   int page, row;
   slot_of_row(a, r, page, row);
   if (page < 0) return;
@@ -74,74 +75,88 @@ __global__ void __launch_bounds__(kAppendThreads) cache_append_kernel(const Appe
 }
 
 // ------------------------------------------------------------------- quantise
-// The format's own arithmetic for one value: fp32 difference and quotient,
-// rounded to nearest even.
-__device__ __forceinline__ uint32_t q4_code(float x, float lo, float s) {
-  return (uint32_t)fminf(rintf(__fdiv_rn(x - lo, s)), 15.f);
+// Minimum and maximum of three, NaN if one is.
+__device__ __forceinline__ float min3_nan(float a, float b, float c) {
+  float d;
+  asm("min.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
 }
-
-__device__ __forceinline__ __nv_bfloat162 as_bf162(uint32_t v) { return *reinterpret_cast<__nv_bfloat162*>(&v); }
-__device__ __forceinline__ uint32_t as_u32(__nv_bfloat162 v) { return *reinterpret_cast<uint32_t*>(&v); }
+__device__ __forceinline__ float max3_nan(float a, float b, float c) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
 
 // Codes of the lane's 8 columns and the parameter word of its group, which 8
 // neighbouring lanes share.  kKeys: code i at bits 16 (i % 2) + 4 (i / 2) (a K
 // word), otherwise at bits 4 i (two V half words).
 //
-// Minimum and maximum are taken on packed bf16 pairs, NaN winning, so a group
-// that is not finite ends up with a range that is not.  Quotients are products
-// with 1/s, off by less than 2^-18 here; only a lane that has one within 2^-15
-// of a border between two codes (or a scale so small that 1/s is not safe)
-// divides.  The same holds for range/15 and the border between two bf16
-// values.  Dividing throughout took 764 instructions a vector pair, this
-// takes 280.
+// NaN wins the minimum and the maximum, so a group that is not finite ends up
+// with a range that is not.  The format's quotients are fp32 quotients rounded
+// to nearest; here each is a product with the rounded reciprocal and one
+// correction by its exact remainder, which gives the same number (Markstein,
+// "Computation of elementary functions on the IBM RISC System/6000", 1990: with
+// y = 1/b rounded to nearest, q = a y, r = a - q b, q + r y is a / b rounded to
+// nearest; a reciprocal within one ulp is brought there by one Newton step
+// unless b's significand is all ones, and a bf16's is not).  So a quotient that
+// lies exactly between two codes, which bf16 rows have in one group of eight,
+// rounds as it should.  Where the scale is below 2^-100 and the remainders could
+// leave fp32's range, the lane divides.  Dividing throughout took 764
+// instructions a pair of vectors; deciding the ties by their remainders
+// afterwards 359, this takes 235.
 template <bool kKeys>
 __device__ __forceinline__ void quantise8(const uint4& vec, uint32_t& codes, uint32_t& param) {
   const uint32_t w[4] = {vec.x, vec.y, vec.z, vec.w};
-  __nv_bfloat162 mn = __hmin2_nan(__hmin2_nan(as_bf162(w[0]), as_bf162(w[1])), __hmin2_nan(as_bf162(w[2]), as_bf162(w[3])));
-  __nv_bfloat162 mx = __hmax2_nan(__hmax2_nan(as_bf162(w[0]), as_bf162(w[1])), __hmax2_nan(as_bf162(w[2]), as_bf162(w[3])));
+  float2 x[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) x[i] = make_float2(bf16_lo_f(w[i]), bf16_hi_f(w[i]));
+  float lo = min3_nan(min3_nan(x[0].x, x[0].y, x[1].x), min3_nan(x[1].y, x[2].x, x[2].y), min3_nan(x[3].x, x[3].y, x[3].y));
+  float hi = max3_nan(max3_nan(x[0].x, x[0].y, x[1].x), max3_nan(x[1].y, x[2].x, x[2].y), max3_nan(x[3].x, x[3].y, x[3].y));
 #pragma unroll
   for (int o = 1; o < 8; o <<= 1) {
-    mn = __hmin2_nan(mn, as_bf162(__shfl_xor_sync(0xffffffffu, as_u32(mn), o)));
-    mx = __hmax2_nan(mx, as_bf162(__shfl_xor_sync(0xffffffffu, as_u32(mx), o)));
+    lo = min3_nan(lo, lo, __shfl_xor_sync(0xffffffffu, lo, o));
+    hi = max3_nan(hi, hi, __shfl_xor_sync(0xffffffffu, hi, o));
   }
-  mn = __hmin2_nan(mn, __lowhigh2highlow(mn));
-  mx = __hmax2_nan(mx, __lowhigh2highlow(mx));
-  const float lo = bf16_hi_f(as_u32(mn)), range = bf16_hi_f(as_u32(mx)) - lo;
+  const float range = hi - lo;
   // A group that cannot be held reads back NaN: scale 0, minimum NaN.
   const bool finite = range < INFINITY;
-  float ratio = range * (1.f / 15.f);
-  if (((__float_as_uint(ratio) + 0x8004u) & 0xffffu) < 8u || ratio < 0x1p-100f) ratio = __fdiv_rn(range, 15.f);
+  constexpr float k15th = 1.f / 15.f;
+  float ratio = range * k15th;
+  ratio = fmaf(fmaf(-ratio, 15.f, range), k15th, ratio);
+  if (ratio < 0x1p-100f) ratio = __fdiv_rn(range, 15.f);
   const uint32_t s16 = pack_bf16(ratio, 0.f) & 0xffffu;
   const float s = __uint_as_float(s16 << 16);
   param = finite ? s16 | (__float_as_uint(lo) & 0xffff0000u) : 0x7fc00000u;
-  const float inv = __frcp_rn(s);
-  // q + 1.5 2^23 holds round(q) in its low bits; the words' sum takes the
-  // constant's own bits out again.
+  float inv;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));
+  inv = fmaf(fmaf(-s, inv, 1.f), inv, inv);
+  // q + 1.5 2^23 holds round(q) in its low bits (ties to even); the constant's own
+  // bits, as far as the shifts leave them in a word, are taken out at the end.
   constexpr uint32_t kMagicBits = 0x4b400000u;
-  const float2 lo2 = make_float2(-lo, -lo), inv2 = make_float2(inv, inv);
-  const float2 magic = make_float2(12582912.f, 12582912.f), unmagic = make_float2(-12582912.f, -12582912.f);
+  constexpr uint32_t kMagicSum = kMagicBits + (kMagicBits << 4) + (kMagicBits << 8) + (kMagicBits << 12) +
+                                 (kMagicBits << 16) + (kMagicBits << 20) + (kMagicBits << 24) + (kMagicBits << 28);
+  const float2 lo2 = make_float2(-lo, -lo), inv2 = make_float2(inv, inv), s2 = make_float2(-s, -s);
+  const float2 magic = make_float2(12582912.f, 12582912.f);
   uint32_t sum = 0;
-  float far = 0.f;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const float2 q = mul2(add2(make_float2(bf16_lo_f(w[i]), bf16_hi_f(w[i])), lo2), inv2);
-    const float2 t = add2(q, magic);
-    const float2 n = add2(t, unmagic);
-    far = fmaxf(far, fmaxf(fabsf(q.x - n.x), fabsf(q.y - n.y)));
+    x[i] = add2(x[i], lo2);
+    const float2 q = mul2(x[i], inv2);
+    const float2 t = add2(fma2(fma2(q, s2, x[i]), inv2, q), magic);
     const int p0 = kKeys ? 4 * i : 8 * i, p1 = kKeys ? 16 + 4 * i : 8 * i + 4;
-    sum += ((__float_as_uint(t.x) - kMagicBits) << p0) + ((__float_as_uint(t.y) - kMagicBits) << p1);
+    sum += (__float_as_uint(t.x) << p0) + (__float_as_uint(t.y) << p1);
   }
-  if (!(far < 0.5f - 0x1p-15f) || s < 0x1p-100f || !finite) {
-    sum = 0;
-    if (s > 0.f && finite) {
+  codes = sum - kMagicSum;
+  if (!finite || s < 0x1p-100f) {
+    codes = 0;
+    if (finite && s > 0.f) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int p0 = kKeys ? 4 * i : 8 * i, p1 = kKeys ? 16 + 4 * i : 8 * i + 4;
-        sum |= q4_code(bf16_lo_f(w[i]), lo, s) << p0 | q4_code(bf16_hi_f(w[i]), lo, s) << p1;
+      for (int k = 0; k < 8; ++k) {
+        const float q = __fdiv_rn(k & 1 ? x[k / 2].y : x[k / 2].x, s);
+        codes |= (uint32_t)fminf(rintf(q), 15.f) << (kKeys ? 4 * (k / 2) + 16 * (k & 1) : 4 * k);
       }
     }
   }
-  codes = sum;
 }
 
 template <int D>
@@ -150,10 +165,9 @@ __global__ void __launch_bounds__(kAppendThreads) cache_append_q4_kernel(const A
   constexpr int LPR = D / 8;   // lanes of a row
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const uint32_t i = blockIdx.x * kAppendThreads + threadIdx.x, rh = i / LPR;
-  const int l = i % LPR;
-  const bool in = rh < (uint32_t)a.N * a.Hkv;
-  const int r = rh / (uint32_t)a.Hkv, h = rh - r * a.Hkv;
+  const uint32_t i = blockIdx.x * kAppendThreads + threadIdx.x;
+  const int l = i % LPR, r = i / LPR, h = blockIdx.y;
+  const bool in = r < a.N;
   uint4 kv = make_uint4(0, 0, 0, 0), vv = kv;
   if (in) {   // beside the slot's load
     kv = __ldg(static_cast<const uint4*>(a.k) + r * a.ks[0] + h * a.ks[1] + l);
@@ -184,7 +198,12 @@ __global__ void __launch_bounds__(kAppendThreads) cache_append_q4_kernel(const A
 // row of results is written without gaps (with eight, an fp32 row is written
 // 16 bytes of every 32 at a time: 38 against 24 us for 134 MB), and kGatherRows
 // rows, so that their loads overlap.
-constexpr int kGatherRows = 4;
+constexpr int kGatherRows = 2;
+
+// The low 4 bits as a number, without a conversion (a quarter-rate instruction).
+__device__ __forceinline__ float code_value(uint32_t bits) {
+  return __uint_as_float((bits & 15u) | 0x4b000000u) - 8388608.f;
+}
 
 template <int D, bool kBf16>
 __global__ void __launch_bounds__(kAppendThreads) cache_gather_q4_kernel(const AppendArgs a) {
@@ -193,17 +212,15 @@ __global__ void __launch_bounds__(kAppendThreads) cache_gather_q4_kernel(const A
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int l = threadIdx.x % LPR;
-  const uint32_t first = blockIdx.x * (RPC * kGatherRows) + threadIdx.x / LPR;
+  const int first = blockIdx.x * (RPC * kGatherRows) + threadIdx.x / LPR, h = blockIdx.y;
   const uint8_t* block[kGatherRows];
-  int r[kGatherRows], h[kGatherRows], row[kGatherRows];
+  int row[kGatherRows];
 #pragma unroll
   for (int u = 0; u < kGatherRows; ++u) {
-    const uint32_t rh = first + u * RPC;
+    const int r = first + u * RPC;
     int page = -1;
-    r[u] = rh / (uint32_t)a.Hkv;
-    h[u] = rh - r[u] * a.Hkv;
-    if (rh < (uint32_t)a.N * a.Hkv) slot_of_row(a, r[u], page, row[u]);
-    block[u] = page < 0 ? nullptr : a.cache + ((size_t)page * a.Hkv + h[u]) * B::kBytes;
+    if (r < a.N) slot_of_row(a, r, page, row[u]);
+    block[u] = page < 0 ? nullptr : a.cache + ((size_t)page * a.Hkv + h) * B::kBytes;
   }
   // columns 4 l .. 4 l + 3: a half of K's word l / 2 (columns 8 (l / 2) ..), and
   // a half word of V's
@@ -224,18 +241,18 @@ __global__ void __launch_bounds__(kAppendThreads) cache_gather_q4_kernel(const A
     float kx[4], vx[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      kx[e] = fmaf(bf16_lo_f(kp[u]), (float)((kc[u] >> (16 * (e & 1) + 4 * (e >> 1))) & 15u), bf16_hi_f(kp[u]));
-      vx[e] = fmaf(bf16_lo_f(vp[u]), (float)((vc[u] >> (4 * e)) & 15u), bf16_hi_f(vp[u]));
+      kx[e] = fmaf(bf16_lo_f(kp[u]), code_value(kc[u] >> (16 * (e & 1) + 4 * (e >> 1))), bf16_hi_f(kp[u]));
+      vx[e] = fmaf(bf16_lo_f(vp[u]), code_value(vc[u] >> (4 * e)), bf16_hi_f(vp[u]));
     }
     // strides in 16-byte vectors
-    uint4* ko = static_cast<uint4*>(a.k_out) + r[u] * a.ks[0] + h[u] * a.ks[1];
-    uint4* vo = static_cast<uint4*>(a.v_out) + r[u] * a.vs[0] + h[u] * a.vs[1];
+    uint4* ko = static_cast<uint4*>(a.k_out) + (first + u * RPC) * a.ks[0] + h * a.ks[1];
+    uint4* vo = static_cast<uint4*>(a.v_out) + (first + u * RPC) * a.vs[0] + h * a.vs[1];
     if (kBf16) {
-      reinterpret_cast<uint2*>(ko)[l] = make_uint2(pack_bf16(kx[0], kx[1]), pack_bf16(kx[2], kx[3]));
-      reinterpret_cast<uint2*>(vo)[l] = make_uint2(pack_bf16(vx[0], vx[1]), pack_bf16(vx[2], vx[3]));
+      __stcs(reinterpret_cast<uint2*>(ko) + l, make_uint2(pack_bf16(kx[0], kx[1]), pack_bf16(kx[2], kx[3])));
+      __stcs(reinterpret_cast<uint2*>(vo) + l, make_uint2(pack_bf16(vx[0], vx[1]), pack_bf16(vx[2], vx[3])));
     } else {
-      reinterpret_cast<float4*>(ko)[l] = make_float4(kx[0], kx[1], kx[2], kx[3]);
-      reinterpret_cast<float4*>(vo)[l] = make_float4(vx[0], vx[1], vx[2], vx[3]);
+      __stcs(reinterpret_cast<float4*>(ko) + l, make_float4(kx[0], kx[1], kx[2], kx[3]));
+      __stcs(reinterpret_cast<float4*>(vo) + l, make_float4(vx[0], vx[1], vx[2], vx[3]));
     }
   }
 }

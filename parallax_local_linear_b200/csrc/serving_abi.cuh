@@ -156,7 +156,7 @@ plx_status validate_append(const plx_append_params* p) {
   if (p->dtype != PLX_F32 && p->dtype != PLX_BF16) return PLX_ERR_INVALID_ARG;
   if (p->head_dim != 64 && p->head_dim != 128) return PLX_ERR_UNSUPPORTED;
   if (p->page_size != kQ4Page) return PLX_ERR_UNSUPPORTED;
-  if ((int64_t)p->num_rows * p->num_kv_heads >= (int64_t)INT32_MAX / 32) return PLX_ERR_UNSUPPORTED;   // threads in 32 bits
+  if (p->num_rows >= INT32_MAX / 32 || p->num_kv_heads > 65535) return PLX_ERR_UNSUPPORTED;   // the grid's limits
   const int elt = p->dtype == PLX_BF16 ? 2 : 4;
   if (!strides_ok(p->k_stride, 2, elt) || !strides_ok(p->v_stride, 2, elt)) return PLX_ERR_INVALID_ARG;
   return PLX_OK;
@@ -176,14 +176,12 @@ AppendArgs append_args(const int64_t* slots, const plx_append_params* p) {
   return a;
 }
 
-// `lanes` threads for each (row, KV head), or for `rows` of them.
+// `lanes` threads for `rows` rows of one KV head (blockIdx.y).
 template <typename Kernel>
 plx_status launch_rows(Kernel kern, const AppendArgs& a, int lanes, cudaStream_t stream, int rows = 1) {
-  const long long per_cta = kAppendThreads / lanes * rows;
-  const long long ctas = ((long long)a.N * a.Hkv + per_cta - 1) / per_cta;
-  return launch_pdl(kern, dim3((unsigned)ctas), dim3(kAppendThreads), 0, stream, a) == cudaSuccess
-             ? PLX_OK
-             : PLX_ERR_CUDA;
+  const int per_cta = kAppendThreads / lanes * rows;
+  const dim3 grid((unsigned)((a.N + per_cta - 1) / per_cta), (unsigned)a.Hkv);
+  return launch_pdl(kern, grid, dim3(kAppendThreads), 0, stream, a) == cudaSuccess ? PLX_OK : PLX_ERR_CUDA;
 }
 
 // -------------------------------------------------------------- 4-bit decode

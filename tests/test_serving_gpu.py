@@ -460,6 +460,23 @@ def test_cache_append_q4_borders(px):
     _check_q4(px, x.bfloat16(), x.bfloat16(), torch.arange(2, device="cuda"), 1)
 
 
+@pytest.mark.parametrize("seed", range(4))
+def test_cache_append_q4_codes_are_the_quotients(px, seed):
+    # many groups of every size of value: each code is the fp32 quotient rounded to nearest even
+    g = torch.Generator(device="cuda")
+    g.manual_seed(100 + seed)
+    N, Hkv, d = 640, 4, 128
+    size = torch.exp2(torch.randint(-110, 110, (N, Hkv, 1), device="cuda", generator=g).float())
+    k = (size * torch.randn(N, Hkv, d, device="cuda", generator=g)).bfloat16()
+    # few significant bits: quotients on and next to the borders
+    v = (torch.randint(-200, 200, (N, Hkv, d), device="cuda", generator=g) * 2.0 ** (seed - 2)).bfloat16()
+    cache, _, _ = _check_q4(px, k, v, torch.arange(N, device="cuda"), 10)
+    kq, vq = px.cache_gather_q4(cache, torch.arange(N, device="cuda"), out_dtype=torch.float32)
+    for got, x in ((kq, k), (vq, v)):
+        want = S.q4_values(*S.q4_quantise(x.float().cpu().numpy()))
+        _within(got, want, U * np.abs(want) + 2.0 ** -149, "values")
+
+
 def test_cache_rows_take_slices_and_report_bad_slots(px):
     N, Hkv, d = 9, 2, 128
     x = torch.randn(N, 6 * Hkv * d, device="cuda").bfloat16()
