@@ -1077,15 +1077,18 @@ _q4_workspaces = {}
 
 
 def _q4_workspace(index, nbytes, units):
-    """The 4-bit decode's workspace: one per device and stream, since calls on
-    different streams may overlap.  Partials are at its front and the counters
-    (4 bytes a unit) at its end; it is large enough for the most of either that
-    a call has needed, so that one call's partials never reach another's
-    counters, and zeroed when allocated.  A captured graph gets one of its own
-    (zeroed in the graph), so that graphs replayed at once do not share it."""
-    if torch.cuda.is_current_stream_capturing():
-        return torch.zeros(nbytes, dtype=torch.uint8, device=index)
+    """The 4-bit decode's workspace where the caller gives none: one per device
+    and stream, since calls on different streams may overlap.  Partials are at
+    its front and the counters (4 bytes a unit) at its end; it is large enough
+    for the most of either that a call has needed, so that one call's partials
+    never reach another's counters, and zeroed when allocated.  A captured graph
+    gets one of its own, whose counters it clears, so that graphs replayed at
+    once do not share it."""
     counters = (4 * units + 255) & ~255
+    if torch.cuda.is_current_stream_capturing():
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=index)
+        ws[-counters:].zero_()
+        return ws
     key = (index, _raw_stream(index))
     with _ws_lock:
         ws, most_slots, most_counters = _q4_workspaces.get(key, (None, 1 << 20, 1 << 14))
@@ -1096,15 +1099,34 @@ def _q4_workspace(index, nbytes, units):
         return ws
 
 
+def decode_q4_workspace(q, kv_cache, *, page_table=None, kv_len=None, num_ctas=0):
+    """A zeroed workspace for decode_q4 calls of these shapes (pass it as
+    ``workspace``): for a captured graph, which otherwise clears counters at each
+    replay.  Calls that share one must not overlap on the GPU."""
+    B, Hkv = q.shape[0], kv_cache.shape[1]
+    if kv_len is None:
+        kv_len = PAGE_SIZE * (kv_cache.shape[2] if page_table is None else page_table.shape[1])
+    paged = page_table is not None
+    p = _DECODE.pack(B, q.shape[1], Hkv, q.shape[2], int(kv_len), PAGE_SIZE if paged else 0,
+                     kv_cache.shape[0] if paged else 0, page_table.shape[1] if paged else 0, PLX_BF16, PLX_BF16, 1.0,
+                     int(num_ctas))
+    with _device_guard(_cuda_index("q", q)):
+        nbytes = lib.parallax_decode_q4_workspace_size(p, 0)
+    if nbytes == SIZE_MAX:
+        raise ParallaxError(1, "parallax_decode_q4_workspace_size")
+    return torch.zeros(nbytes, dtype=torch.uint8, device=q.device)
+
+
 def decode_q4(q, rho, kv_cache, scale=None, *, seq_lens=None, page_table=None, out=None, out_dtype=None, num_ctas=0,
-              kv_len=None):
+              kv_len=None, workspace=None):
     """Parallax decode over the 4-bit cache.
 
     q, rho: [B, Hq, d] bfloat16.  Paged: kv_cache uint8 [P, Hkv, block bytes],
     page_table int32 [B, max_pages] and seq_lens int32 [B].  Contiguous:
     kv_cache [B, Hkv, ceil(kv_len / 64), block bytes] with ``kv_len`` (default:
     all of its pages' tokens) and optional seq_lens.  Returns out [B, Hq, d] in
-    ``out_dtype`` (default bfloat16).
+    ``out_dtype`` (default bfloat16).  ``workspace``: see decode_q4_workspace
+    (default: one that the binding keeps for the stream).
     """
     if q.dim() != 3 or tuple(rho.shape) != tuple(q.shape):
         raise ValueError(f"q and rho must be [B, Hq, d] and alike, got {tuple(q.shape)} and {tuple(rho.shape)}")
@@ -1153,10 +1175,15 @@ def decode_q4(q, rho, kv_cache, scale=None, *, seq_lens=None, page_table=None, o
                      page_table.shape[1] if paged else 0, PLX_BF16, _dtype_code(out_dtype),
                      (1.0 / d ** 0.5) if scale is None else float(scale), int(num_ctas))
     with _device_guard(index):
-        nbytes = lib.parallax_decode_q4_workspace_size(p, 0)
-        if nbytes == SIZE_MAX:
-            raise ParallaxError(1, "parallax_decode_q4_workspace_size")
-        ws = _q4_workspace(index, nbytes, B * Hkv)
+        if workspace is not None:
+            _on(index, "workspace", workspace, torch.uint8)
+            _check_shape("workspace", workspace, (workspace.numel(),))
+            ws = workspace
+        else:
+            nbytes = lib.parallax_decode_q4_workspace_size(p, 0)
+            if nbytes == SIZE_MAX:
+                raise ParallaxError(1, "parallax_decode_q4_workspace_size")
+            ws = _q4_workspace(index, nbytes, B * Hkv)
         st = lib.parallax_decode_q4(q.data_ptr(), rho.data_ptr(), kv_cache.data_ptr(), _raw(page_table),
                                     _raw(seq_lens), out.data_ptr(), ws.data_ptr(), ws.numel(), p, _raw_stream(index))
     if st != 0:

@@ -256,6 +256,28 @@ def test_streams_and_graphs(px):
     assert px.last_device_error() == 0
 
 
+def test_given_workspace(px):
+    # one workspace in a captured graph and in direct calls; too small or misplaced ones are refused
+    x = _inputs([3000, 17, 900], 4, 2, 128, seed=30)
+    want = _run(px, x, None)
+    ws = px.decode_q4_workspace(x["q"], x["cache"], page_table=x["table"], kv_len=x["kv_len"])
+    assert torch.equal(_run(px, x, None, workspace=ws), want)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = _run(px, x, None, workspace=ws)
+    for _ in range(3):
+        out.zero_()
+        g.replay()
+        assert torch.equal(out, want)
+    assert torch.equal(_run(px, x, None, workspace=ws), want)
+    for bad in (ws[:-256], ws[256:]):
+        with pytest.raises(px.ParallaxError):
+            _run(px, x, None, workspace=bad)
+    with pytest.raises(TypeError):
+        _run(px, x, None, workspace=ws.view(torch.int32))
+
+
 def test_serving_step(px):
     """Lengths to output: page plan, norm with rotation, 4-bit append, 4-bit decode, over several steps."""
     torch.manual_seed(20)
