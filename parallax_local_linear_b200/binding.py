@@ -770,8 +770,10 @@ def page_plan(cached_lens, new_lens, page_table, free_pages, *, num_rows, num_pa
     if free_head is not None:
         _on(index, "free_head", free_head, i32)
     num_rows = int(num_rows)
-    slots = torch.empty(num_rows, dtype=torch.int64, device=cached_lens.device)
-    seq_lens, cu, positions, used = cached_lens.new_empty(num_rows + 2 * B + 2).split((B, B + 1, num_rows, 1))
+    # one allocation, the slots (8-byte entries) first
+    slots, seq_lens, cu, positions, used = cached_lens.new_empty(3 * num_rows + 2 * B + 2).split_with_sizes(
+        (2 * num_rows, B, B + 1, num_rows, 1))
+    slots = slots.view(torch.int64)
     with _device_guard(index):
         st = lib.parallax_page_plan(cached_lens.data_ptr(), new_lens.data_ptr(), page_table.data_ptr(),
                                     free_pages.data_ptr(), _raw(free_head), seq_lens.data_ptr(), cu.data_ptr(),
@@ -791,56 +793,57 @@ def _head_strides(name, t, batched):
     return (s[0], s[2], s[1]) if batched else (0, s[0], s[1])
 
 
-def _head_like(x):
-    return torch.empty_like(x, memory_format=torch.contiguous_format)
-
-
 def _norm_rope_call(q, rho, k, cos, sin, positions, weights, eps, norm, interleaved):
     """Checks and parameters that the two directions share: (sets, params, device index,
     batched), a set being (name, x, weight)."""
-    batched = q.dim() == 4
-    if q.dim() not in (3, 4):
-        raise ValueError(f"q must be [B, H, T, d] or packed [N, H, d], got {tuple(q.shape)}")
-    if rho is not None and rho.shape != q.shape:
-        raise ValueError(f"rho must have q's shape {tuple(q.shape)}, got {tuple(rho.shape)}")
-    d = q.shape[-1]
-    B, T = (q.shape[0], q.shape[2]) if batched else (1, q.shape[0])
-    if k is not None and (k.dim() != q.dim() or k.shape[-1] != d or k.shape[0] != q.shape[0]
-                          or (batched and k.shape[2] != T)):
-        raise ValueError(f"k's rows {tuple(k.shape)} do not match q's {tuple(q.shape)}")
-    if (cos is None) != (sin is None):
-        raise ValueError("cos and sin come together")
-    rot, max_pos = 0, 0
-    if cos is not None:
-        if cos.dim() != 2 or cos.shape != sin.shape:
-            raise ValueError("cos and sin must be [max_pos, rot_dim / 2] and alike")
-        if not (cos.is_contiguous() and sin.is_contiguous()):
-            raise ValueError("cos and sin must be contiguous")
-        max_pos, rot = cos.shape[0], 2 * cos.shape[1]
-    pos_stride = 0
-    if positions is not None:
-        shapes = ((T,), (B, T)) if batched else ((T,),)
-        if tuple(positions.shape) not in shapes:
-            raise ValueError(f"positions must have shape {' or '.join(map(str, shapes))}, got {tuple(positions.shape)}")
-        if not positions.is_contiguous():
-            raise ValueError("positions must be contiguous")
-        pos_stride = T if positions.dim() == 2 else 0
-    elif rot and T > max_pos:
-        raise ValueError(f"{T} tokens need as many rows of cos and sin, got {max_pos}")
+    shape = q.shape
+    batched = len(shape) == 4
+    if not batched and len(shape) != 3:
+        raise ValueError(f"q must be [B, H, T, d] or packed [N, H, d], got {tuple(shape)}")
+    d = shape[-1]
+    B, T = (shape[0], shape[2]) if batched else (1, shape[0])
     index, dtype = _cuda_index("q", q), q.dtype
-    sets = [s for s in zip(("q", "rho", "k"), (q, rho, k), weights) if s[1] is not None]
-    for name, x, w in sets:
-        _on(index, name, x, dtype)
+    sets = [("q", q, weights[0])]
+    if rho is not None:
+        if rho.shape != shape:
+            raise ValueError(f"rho must have q's shape {tuple(shape)}, got {tuple(rho.shape)}")
+        _on(index, "rho", rho, dtype)
+        sets.append(("rho", rho, weights[1]))
+    if k is not None:
+        ks = k.shape
+        if len(ks) != len(shape) or ks[-1] != d or ks[0] != shape[0] or (batched and ks[2] != T):
+            raise ValueError(f"k's rows {tuple(ks)} do not match q's {tuple(shape)}")
+        _on(index, "k", k, dtype)
+        sets.append(("k", k, weights[2]))
+    for name, _, w in sets:
         if w is not None:
             if not norm:
                 raise ValueError(f"{name}_weight needs norm=True")
             _check_shape(name + "_weight", w, (d,))
             _on(index, name + "_weight", w, dtype)
-    if cos is not None:
+    rot, max_pos = 0, 0
+    if cos is not None and sin is not None:
+        if cos.dim() != 2 or cos.shape != sin.shape:
+            raise ValueError("cos and sin must be [max_pos, rot_dim / 2] and alike")
+        if not (cos.is_contiguous() and sin.is_contiguous()):
+            raise ValueError("cos and sin must be contiguous")
+        max_pos, rot = cos.shape
+        rot *= 2
         _on(index, "cos", cos, torch.float32)
         _on(index, "sin", sin, torch.float32)
+    elif cos is not None or sin is not None:
+        raise ValueError("cos and sin come together")
+    pos_stride = 0
     if positions is not None:
+        ps = positions.shape
+        if ps != (T,) and not (batched and ps == (B, T)):
+            raise ValueError(f"positions must have shape {(T,)}{f' or {(B, T)}' if batched else ''}, got {tuple(ps)}")
+        if not positions.is_contiguous():
+            raise ValueError("positions must be contiguous")
         _on(index, "positions", positions, torch.int32)
+        pos_stride = T if len(ps) == 2 else 0
+    elif rot and T > max_pos:
+        raise ValueError(f"{T} tokens need as many rows of cos and sin, got {max_pos}")
     p = _NORM_ROPE.pack(B, T, d, rot, max_pos, 1 if interleaved else 0, 1 if norm else 0, _dtype_code(dtype), eps,
                         pos_stride)
     return sets, p, index, batched
@@ -868,15 +871,15 @@ def norm_rope(q, rho, k, cos, sin, positions=None, *, q_weight=None, rho_weight=
     for name, x, w in sets:
         strides = _head_strides(name, x, batched)
         if given is None:
-            y = _head_like(x)
+            y = torch.empty_like(x, memory_format=torch.contiguous_format)
         else:
             y = given.get(name)
             if y is None or y.shape != x.shape:
                 raise ValueError(f"out's {name} must have shape {tuple(x.shape)}")
             _on(index, "out's " + name, y, x.dtype)
         done[name] = y
-        rows += _HEAD_ROWS.pack(x.data_ptr(), y.data_ptr(), _raw0(w), x.shape[1], *strides,
-                                *_head_strides("out's " + name, y, batched))
+        rows += _HEAD_ROWS.pack(x.data_ptr(), y.data_ptr(), 0 if w is None else w.data_ptr(), x.shape[1], *strides,
+                                *_head_strides("out's", y, batched))
     with _device_guard(index):
         st = lib.parallax_norm_rope(rows, len(sets), _raw(positions), _raw(cos), _raw(sin), p, _raw_stream(index))
     if st != 0:
@@ -904,7 +907,7 @@ def norm_rope_backward(dq, drho, dk, q, rho, k, cos, sin, positions=None, *, q_w
         if dy is None or dy.shape != x.shape:
             raise ValueError(f"d{name} must have shape {tuple(x.shape)}")
         _on(index, "d" + name, dy, x.dtype)
-        dx = dxs[name] = _head_like(x)
+        dx = dxs[name] = torch.empty_like(x, memory_format=torch.contiguous_format)
         if norm:
             dws[name] = torch.empty(x.shape[-1], dtype=torch.float32, device=x.device)
         rows += _HEAD_ROWS.pack(x.data_ptr(), 0, _raw0(w), x.shape[1], *_head_strides(name, x, batched), *no_strides)
@@ -1169,8 +1172,11 @@ def decode_q4(q, rho, kv_cache, scale=None, *, seq_lens=None, page_table=None, o
         _on(index, "page_table", page_table, torch.int32)
     if seq_lens is not None:
         _on(index, "seq_lens", seq_lens, torch.int32)
-    out, out_dtype = _output(out, out_dtype, q.shape, torch.bfloat16, q.device)
-    _on(index, "out", out)
+    if out is None and (out_dtype is None or out_dtype is torch.bfloat16):
+        out, out_dtype = torch.empty_like(q), torch.bfloat16
+    else:
+        out, out_dtype = _output(out, out_dtype, q.shape, torch.bfloat16, q.device)
+        _on(index, "out", out)
     p = _DECODE.pack(B, Hq, Hkv, d, kv_len, PAGE_SIZE if paged else 0, kv_cache.shape[0] if paged else 0,
                      page_table.shape[1] if paged else 0, PLX_BF16, _dtype_code(out_dtype),
                      (1.0 / d ** 0.5) if scale is None else float(scale), int(num_ctas))

@@ -3,9 +3,24 @@
 // parallax.cu after its host helpers.
 #pragma once
 
+#include <atomic>
+
 namespace {
 
 using namespace plx;
+
+// Raises a kernel's dynamic shared-memory limit to `bytes`, once per device
+// (every call of the kernel asks for as much: 2 us of host time otherwise).
+template <auto kKernel>
+cudaError_t set_smem_once(int bytes) {
+  static std::atomic<bool> done[kMaxDevices];
+  int dev = 0;
+  if (note(cudaGetDevice(&dev)) != cudaSuccess) return cudaErrorInvalidDevice;
+  if (dev >= 0 && dev < kMaxDevices && done[dev].load(std::memory_order_acquire)) return cudaSuccess;
+  const cudaError_t e = set_smem(kKernel, bytes);
+  if (e == cudaSuccess && dev >= 0 && dev < kMaxDevices) done[dev].store(true, std::memory_order_release);
+  return e;
+}
 
 // -------------------------------------------------------------- page plan
 plx_status validate_page_plan(const plx_page_plan_params* p) {
@@ -127,9 +142,8 @@ plx_status launch_norm_rope(const NormRopeArgs& a, cudaStream_t stream) {
 
 template <typename T, int D, bool kInter>
 plx_status launch_norm_rope_bwd(const NormRopeArgs& a, int ctas, bool dw, cudaStream_t stream) {
-  auto kern = norm_rope_bwd_kernel<T, D, kInter>;
-  if (set_smem(kern, kNrBwdSmem) != cudaSuccess ||
-      launch_pdl(kern, dim3(ctas), dim3(kNrThreads), kNrBwdSmem, stream, a) != cudaSuccess)
+  if (set_smem_once<norm_rope_bwd_kernel<T, D, kInter>>(kNrBwdSmem) != cudaSuccess ||
+      launch_pdl(norm_rope_bwd_kernel<T, D, kInter>, dim3(ctas), dim3(kNrThreads), kNrBwdSmem, stream, a) != cudaSuccess)
     return PLX_ERR_CUDA;
   if (!dw) return PLX_OK;
   return launch_pdl(norm_rope_dw_kernel<D>, dim3(a.sets), dim3(kNrDwThreads), 0, stream, a) == cudaSuccess ? PLX_OK
@@ -220,9 +234,8 @@ DecodeQ4Plan plan_decode_q4(const plx_decode_params* p, int num_sms) {
 
 template <int D, int NT>
 cudaError_t launch_decode_q4(const DecodeQ4Args& a, int ctas, cudaStream_t stream) {
-  auto kern = decode_q4_kernel<D, NT>;
-  const cudaError_t e = set_smem(kern, Q4Smem<D, NT>::kBytes);
-  return e != cudaSuccess ? e : launch_pdl(kern, dim3(ctas), dim3(Q4Smem<D, NT>::kThreads),
+  const cudaError_t e = set_smem_once<decode_q4_kernel<D, NT>>(Q4Smem<D, NT>::kBytes);
+  return e != cudaSuccess ? e : launch_pdl(decode_q4_kernel<D, NT>, dim3(ctas), dim3(Q4Smem<D, NT>::kThreads),
                                                Q4Smem<D, NT>::kBytes, stream, a);
 }
 
@@ -281,7 +294,8 @@ plx_status parallax_page_plan(const int32_t* cached_lens, const int32_t* new_len
   int64_t ctas = by_rows > by_requests ? by_rows : by_requests;
   if (ctas > num_sms) ctas = num_sms;
   const int smem = plan_smem_bytes(a.B);
-  if (smem > 48 * 1024 && set_smem(page_plan_kernel, plan_smem_bytes(kPlanMaxBatch)) != cudaSuccess) return PLX_ERR_CUDA;
+  if (smem > 48 * 1024 && set_smem_once<page_plan_kernel>(plan_smem_bytes(kPlanMaxBatch)) != cudaSuccess)
+    return PLX_ERR_CUDA;
   return launch_pdl(page_plan_kernel, dim3((unsigned)ctas), dim3(kPlanThreads), smem, stream, a) == cudaSuccess
              ? PLX_OK
              : PLX_ERR_CUDA;
