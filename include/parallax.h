@@ -509,7 +509,8 @@ typedef struct plx_norm_rope_params {
 /* One set of head rows: x[b, t, h] at x + b * x_stride[0] + t * x_stride[1] +
  * h * x_stride[2] elements, d contiguous columns; y likewise.  Pointers are
  * 16-byte aligned and strides multiples of 16 bytes.  y may be x itself with
- * the same strides (in place); otherwise it must not overlap any input. */
+ * the same strides (in place); otherwise it must not overlap any input.  A
+ * stride of y is 0 only where there is one entry. */
 typedef struct plx_head_rows {
   const void* x;
   void* y;

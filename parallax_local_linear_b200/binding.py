@@ -786,11 +786,14 @@ def page_plan(cached_lens, new_lens, page_table, free_pages, *, num_rows, num_pa
 
 
 def _head_strides(name, t, batched):
-    """Element strides (batch entry, token, head) of [B, H, T, d] or packed [N, H, d] rows."""
-    s = t.stride()
+    """Element strides (batch entry, token, head) of [B, H, T, d] or packed [N, H, d] rows
+    (0 for a dimension of one entry, whatever torch says there)."""
+    s, n = t.stride(), t.shape
     if s[-1] != 1 and t.numel() > 0:
         raise ValueError(f"{name}'s last dimension must be contiguous")
-    return (s[0], s[2], s[1]) if batched else (0, s[0], s[1])
+    if batched:
+        return s[0] if n[0] > 1 else 0, s[2] if n[2] > 1 else 0, s[1] if n[1] > 1 else 0
+    return 0, s[0] if n[0] > 1 else 0, s[1] if n[1] > 1 else 0
 
 
 def _norm_rope_call(q, rho, k, cos, sin, positions, weights, eps, norm, interleaved):
@@ -946,6 +949,7 @@ class NormRope(torch.autograd.Function):
         return out
 
     @staticmethod
+    @torch.autograd.function.once_differentiable
     def backward(ctx, dq, drho, dk):
         q, rho, k, qw, rw, kw, cos, sin, positions = ctx.saved_tensors
         grads = [None if x is None else (torch.zeros_like(x) if g is None else _dense_rows(g.to(x.dtype)))
@@ -977,8 +981,9 @@ def _append_params(k, v, slot_map, num_pages, num_kv_heads, head_dim, dtype, ind
     _on(index, "k", k, dtype)
     _on(index, "v", v, dtype)
     _on(index, "slot_map", slot_map, torch.int64)
-    return _APPEND.pack(n, num_kv_heads, head_dim, PAGE_SIZE, num_pages, _dtype_code(dtype), ks[0], ks[1], vs[0],
-                        vs[1])
+    row, head = n > 1, num_kv_heads > 1    # (a dimension of one entry has any stride)
+    return _APPEND.pack(n, num_kv_heads, head_dim, PAGE_SIZE, num_pages, _dtype_code(dtype), ks[0] * row,
+                        ks[1] * head, vs[0] * row, vs[1] * head)
 
 
 def cache_append(k, v, slot_map, k_cache, v_cache):

@@ -53,9 +53,10 @@ struct NormRopeArgs {
 // first (rope_prefill 147 to 133 us).
 __device__ __forceinline__ uint4 load_row(const void* p) {
   uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
                : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "l"(p));
+               : "l"(p)
+               : "memory");   // (y may be x itself)
   return v;
 }
 __device__ __forceinline__ void store_row(void* p, const uint4& v) {

@@ -39,6 +39,13 @@ bool strides_ok(const int64_t* s, int n, int elt) {
   return true;
 }
 
+// Rows that are written have places of their own: no stride of 0 over several.
+bool distinct(const int64_t* s, const int64_t* count, int n) {
+  for (int i = 0; i < n; ++i)
+    if (s[i] == 0 && count[i] > 1) return false;
+  return true;
+}
+
 plx_status validate_norm_rope(const plx_head_rows* rows, const plx_head_grads* grads, int32_t num_sets,
                               const float* cos, const float* sin, const int32_t* positions,
                               const plx_norm_rope_params* p) {
@@ -64,6 +71,8 @@ plx_status validate_norm_rope(const plx_head_rows* rows, const plx_head_grads* g
     if ((int64_t)p->batch * p->tokens >= (int64_t)INT32_MAX / 32) return PLX_ERR_UNSUPPORTED;
     if (r.w && (!p->norm || !aligned(r.w, 16))) return PLX_ERR_INVALID_ARG;
     if (!aligned(r.x, 16) || !strides_ok(r.x_stride, 3, elt)) return PLX_ERR_INVALID_ARG;
+    const int64_t count[3] = {p->batch, p->tokens, r.heads};
+    if (!distinct(grads ? grads[i].dx_stride : r.y_stride, count, 3)) return PLX_ERR_INVALID_ARG;
     if (grads == nullptr) {
       if (!r.x || !r.y || !aligned(r.y, 16) || !strides_ok(r.y_stride, 3, elt)) return PLX_ERR_INVALID_ARG;
     } else {
@@ -418,6 +427,8 @@ plx_status parallax_cache_gather_q4(const void* kv_cache, const int64_t* slot_ma
   if (!kv_cache || !aligned(kv_cache, 16)) return PLX_ERR_INVALID_ARG;
   if (p->num_rows == 0) return PLX_OK;
   if (!k || !v || !slot_map || !aligned(k, 16) || !aligned(v, 16) || !aligned(slot_map, 8)) return PLX_ERR_INVALID_ARG;
+  const int64_t count[2] = {p->num_rows, p->num_kv_heads};
+  if (!distinct(p->k_stride, count, 2) || !distinct(p->v_stride, count, 2)) return PLX_ERR_INVALID_ARG;
   AppendArgs a = append_args(slot_map, p);
   a.k_out = k;
   a.v_out = v;

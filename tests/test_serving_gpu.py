@@ -349,6 +349,64 @@ def test_norm_rope_autograd(px, broadcast):
         assert torch.equal(a, b)
 
 
+def test_norm_rope_autograd_of_single_sets_and_captured(px):
+    # probes absent, a rotation alone, and a captured backward pass (torch itself refuses to capture one of leaves
+    # whose eager graph is still alive: their gradient nodes belong to the eager stream)
+    case = (True, 2, 4, 2, 40, 64, 64, False, True, torch.bfloat16)
+    x, w, cos, sin = _rope_inputs(case, seed=8)
+    q, k = x["q"].clone().requires_grad_(), x["k"].clone().requires_grad_()
+    qw = w["q"].clone().requires_grad_()
+
+    def grads():
+        y, none, z = px.NormRope.apply(q, None, k, qw, None, None, cos, sin)
+        assert none is None
+        return torch.autograd.grad(y.float().sum() + 2 * z.float().sum(), (q, k, qw))
+
+    want = px.norm_rope_backward(torch.ones_like(q), None, torch.full_like(k, 2), q.detach(), None, k.detach(), cos, sin,
+                                 q_weight=w["q"])
+    got = grads()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        grads()
+    torch.cuda.current_stream().wait_stream(s)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        cap = grads()
+    g.replay()
+    for t in (got, cap):
+        assert torch.equal(t[0], want[0]) and torch.equal(t[1], want[2]) and torch.equal(t[2], want[3].bfloat16())
+    with pytest.raises(RuntimeError):      # no second derivatives, and no silence about it
+        y = px.NormRope.apply(q, None, None, None, None, None, cos, sin)[0]
+        (d,) = torch.autograd.grad(y.float().square().sum(), q, create_graph=True)
+        d.float().sum().backward()
+    r = px.NormRope.apply(q, None, None, None, None, None, cos, sin, None, 1e-6, False)[0]
+    assert torch.equal(torch.autograd.grad(r, q, torch.ones_like(r))[0],
+                       px.norm_rope_backward(torch.ones_like(q), None, None, q.detach(), None, None, cos, sin, norm=False)[0])
+
+
+def test_rows_of_one_entry_have_any_stride(px):
+    # torch leaves odd strides on dimensions of one entry; rows still start at 16 bytes
+    base = torch.randn(4096, device="cuda").bfloat16()
+    x = base.as_strided((1, 3, 64), (3, 64, 1))
+    cos, sin = _tables(4, 64)
+    assert torch.equal(px.norm_rope(x, None, None, cos, sin)[0], px.norm_rope(x.clone(), None, None, cos, sin)[0])
+    one = base.as_strided((2, 1, 64), (128, 5, 1))
+    slots = torch.tensor([3, 70], device="cuda")
+    a, b = px.q4_cache(2, 1, 64), px.q4_cache(2, 1, 64)
+    px.cache_append_q4(one, one, slots, a)
+    px.cache_append_q4(one.clone(), one.clone(), slots, b)
+    assert torch.equal(a, b)
+    # keys broadcast over heads
+    k = base[:640].view(5, 1, 128).expand(5, 4, 128)
+    c, d = px.q4_cache(1, 4, 128), px.q4_cache(1, 4, 128)
+    px.cache_append_q4(k, k, torch.arange(5, device="cuda"), c)
+    px.cache_append_q4(k.contiguous(), k.contiguous(), torch.arange(5, device="cuda"), d)
+    assert torch.equal(c, d)
+    with pytest.raises(px.ParallaxError):     # written rows must not lie on one another
+        px.norm_rope(k.contiguous(), None, None, None, None, out=(k, None, None))
+
+
 # ------------------------------------------------------------------ cache rows
 def _slots(N, pages, seed, skip=()):
     rng = np.random.default_rng(seed)

@@ -93,6 +93,9 @@ def test_norm_rope_pointers(px, backward, ptrs, kw):
 
 
 def test_norm_rope_forward_and_backward_only(px):
+    assert _rope(px, ys=(0, 512, 0)) == 1 and _rope(px, ys=(0, 0, 128)) == 1    # rows on top of each other
+    assert _rope(px, backward=True, ys=(0, 0, 128)) == 1
+    assert _append(px, "gather", ks=(0, 128)) == 1 and _append(px, "gather", vs=(512, 0)) == 1
     assert _rope(px, dict(y=None)) == 1 and _rope(px, dict(y=_addr(2, 2))) == 1
     assert _rope(px, dict(), tokens=0) == 0
     assert _rope(px, backward=True, g=dict(dy=None)) == 1
