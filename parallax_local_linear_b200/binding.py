@@ -281,20 +281,28 @@ _ws_lock = threading.Lock()
 _workspaces = {}
 
 
-def _workspace(device, nbytes):
+def _workspace(device, nbytes, params):
     """A zero-initialised workspace per device, grown on demand.
 
-    The counter region must start at zero; the library leaves it zero after
-    every call, so the buffer is zeroed only when (re)allocated.
+    The counter region at its front (4 bytes per unit, padded to 256) must
+    start at zero, and the library leaves it zero after every call.  What lies
+    behind one call's counters holds its partials, though, and a later call
+    with more units has counters there: those are cleared for it.
     """
     if nbytes == 0:
         return None
+    units = params.batch * (params.num_kv_heads if params.in_dtype == PLX_BF16 else params.num_q_heads)
+    counters = (4 * units + 255) & ~255
     idx = device.index if device.index is not None else torch.cuda.current_device()
     with _ws_lock:
-        ws = _workspaces.get(idx)
+        ws, clean = _workspaces.get(idx, (None, 0))
         if ws is None or ws.numel() < nbytes:
             ws = torch.zeros(max(nbytes, 1 << 20), dtype=torch.uint8, device=device)
-            _workspaces[idx] = ws
+        elif counters > clean:
+            ws[:counters].zero_()
+            if torch.cuda.is_current_stream_capturing():   # cleared when the graph runs, not yet
+                counters = clean
+        _workspaces[idx] = (ws, counters)
         return ws
 
 
@@ -361,7 +369,7 @@ def decode(q, rho, k_cache, v_cache, scale=None, *, seq_lens=None, page_table=No
     p = decode_params(q, k_cache, page_table=page_table, kv_len=kv_len, scale=scale,
                       out_dtype=out_dtype, num_ctas=num_ctas)
     nbytes = decode_workspace_size(p)
-    ws = _workspace(q.device, nbytes)
+    ws = _workspace(q.device, nbytes, p)
     st = lib.parallax_decode(_ptr(q), _ptr(rho), _ptr(k_cache), _ptr(v_cache), _ptr(page_table),
                              _ptr(seq_lens), _ptr(out), _ptr(ws), 0 if ws is None else ws.numel(),
                              ctypes.byref(p), _stream_ptr(q.device))
@@ -469,7 +477,7 @@ def decode_projected(x, w_q, w_rho, k_cache, v_cache, scale=None, *, seq_lens=No
     p = decode_params(q_out, k_cache, page_table=page_table, kv_len=kv_len, scale=scale,
                       out_dtype=out_dtype, num_ctas=num_ctas)
     nbytes = decode_workspace_size(p)
-    ws = _workspace(x.device, nbytes)
+    ws = _workspace(x.device, nbytes, p)
     st = lib.parallax_decode_projected(_ptr(x), _ptr(w_q), _ptr(w_rho), int(x.shape[1]), _ptr(k_cache),
                                        _ptr(v_cache), _ptr(page_table), _ptr(seq_lens), _ptr(q_out),
                                        _ptr(rho_out), _ptr(out), _ptr(ws), 0 if ws is None else ws.numel(),
