@@ -90,7 +90,10 @@ struct Q4Smem {
   static constexpr int kRow = 2 * D + 4;                           // a head's state: m l c aref O1 O2
   static constexpr int kState = 4 * NT * kRow * 4;                 // bytes of a piece
   static constexpr int kStateOff = kWarps * kRing;
-  static constexpr int kMetaOff = kStateOff + kWarps * kState;
+  static constexpr int kQRow = 2 * D + 16;                         // a staged q or rho row (16 bytes apart in the banks)
+  static constexpr int kQ = 8 * NT * kQRow;                        // per warp
+  static constexpr int kQOff = kStateOff + kWarps * kState;
+  static constexpr int kMetaOff = kQOff + kWarps * kQ;
   static constexpr int kPreOff = kMetaOff + kWarps * 8 * 4;
   static constexpr int kBytes = kPreOff + (kThreads + 4) * 4;
   static_assert(kState <= kRing, "a warp's last piece fits in its ring");
@@ -126,6 +129,12 @@ __device__ __forceinline__ float2 unpack_half(uint32_t v) {
 // 16 bytes from global to shared memory, not through L1.
 __device__ __forceinline__ void q4_copy16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(reinterpret_cast<uint64_t>(src)) : "memory");
+}
+// Zeros instead where !read.
+__device__ __forceinline__ void q4_copy16(uint32_t dst, const void* src, bool read) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(reinterpret_cast<uint64_t>(src)),
+               "r"(read ? 16 : 0)
+               : "memory");
 }
 __device__ __forceinline__ void q4_copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -201,22 +210,26 @@ struct Q4Cursor {
       b = x / per_seq;
       base = b * per_seq;
     } else {
-      int lo = 0, hi = s.shares - 1;   // last share with pre <= x that is not empty
-      while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (s.pre[mid] <= x) lo = mid; else hi = mid - 1;
-      }
-      const int i = lo * s.per + lane;
-      const int n = lane < s.per && i < s.a.B ? s.pages(i) * s.a.Hkv : 0;
-      int inc = n;
+      // last share with pre <= x (it is not empty): first among every 32nd part's first, then in that part
+      const int part = s.shares / 32;
+      int lo = __popc(__ballot_sync(0xffffffffu, s.pre[lane * part] <= x)) - 1;
+      lo = lo * part + __popc(__ballot_sync(0xffffffffu, lane < part && s.pre[lo * part + min(lane, part - 1)] <= x)) - 1;
+      if (s.per == 1) {
+        b = lo;
+        base = s.pre[lo];
+      } else {
+        const int i = lo * s.per + lane;
+        const int n = lane < s.per && i < s.a.B ? s.pages(i) * s.a.Hkv : 0;
+        int inc = n;
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(0xffffffffu, inc, o);
-        if (lane >= o) inc += v;
+        for (int o = 1; o < 32; o <<= 1) {
+          const int v = __shfl_up_sync(0xffffffffu, inc, o);
+          if (lane >= o) inc += v;
+        }
+        const int first = __ffs(__ballot_sync(0xffffffffu, s.pre[lo] + inc > x)) - 1;
+        b = lo * s.per + first;
+        base = s.pre[lo] + __shfl_sync(0xffffffffu, inc - n, first);
       }
-      const int first = __ffs(__ballot_sync(0xffffffffu, s.pre[lo] + inc > x)) - 1;
-      b = lo * s.per + first;
-      base = s.pre[lo] + __shfl_sync(0xffffffffu, inc - n, first);
     }
     len = s.len(b);
     tiles = (len + kQ4Page - 1) / kQ4Page;
@@ -482,14 +495,20 @@ __global__ void __launch_bounds__(Q4Smem<D, NT>::kThreads, 1) decode_q4_kernel(c
     }
     pre[tid] = base + inc - sum;
     sp.T = total;
-    // sequences without tokens have no pages: their rows are zero
-    for (int b = blockIdx.x; b < a.B; b += gridDim.x)
-      if (sp.len(b) == 0)
-        for (int i = tid; i < a.Hq * D / 4; i += kThreads) store_out4(a, (size_t)b * a.Hq * D + 4 * i, 0.f, 0.f, 0.f, 0.f);
   }
   __syncthreads();
   sp.G = min((uint32_t)gridDim.x, (sp.T + a.min_pages - 1) / a.min_pages);
-  if (blockIdx.x >= sp.G) return;
+  // Sequences without tokens have no pages: their rows are zero.
+  auto zero_rows = [&] {
+    if (a.seq_lens == nullptr) return;
+    for (int b = blockIdx.x; b < a.B; b += gridDim.x)
+      if (sp.len(b) == 0)
+        for (int i = tid; i < a.Hq * D / 4; i += kThreads) store_out4(a, (size_t)b * a.Hq * D + 4 * i, 0.f, 0.f, 0.f, 0.f);
+  };
+  if (blockIdx.x >= sp.G) {
+    zero_rows();
+    return;
+  }
   sp.W = sp.G * kWarps;
   sp.quot = sp.T / sp.W;
   sp.rem = sp.T % sp.W;
@@ -497,6 +516,7 @@ __global__ void __launch_bounds__(Q4Smem<D, NT>::kThreads, 1) decode_q4_kernel(c
   const uint32_t gw = blockIdx.x * kWarps + warp;
   const int y0 = (int)sp.start(gw), y1 = (int)sp.start(gw + 1), n = y1 - y0;
   uint8_t* ring = q4_smem + warp * SM::kRing;
+  uint8_t* q_rows = q4_smem + SM::kQOff + warp * SM::kQ;
   float* first_state = reinterpret_cast<float*>(q4_smem + SM::kStateOff + warp * SM::kState);
   if (lane < 8) meta[warp * 8 + lane] = -1;
   __syncwarp();
@@ -505,6 +525,22 @@ __global__ void __launch_bounds__(Q4Smem<D, NT>::kThreads, 1) decode_q4_kernel(c
     Q4Cursor cur, ahead;
     cur.seek(sp, y0);
     ahead = cur;
+    // The q and rho rows of a unit come the same way, into q_rows: row 8 t + 2 i
+    // is q and row 8 t + 2 i + 1 rho of head 4 t + i (zeros past the group).  They
+    // are asked for before the unit's first pages (behind those they waited for
+    // 2.5 us of page copies), the next unit's as soon as the warp has made its
+    // operands of the current one's.
+    auto fetch_q = [&](int b, int hu) {
+#pragma unroll
+      for (int k = lane; k < 8 * NT * (D / 8); k += 32) {
+        const int n = k / (D / 8), v = k % (D / 8), h = n / 2;
+        const bool live = h < a.group;
+        const __nv_bfloat16* src = ((n & 1) ? a.rho : a.q) +
+                                   ((size_t)b * a.Hq + (size_t)hu * a.group + (live ? h : 0)) * D + 8 * v;
+        q4_copy16(smem_u32(q_rows + n * SM::kQRow + 16 * v), src, live);
+      }
+    };
+    fetch_q(cur.b, cur.hu);
     // Part 2 i is the keys of the run's page i, part 2 i + 1 its values; part k
     // goes to slot k % S.  A page's entry in the page table is read when the
     // part before it is issued and looked at when its own keys are.  Every
@@ -564,18 +600,23 @@ __global__ void __launch_bounds__(Q4Smem<D, NT>::kThreads, 1) decode_q4_kernel(c
     };
 
     for (int i = 0; i < n; ++i) {
+      landed();
+      const int nvalid = cur.len - cur.local * kQ4Page;   // tokens of this page (>= 1; 64 or more: all)
+      if (nvalid < kQ4Page) clear_tail(nvalid);
       if (seg == 0) {
+        // The unit's rows went out with the part that followed the previous
+        // unit's first keys, at the latest the last but one so far.
+        if constexpr (S > 2) {
+          q4_copy_wait<1>();
+          __syncwarp();
+        }
         st.reset();
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
-          const int h = 4 * t + (r >> 1);
-          const bool live = h < a.group;
-          const __nv_bfloat16* row = ((r & 1) ? a.rho : a.q) +
-                                     ((size_t)cur.b * a.Hq + (size_t)cur.hu * a.group + (live ? h : 0)) * D + 8 * hc;
           uint4 v[J];
 #pragma unroll
           for (int j = 0; j < J; ++j)
-            v[j] = live ? __ldg(reinterpret_cast<const uint4*>(row + 32 * j)) : make_uint4(0, 0, 0, 0);
+            v[j] = *reinterpret_cast<const uint4*>(q_rows + (8 * t + r) * SM::kQRow + 64 * j + 16 * hc);
           float f[J][8], mx = 0.f, gsum[G];
 #pragma unroll
           for (int g = 0; g < G; ++g) gsum[g] = 0.f;
@@ -618,11 +659,14 @@ __global__ void __launch_bounds__(Q4Smem<D, NT>::kThreads, 1) decode_q4_kernel(c
             rs[t][g] = __shfl_sync(0xffffffffu, gsum[g], 8 * hc + 4);
           }
         }
+        if (i + cur.tiles - cur.local < n) {   // the run goes on past this unit
+          Q4Cursor next = cur;
+          next.local = next.tiles - 1;
+          next.next_page(sp);
+          __syncwarp();   // every lane has read the rows
+          fetch_q(next.b, next.hu);
+        }
       }
-
-      landed();
-      const int nvalid = cur.len - cur.local * kQ4Page;   // tokens of this page (>= 1; 64 or more: all)
-      if (nvalid < kQ4Page) clear_tail(nvalid);
 
       // ---- scores and probe values of tokens 16 mt + r and + 8
       float x[NT][8], av[NT][8];
@@ -770,6 +814,7 @@ __global__ void __launch_bounds__(Q4Smem<D, NT>::kThreads, 1) decode_q4_kernel(c
       }
     }
   }
+  zero_rows();
   __syncthreads();
 
   // ---- merge the CTA's pieces.  A team of four warps takes every kTeams-th
