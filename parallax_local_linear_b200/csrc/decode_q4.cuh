@@ -863,16 +863,16 @@ __global__ void __launch_bounds__(Q4Smem<D, NT>::kThreads, 1) decode_q4_kernel(c
       }
     }
     if (whole) continue;
-    __threadfence();
     team_bar();
-    if (tt == 0) {
-      const int prev = atomicAdd(a.counters + unit, 1);
-      s_last[team] = prev == (int)(c1 - c0);
-      if (s_last[team]) atomicExch(a.counters + unit, 0);
+    if (tt == 0) {   // (the barrier puts the team's writes before this thread's fence, and its fence before their reads)
+      __threadfence();
+      const bool last = atomicAdd(a.counters + unit, 1) == (int)(c1 - c0);
+      s_last[team] = last;
+      if (last) atomicExch(a.counters + unit, 0);
+      __threadfence();
     }
     team_bar();
     if (s_last[team]) {
-      __threadfence();
       for (int i = tt; i < items; i += 128) {
         const int h = i / (D / 4), d = 4 * (i % (D / 4));
         Q4Merged s;
