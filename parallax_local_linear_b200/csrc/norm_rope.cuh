@@ -9,11 +9,12 @@
 // Both directions read each row once and write one row: HBM bounds them.  A
 // row lies in the 16-byte vectors of LPR neighbouring lanes (16 lanes for 128
 // bf16 columns), so its sums are butterfly shuffles among them and the row
-// never leaves registers.  A lane's rotation partner holds the pair's other
-// column (another lane of the row, or the lane itself when interleaved), and
-// the lane forms only its own column of the pair: the partner's raw vector
-// comes by four shuffles.  A group of lanes takes several heads of one token,
-// so a token's cos and sin are read once for them.
+// never leaves registers.  A lane's columns are two runs of 8 bytes, one on
+// each side of the pairs it turns (column f and f + rot/2; next to each other
+// when interleaved or past rot), so that a pair never lies in two lanes: with
+// whole 16-byte vectors the partner's came by four shuffles and was unpacked a
+// second time.  A group of lanes takes several heads of one token, so a
+// token's cos and sin are read once for them.
 #pragma once
 
 #include "ptx.cuh"
@@ -51,16 +52,16 @@ struct NormRopeArgs {
 
 // Rows are read once and written once: neither way through L1, and out of L2
 // first (rope_prefill 147 to 133 us).
-__device__ __forceinline__ uint4 load_row(const void* p) {
-  uint4 v;
-  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+__device__ __forceinline__ uint2 load_row(const void* p) {
+  uint2 v;
+  asm volatile("ld.global.L1::no_allocate.v2.u32 {%0, %1}, [%2];"
+               : "=r"(v.x), "=r"(v.y)
                : "l"(p)
                : "memory");   // (y may be x itself)
   return v;
 }
-__device__ __forceinline__ void store_row(void* p, const uint4& v) {
-  asm volatile("st.global.cs.v4.u32 [%0], {%1, %2, %3, %4};" ::"l"(p), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+__device__ __forceinline__ void store_row(void* p, uint32_t v0, uint32_t v1) {
+  asm volatile("st.global.cs.v2.u32 [%0], {%1, %2};" ::"l"(p), "r"(v0), "r"(v1) : "memory");
 }
 // 16 bytes into shared memory as they arrive; zeros where !read.
 __device__ __forceinline__ void copy_row(uint32_t dst, const void* src, bool read) {
@@ -69,7 +70,7 @@ __device__ __forceinline__ void copy_row(uint32_t dst, const void* src, bool rea
                : "memory");
 }
 
-// A lane's share of a row: E values from one 16-byte vector, in pairs (the
+// A lane's share of a row: E values from two runs of 8 bytes, in pairs (the
 // packed fp32 arithmetic takes two at an instruction).
 template <typename T>
 struct RowVec;
@@ -99,50 +100,40 @@ struct RowVec<float> {
   }
 };
 
-// The lane's own columns of the rotation at one position:
-//     y_e = n_e c[e] + partner(n)_e s[e].
-// (c, s) is (cos, -sin) for the first column of a pair, (cos, sin) for the
-// second and (1, 0) past rot.
-template <int P>
+// cos and sin of the lane's pairs at one position: pairs i and i + P/2 of its
+// columns turn by (c, s)[i], or with kInter the two columns of pair i do.
+// (1, 0) past rot.
+template <int P, bool kInter>
 struct Turn {
-  float2 c[P], s[P];
+  static constexpr int N = kInter ? P : P / 2;
+  float2 c[N], s[N];
 };
 
 template <int P, bool kInter>
-__device__ __forceinline__ void load_turn(const NormRopeArgs& a, int pos, int col0, Turn<P>& t) {
-  const int half = a.rot / 2;
+__device__ __forceinline__ void load_turn(const NormRopeArgs& a, int pos, int col0, Turn<P, kInter>& t) {
   if (col0 >= a.rot) {
 #pragma unroll
-    for (int i = 0; i < P; ++i) {
+    for (int i = 0; i < t.N; ++i) {
       t.c[i] = make_float2(1.f, 1.f);
       t.s[i] = make_float2(0.f, 0.f);
     }
     return;
   }
-  const size_t row = (size_t)pos * half;
-  if (kInter) {
-    const float* cp = a.cos + row + col0 / 2;
-    const float* sp = a.sin + row + col0 / 2;
+  const size_t row = (size_t)pos * (a.rot / 2);
 #pragma unroll
-    for (int i = 0; i < P; ++i) {
-      const float c = __ldg(cp + i), s = __ldg(sp + i);
+  for (int i = 0; i < t.N; ++i) {
+    if (kInter) {
+      const float c = __ldg(a.cos + row + col0 / 2 + i), s = __ldg(a.sin + row + col0 / 2 + i);
       t.c[i] = make_float2(c, c);
-      t.s[i] = make_float2(-s, s);
-    }
-  } else {
-    const bool second = col0 >= half;   // rot is a multiple of 16: a lane's columns lie in one half
-    const int f0 = second ? col0 - half : col0;
-#pragma unroll
-    for (int i = 0; i < P / 2; ++i) {
-      const float4 c = __ldg(reinterpret_cast<const float4*>(a.cos + row + f0) + i);
-      const float4 s = __ldg(reinterpret_cast<const float4*>(a.sin + row + f0) + i);
-      t.c[2 * i] = make_float2(c.x, c.y);
-      t.c[2 * i + 1] = make_float2(c.z, c.w);
-      t.s[2 * i] = second ? make_float2(s.x, s.y) : make_float2(-s.x, -s.y);
-      t.s[2 * i + 1] = second ? make_float2(s.z, s.w) : make_float2(-s.z, -s.w);
+      t.s[i] = make_float2(s, s);
+    } else {
+      t.c[i] = __ldg(reinterpret_cast<const float2*>(a.cos + row + col0) + i);
+      t.s[i] = __ldg(reinterpret_cast<const float2*>(a.sin + row + col0) + i);
     }
   }
 }
+
+__device__ __forceinline__ float2 neg2(float2 v) { return make_float2(-v.x, -v.y); }
 
 template <int LPR>
 __device__ __forceinline__ float row_sum(float v) {
@@ -153,30 +144,28 @@ __device__ __forceinline__ float row_sum(float v) {
 
 template <typename T, int D, bool kInter>
 struct NrLane {
-  static constexpr int E = RowVec<T>::E, P = E / 2, LPR = D / E, RPW = 32 / LPR;
-  int col0, src;       // first column, lane of the rotation partner
+  static constexpr int E = RowVec<T>::E, P = E / 2, H = P / 2, LPR = D / E;
+  int col0, col1;      // first columns of the two runs
 
   __device__ __forceinline__ explicit NrLane(const NormRopeArgs& a) {
-    const int lane = threadIdx.x & 31, l = lane % LPR;
-    col0 = l * E;
-    const int shift = a.rot / 2 / E;
-    src = col0 >= a.rot || kInter ? lane : (col0 < a.rot / 2 ? lane + shift : lane - shift);
+    const int l = (threadIdx.x & 31) % LPR, turning = kInter ? 0 : a.rot / E;   // lanes with a run on each side
+    col0 = l < turning ? l * (E / 2) : l * E;
+    col1 = col0 + (l < turning ? a.rot / 2 : E / 2);
   }
-  // The partner columns of a vector of the lane's row.  Every lane takes part.
-  __device__ __forceinline__ void partner(const uint4& v, float2 (&f)[P]) const {
-    if (kInter) {   // the partner of column e is e ^ 1
-      RowVec<T>::unpack(v, f);
-#pragma unroll
-      for (int i = 0; i < P; ++i) f[i] = make_float2(f[i].y, f[i].x);
-    } else {
-      RowVec<T>::unpack(make_uint4(__shfl_sync(0xffffffffu, v.x, src), __shfl_sync(0xffffffffu, v.y, src),
-                                   __shfl_sync(0xffffffffu, v.z, src), __shfl_sync(0xffffffffu, v.w, src)),
-                        f);
-    }
+  __device__ __forceinline__ uint4 weights(const void* w) const {
+    if (w == nullptr) return make_uint4(0, 0, 0, 0);
+    const uint2 v0 = __ldg(reinterpret_cast<const uint2*>(static_cast<const T*>(w) + col0));
+    const uint2 v1 = __ldg(reinterpret_cast<const uint2*>(static_cast<const T*>(w) + col1));
+    return make_uint4(v0.x, v0.y, v1.x, v1.y);
   }
-  __device__ __forceinline__ uint4 load_weights(const void* w) const {
-    return w == nullptr ? make_uint4(0, 0, 0, 0)
-                        : __ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(w) + col0));
+  // The other column of each pair of columns.
+  static __device__ __forceinline__ float2 partner(const float2 (&f)[P], int i) {
+    return kInter ? make_float2(f[i].y, f[i].x) : f[(i + H) % P];
+  }
+  __device__ __forceinline__ void store(T* row, const float2 (&o)[P]) const {
+    const uint4 v = RowVec<T>::pack(o);
+    store_row(row + col0, v.x, v.y);
+    store_row(row + col1, v.z, v.w);
   }
 };
 
@@ -193,7 +182,7 @@ __device__ __forceinline__ int nr_position(const NormRopeArgs& a, int b, int t) 
 // A group of LPR lanes takes the rows of chunk blockIdx.y (a set's next `hpg`
 // heads) of one token; neighbouring groups take neighbouring tokens.
 template <typename T, int D, bool kInter>
-__global__ void __launch_bounds__(kNrThreads) norm_rope_kernel(const NormRopeArgs a) {
+__global__ void __launch_bounds__(kNrThreads, 5) norm_rope_kernel(const NormRopeArgs a) {
   using L = NrLane<T, D, kInter>;
   constexpr int P = L::P;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -210,34 +199,38 @@ __global__ void __launch_bounds__(kNrThreads) norm_rope_kernel(const NormRopeArg
   // y = r (x wc + partner(x) ws) with the weights taken into the rotation
   float2 wc[P], ws[P];
   {
-    Turn<P> tn;
+    Turn<P, kInter> tn;
     load_turn<P, kInter>(a, live ? pos : 0, live ? ln.col0 : D, tn);
-    const uint4 wv = ln.load_weights(set.w);
-    float2 w[P], wp[P];
-    RowVec<T>::unpack(wv, w);
-    ln.partner(wv, wp);
+    float2 w[P];
+    RowVec<T>::unpack(ln.weights(set.w), w);
+#pragma unroll
+    for (int i = 0; i < P; ++i)
+      if (set.w == nullptr) w[i] = make_float2(1.f, 1.f);
 #pragma unroll
     for (int i = 0; i < P; ++i) {
-      wc[i] = set.w == nullptr ? tn.c[i] : mul2(w[i], tn.c[i]);
-      ws[i] = set.w == nullptr ? tn.s[i] : mul2(wp[i], tn.s[i]);
+      const float2 c = tn.c[i % tn.N], sn = tn.s[i % tn.N];
+      wc[i] = mul2(w[i], c);
+      ws[i] = mul2(L::partner(w, i), kInter ? make_float2(-sn.x, sn.y) : i < L::H ? neg2(sn) : sn);
     }
   }
-  const T* x = static_cast<const T*>(set.x) + b * set.xs[0] + t * set.xs[1] + h0 * set.xs[2] + ln.col0;
-  T* y = static_cast<T*>(set.y) + b * set.ys[0] + t * set.ys[1] + h0 * set.ys[2] + ln.col0;
+  const T* x = static_cast<const T*>(set.x) + b * set.xs[0] + t * set.xs[1] + h0 * set.xs[2];
+  T* y = static_cast<T*>(set.y) + b * set.ys[0] + t * set.ys[1] + h0 * set.ys[2];
   const int heads = live ? min(a.hpg, set.heads - h0) : 0;
-  constexpr int U = 4;   // rows in flight
+  constexpr int U = 2;   // rows in flight (four on three CTAs an SM instead of five are 1% slower, and more in small calls)
   for (int j = 0; j < a.hpg; j += U) {
-    uint4 v[U];
+    uint2 v0[U], v1[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      v[u] = make_uint4(0, 0, 0, 0);
-      if (j + u < heads) v[u] = load_row(x + (j + u) * set.xs[2]);
+      v0[u] = v1[u] = make_uint2(0, 0);
+      if (j + u < heads) {
+        v0[u] = load_row(x + (j + u) * set.xs[2] + ln.col0);
+        v1[u] = load_row(x + (j + u) * set.xs[2] + ln.col1);
+      }
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      float2 f[P], p[P], o[P];
-      RowVec<T>::unpack(v[u], f);
-      ln.partner(v[u], p);
+      float2 f[P], o[P];
+      RowVec<T>::unpack(make_uint4(v0[u].x, v0[u].y, v1[u].x, v1[u].y), f);
       float r = 1.f;
       if (a.norm) {
         float2 ss = make_float2(0.f, 0.f);
@@ -246,8 +239,8 @@ __global__ void __launch_bounds__(kNrThreads) norm_rope_kernel(const NormRopeArg
         r = rsqrtf(row_sum<L::LPR>(ss.x + ss.y) + a.eps);
       }
 #pragma unroll
-      for (int i = 0; i < P; ++i) o[i] = mul2(fma2(f[i], wc[i], mul2(p[i], ws[i])), make_float2(r, r));
-      if (j + u < heads) store_row(y + (j + u) * set.ys[2], RowVec<T>::pack(o));
+      for (int i = 0; i < P; ++i) o[i] = mul2(fma2(f[i], wc[i], mul2(L::partner(f, i), ws[i])), make_float2(r, r));
+      if (j + u < heads) ln.store(y + (j + u) * set.ys[2], o);
     }
   }
 }
@@ -266,77 +259,110 @@ __global__ void __launch_bounds__(kNrThreads, kNrBwdCtasPerSm) norm_rope_bwd_ker
   while (si + 1 < a.sets && (int)blockIdx.x >= a.set[si + 1].first_cta) ++si;
   const NormRopeSet& set = a.set[si];
   float2 w[P], acc[P];
-  RowVec<T>::unpack(ln.load_weights(set.w), w);
+  RowVec<T>::unpack(ln.weights(set.w), w);
 #pragma unroll
   for (int i = 0; i < P; ++i) {
     if (set.w == nullptr) w[i] = make_float2(1.f, 1.f);
     acc[i] = make_float2(0.f, 0.f);
   }
-  const uint32_t groups = set.ctas * (kNrThreads / L::LPR), tokens = a.B * a.T, items = tokens * set.chunks;
+  const int groups = set.ctas * (kNrThreads / L::LPR), tokens = a.B * a.T;
+  const uint32_t items = (uint32_t)tokens * set.chunks;
   const uint32_t group = (blockIdx.x - set.first_cta) * (kNrThreads / L::LPR) + threadIdx.x / L::LPR;
 
-  // An item is kNrBwdHeads heads of a token.  The next item's vectors come into
-  // this thread's own part of shared memory while it works on the current one
-  // (loading two rows at a time into registers left 24 warps waiting: 268
-  // against 231 us for rope_grad at its best chunk).
+  // An item is kNrBwdHeads heads of a token.  The next item's rows come into the
+  // warp's own part of shared memory while it works on the current one (loading
+  // two rows at a time into registers left 24 warps waiting: 231 against 177 us
+  // for rope_grad).
   struct Item {
     const T* x;
     const T* dy;
     T* dx;
     int heads, pos;      // rows to write; position, or -1
   };
-  auto decode = [&](uint32_t item) {
+  // The group's items are `groups` tokens apart, chunk after chunk; stepping
+  // through them needs no division.
+  int chunk = 0, b = 0;
+  uint32_t t = group;
+  auto settle = [&] {
+    while (b < a.B && t >= (uint32_t)a.T) {
+      t -= a.T;
+      ++b;
+    }
+    while (b >= a.B && chunk < set.chunks) {
+      b -= a.B;
+      ++chunk;
+      while (b < a.B && t >= (uint32_t)a.T) {
+        t -= a.T;
+        ++b;
+      }
+    }
+  };
+  settle();
+  auto here = [&] {
     Item it;
-    const bool in = item < items;
-    const int chunk = in ? item / tokens : 0, tok = in ? item - chunk * tokens : 0;
-    const int b = a.B == 1 ? 0 : tok / a.T, t = tok - b * a.T, h0 = chunk * kNrBwdHeads;
-    it.pos = in ? nr_position(a, b, t) : -1;
-    it.x = static_cast<const T*>(set.x) + b * set.xs[0] + t * set.xs[1] + h0 * set.xs[2] + ln.col0;
-    it.dy = static_cast<const T*>(set.dy) + b * set.ds[0] + t * set.ds[1] + h0 * set.ds[2] + ln.col0;
-    it.dx = static_cast<T*>(set.y) + b * set.ys[0] + t * set.ys[1] + h0 * set.ys[2] + ln.col0;
+    const bool in = chunk < set.chunks;
+    const int h0 = in ? chunk * kNrBwdHeads : 0, bb = in ? b : 0, tt = in ? (int)t : 0;
+    it.pos = in ? nr_position(a, bb, tt) : -1;
+    it.x = static_cast<const T*>(set.x) + bb * set.xs[0] + tt * set.xs[1] + h0 * set.xs[2];
+    it.dy = static_cast<const T*>(set.dy) + bb * set.ds[0] + tt * set.ds[1] + h0 * set.ds[2];
+    it.dx = static_cast<T*>(set.y) + bb * set.ys[0] + tt * set.ys[1] + h0 * set.ys[2];
     it.heads = in ? min(kNrBwdHeads, set.heads - h0) : 0;   // (padding rows of a token read nothing and write zeros)
     return it;
   };
-  extern __shared__ __align__(16) uint8_t nr_smem[];   // [2][kNrBwdHeads][x, dy][thread]
+  // [2][kNrBwdHeads][x, dy][group]: rows as they are in memory
+  extern __shared__ __align__(16) uint8_t nr_smem[];
+  const int lane_row = (threadIdx.x & 31) % L::LPR;
   auto slot = [&](int buf, int j, int which) {
-    return nr_smem + (((buf * kNrBwdHeads + j) * 2 + which) * kNrThreads + threadIdx.x) * 16;
+    return nr_smem + ((buf * kNrBwdHeads + j) * 2 + which) * (kNrThreads * 16) + (threadIdx.x / L::LPR) * (L::LPR * 16);
   };
   auto fetch = [&](const Item& it, int buf) {
+    const T* x = it.x + lane_row * L::E;
+    const T* dy = it.dy + lane_row * L::E;
+    const int reads = it.pos >= 0 ? it.heads : 0;
 #pragma unroll
-    for (int j = 0; j < kNrBwdHeads; ++j) {
-      const bool read = it.pos >= 0 && j < it.heads;
-      copy_row(smem_u32(slot(buf, j, 0)), read && a.norm ? it.x + j * set.xs[2] : static_cast<const T*>(set.dy), read && a.norm);
-      copy_row(smem_u32(slot(buf, j, 1)), read ? it.dy + j * set.ds[2] : static_cast<const T*>(set.dy), read);
+    for (int j = 0; j < kNrBwdHeads; ++j) {   // (nothing is read where the size is 0)
+      copy_row(smem_u32(slot(buf, j, 0) + lane_row * 16), x, j < reads && a.norm);
+      copy_row(smem_u32(slot(buf, j, 1) + lane_row * 16), dy, j < reads);
+      x += set.xs[2];
+      dy += set.ds[2];
     }
   };
-  Item next = decode(group);
+  auto take = [&](int buf, int j, int which) {
+    const T* row = reinterpret_cast<const T*>(slot(buf, j, which));
+    const uint2 v0 = *reinterpret_cast<const uint2*>(row + ln.col0), v1 = *reinterpret_cast<const uint2*>(row + ln.col1);
+    return make_uint4(v0.x, v0.y, v1.x, v1.y);
+  };
+  Item next = here();
   fetch(next, 0);
   asm volatile("cp.async.commit_group;" ::: "memory");
   int buf = 0;
   // Every lane of a warp makes the same number of rounds: the sums' shuffles need all of them.
   for (uint32_t base = 0; base < items; base += groups, buf ^= 1) {
     const Item it = next;
+    __syncwarp();   // every lane has read the slots that are filled next
     if (base + groups < items) {
-      next = decode(base + groups + group);
+      t += groups;
+      settle();
+      next = here();
       fetch(next, buf ^ 1);
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
-    Turn<P> tn;
+    Turn<P, kInter> tn;
     load_turn<P, kInter>(a, max(it.pos, 0), it.pos >= 0 ? ln.col0 : D, tn);
-#pragma unroll
-    for (int i = 0; i < P; ++i) tn.s[i] = make_float2(-tn.s[i].x, -tn.s[i].y);   // the transposed rotation
     asm volatile("cp.async.wait_group 1;" ::: "memory");
+    __syncwarp();
 #pragma unroll
     for (int j = 0; j < kNrBwdHeads; ++j) {
-      const uint4 vd = *reinterpret_cast<const uint4*>(slot(buf, j, 1));
-      float2 f[P], d[P], p[P], g[P];
-      RowVec<T>::unpack(*reinterpret_cast<const uint4*>(slot(buf, j, 0)), f);
-      RowVec<T>::unpack(vd, d);
-      ln.partner(vd, p);
+      float2 f[P], e[P], d[P], g[P];
+      RowVec<T>::unpack(take(buf, j, 0), f);
+      RowVec<T>::unpack(take(buf, j, 1), e);
       float2 ss = make_float2(0.f, 0.f), gx = ss;
 #pragma unroll
       for (int i = 0; i < P; ++i) {
-        d[i] = fma2(d[i], tn.c[i], mul2(p[i], tn.s[i]));   // dn
+        // dn: the transposed rotation
+        const float2 sn = tn.s[i % tn.N];
+        d[i] = fma2(e[i], tn.c[i % tn.N],
+                    mul2(L::partner(e, i), kInter ? make_float2(sn.x, -sn.y) : i < L::H ? sn : neg2(sn)));
         g[i] = mul2(d[i], w[i]);
         const float2 fd = mul2(f[i], make_float2(1.f / D, 1.f / D));
         ss = fma2(fd, f[i], ss);
@@ -351,7 +377,7 @@ __global__ void __launch_bounds__(kNrThreads, kNrBwdCtasPerSm) norm_rope_bwd_ker
           acc[i] = fma2(d[i], mul2(f[i], make_float2(r, r)), acc[i]);
         }
       }
-      if (j < it.heads) store_row(it.dx + j * set.ys[2], RowVec<T>::pack(g));
+      if (j < it.heads) ln.store(it.dx + j * set.ys[2], g);
     }
   }
   if (set.dw == nullptr) return;
@@ -359,7 +385,8 @@ __global__ void __launch_bounds__(kNrThreads, kNrBwdCtasPerSm) norm_rope_bwd_ker
   static_assert(kNrThreads / L::LPR * D * 4 <= kNrBwdSmem, "the groups' sums fit");
   __syncthreads();   // (each thread has read its own vectors)
 #pragma unroll
-  for (int i = 0; i < P; ++i) *reinterpret_cast<float2*>(&part[threadIdx.x / L::LPR][ln.col0 + 2 * i]) = acc[i];
+  for (int i = 0; i < P; ++i)
+    *reinterpret_cast<float2*>(&part[threadIdx.x / L::LPR][(i < L::H ? ln.col0 : ln.col1) + 2 * (i % L::H)]) = acc[i];
   __syncthreads();
   if (threadIdx.x < D) {
     float sum = 0.f;
