@@ -354,12 +354,12 @@ struct Q4WarpState {
   }
 };
 
-// Adds a page's tokens to the sums: weights from the scores x and probe values
-// av against the reference st.m, 16 tokens at a time.  `slot`: the page's value
+// Adds a page's tokens to the sums: weights from the scores fs x and probe
+// values av against the reference st.m, 16 tokens at a time.  `slot`: the page's value
 // codes and parameters.  kFine: with the weights' low halves.
 template <int D, int NT, bool kFine>
-__device__ __forceinline__ void q4_value_sums(Q4WarpState<D, NT>& st, const uint8_t* slot, const float (&x)[NT][8],
-                                              const float (&av)[NT][8]) {
+__device__ __forceinline__ void q4_value_sums(Q4WarpState<D, NT>& st, const uint8_t* slot, const float (&fs)[NT],
+                                              const float (&x)[NT][8], const float (&av)[NT][8]) {
   using SM = Q4Smem<D, NT>;
   constexpr int G = D / 64, J = D / 32;
   const int lane = threadIdx.x & 31, r = lane >> 2, hc = lane & 3;
@@ -373,7 +373,7 @@ __device__ __forceinline__ void q4_value_sums(Q4WarpState<D, NT>& st, const uint
       lds_words<G>(slot + SM::kCodes + (16 * kk + r + 8 * half) * (4 * G), vp);
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
-        const float p = ex2(x[t][e] - (st.m[t] - 14.f)), pa = p * av[t][e];
+        const float p = ex2(fmaf(fs[t], x[t][e], 14.f - st.m[t])), pa = p * av[t][e];
         st.l[t] += p;
         st.c[t] += pa;
 #pragma unroll
@@ -577,8 +577,8 @@ __global__ void __launch_bounds__(Q4Smem<D, NT>::kThreads, 1) decode_q4_kernel(c
 
     Q4WarpState<D, NT> st;
     uint32_t qf[NT][D / 16][2];     // [q rho ..] operand
-    float fs[NT], fa[NT];           // factors of a score (in powers of two) and of a probe value
-    float qs[NT][G], rs[NT][G];     // group sums of q (times the scale) and rho
+    float fs[NT], fa[NT];           // factors of a score (in powers of two; positive) and of a probe value
+    float qs[NT][G], rs[NT][G];     // group sums of q (over fs) and rho
     int seg = 0;                    // pages of the current unit done by this warp
     uint8_t* slot = ring;
     auto landed = [&] {             // the slot's part is there, for every lane
@@ -590,8 +590,8 @@ __global__ void __launch_bounds__(Q4Smem<D, NT>::kThreads, 1) decode_q4_kernel(c
       issue(part);
       slot = slot == ring + (S - 1) * SM::kPart ? ring : slot + SM::kPart;
     };
-    // Parameters of tokens past the sequence's end become zero (they may be
-    // NaN).
+    // A value page's parameters of tokens past the sequence's end become zero
+    // (they may be NaN).
     auto clear_tail = [&](int nvalid) {
       for (int tok = nvalid + lane; tok < kQ4Page; tok += 32)
 #pragma unroll
@@ -602,7 +602,6 @@ __global__ void __launch_bounds__(Q4Smem<D, NT>::kThreads, 1) decode_q4_kernel(c
     for (int i = 0; i < n; ++i) {
       landed();
       const int nvalid = cur.len - cur.local * kQ4Page;   // tokens of this page (>= 1; 64 or more: all)
-      if (nvalid < kQ4Page) clear_tail(nvalid);
       if (seg == 0) {
         // The unit's rows went out with the part that followed the previous
         // unit's first keys, at the latest the last but one so far.
@@ -640,8 +639,10 @@ __global__ void __launch_bounds__(Q4Smem<D, NT>::kThreads, 1) decode_q4_kernel(c
           // 2^up takes the row's largest entry into [2^13, 2^14); clamped so
           // that the power and its inverse times 2^24 are normal numbers
           const int up = min(120, max(-100, 13 - ((int)(__float_as_uint(mx) >> 23) - 127)));
-          const float sc = __uint_as_float((uint32_t)(up + 127) << 23);
           const float inv = __uint_as_float((uint32_t)(24 - up + 127) << 23);
+          // (a negative scale turns q around)
+          const float sc = __uint_as_float((uint32_t)(up + 127) << 23 | (a.scale_log2 < 0.f && !(r & 1) ? 0x80000000u : 0u));
+          const float unit = __uint_as_float((uint32_t)(up - 24 + 127) << 23 | (__float_as_uint(sc) & 0x80000000u));
 #pragma unroll
           for (int j = 0; j < J; ++j) {
             const float lo = sc * 0.0625f;   // the codes of odd pairs are 2^4 larger
@@ -651,11 +652,11 @@ __global__ void __launch_bounds__(Q4Smem<D, NT>::kThreads, 1) decode_q4_kernel(c
             qf[t][2 * j + 1][1] = pack_half(f[j][6] * lo, f[j][7] * lo);
           }
           // rows 2 hc and 2 hc + 1 are this lane's head's q and rho
-          fs[t] = __shfl_sync(0xffffffffu, inv, 8 * hc) * a.scale_log2;
+          fs[t] = fmaxf(__shfl_sync(0xffffffffu, inv, 8 * hc) * fabsf(a.scale_log2), 0x1p-126f);   // (-inf stays -inf at scale 0)
           fa[t] = __shfl_sync(0xffffffffu, inv, 8 * hc + 4);
 #pragma unroll
           for (int g = 0; g < G; ++g) {
-            qs[t][g] = __shfl_sync(0xffffffffu, gsum[g], 8 * hc) * a.scale_log2;
+            qs[t][g] = __shfl_sync(0xffffffffu, gsum[g] * unit, 8 * hc);
             rs[t][g] = __shfl_sync(0xffffffffu, gsum[g], 8 * hc + 4);
           }
         }
@@ -696,15 +697,15 @@ __global__ void __launch_bounds__(Q4Smem<D, NT>::kThreads, 1) decode_q4_kernel(c
           lds_words<G>(slot + SM::kCodes + (16 * mt + r + 8 * half) * (4 * G), kp);
 #pragma unroll
           for (int t = 0; t < NT; ++t) {
-            float s = 0.f, p = 0.f, sm = 0.f, pmn = 0.f;
+            float s = 0.f, p = 0.f, pmn = -st.aref[t];   // (aref is 0 until the unit's first page has given it)
 #pragma unroll
             for (int g = 0; g < G; ++g) {
               s = fmaf(bf16_lo_f(kp[g]), acc[t][g][2 * half], s);
               p = fmaf(bf16_lo_f(kp[g]), acc[t][g][2 * half + 1], p);
-              sm = fmaf(bf16_hi_f(kp[g]), qs[t][g], sm);
+              s = fmaf(bf16_hi_f(kp[g]), qs[t][g], s);
               pmn = fmaf(bf16_hi_f(kp[g]), rs[t][g], pmn);
             }
-            x[t][2 * mt + half] = fmaf(fs[t], s, sm);
+            x[t][2 * mt + half] = s;   // over fs
             av[t][2 * mt + half] = fmaf(fa[t], p, pmn);
           }
         }
@@ -712,25 +713,30 @@ __global__ void __launch_bounds__(Q4Smem<D, NT>::kThreads, 1) decode_q4_kernel(c
       leave(std::integral_constant<bool, S % 2 != 0>{});   // part 2 i + S
       if (seg == 0) {   // the lane with token 0 (always valid) of the head
 #pragma unroll
-        for (int t = 0; t < NT; ++t) st.aref[t] = __shfl_sync(0xffffffffu, av[t][0], hc);
+        for (int t = 0; t < NT; ++t) {
+          st.aref[t] = __shfl_sync(0xffffffffu, av[t][0], hc);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) av[t][e] -= st.aref[t];
+        }
       }
-      if (nvalid < kQ4Page) {   // (their parameters were cleared, so their probe values are finite)
+
+      landed();
+      if (nvalid < kQ4Page) {   // tokens past the sequence's end weigh nothing, whatever their parameters
+        clear_tail(nvalid);
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
           for (int e = 0; e < 8; ++e)
-            if (16 * (e >> 1) + r + 8 * (e & 1) >= nvalid) x[t][e] = -INFINITY;
+            if (16 * (e >> 1) + r + 8 * (e & 1) >= nvalid) {
+              x[t][e] = -INFINITY;
+              av[t][e] = 0.f;
+            }
       }
-
-      landed();
-      if (nvalid < kQ4Page) clear_tail(nvalid);
 
       // ---- the running reference: the page's largest score, probe value and scale
       float mx[NT], ma[NT];
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) av[t][e] -= st.aref[t];
         mx[t] = max3(max3(x[t][0], x[t][1], x[t][2]), max3(x[t][3], x[t][4], x[t][5]), fmaxf(x[t][6], x[t][7]));
         ma[t] = max3(max3(fabsf(av[t][0]), fabsf(av[t][1]), fabsf(av[t][2])),
                      max3(fabsf(av[t][3]), fabsf(av[t][4]), fabsf(av[t][5])),
@@ -755,7 +761,7 @@ __global__ void __launch_bounds__(Q4Smem<D, NT>::kThreads, 1) decode_q4_kernel(c
           ma[t] = fmaxf(ma[t], __shfl_xor_sync(0xffffffffu, ma[t], off));
         }
         const float big = ma[t] * __uint_as_float(vmax);
-        const float m_new = fmaxf(st.m[t], mx[t] + lg2(fminf(fmaxf(big, 0x1p-60f), 0x1p60f)));
+        const float m_new = fmaxf(st.m[t], fs[t] * mx[t] + lg2(fminf(fmaxf(big, 0x1p-60f), 0x1p60f)));
         alpha[t] = ex2(st.m[t] - m_new);
         moved = moved || m_new != st.m[t];
         st.m[t] = m_new;
@@ -781,9 +787,9 @@ __global__ void __launch_bounds__(Q4Smem<D, NT>::kThreads, 1) decode_q4_kernel(c
       }
 
       if (cur.len < kQ4FineKeys)
-        q4_value_sums<D, NT, true>(st, slot, x, av);
+        q4_value_sums<D, NT, true>(st, slot, fs, x, av);
       else
-        q4_value_sums<D, NT, false>(st, slot, x, av);
+        q4_value_sums<D, NT, false>(st, slot, fs, x, av);
       leave(std::integral_constant<bool, S % 2 == 0>{});
       ++seg;
 
