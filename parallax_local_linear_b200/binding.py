@@ -736,10 +736,6 @@ def _raw(t):
     return None if t is None else t.data_ptr()
 
 
-def _raw0(t):
-    return 0 if t is None else t.data_ptr()
-
-
 PagePlan = collections.namedtuple("PagePlan", "seq_lens cu_seqlens slot_map positions pages_used")
 
 
@@ -793,20 +789,30 @@ def page_plan(cached_lens, new_lens, page_table, free_pages, *, num_rows, num_pa
     return PagePlan(seq_lens, cu, slots, positions, used)
 
 
-def _head_strides(name, t, batched):
-    """Element strides (batch entry, token, head) of [B, H, T, d] or packed [N, H, d] rows
+def _dense_strides(shape):
+    """Element strides (batch entry, token, head) of contiguous [B, H, T, d] or packed [N, H, d] rows."""
+    if len(shape) == 4:
+        _, h, t, d = shape
+        return h * t * d, d, t * d
+    return 0, shape[1] * shape[2], shape[2]
+
+
+def _head_strides(name, t, dense):
+    """The same of any tensor of that shape, ``dense`` being its contiguous strides
     (0 for a dimension of one entry, whatever torch says there)."""
+    if t.is_contiguous():
+        return dense
     s, n = t.stride(), t.shape
     if s[-1] != 1 and t.numel() > 0:
         raise ValueError(f"{name}'s last dimension must be contiguous")
-    if batched:
+    if len(n) == 4:
         return s[0] if n[0] > 1 else 0, s[2] if n[2] > 1 else 0, s[1] if n[1] > 1 else 0
     return 0, s[0] if n[0] > 1 else 0, s[1] if n[1] > 1 else 0
 
 
 def _norm_rope_call(q, rho, k, cos, sin, positions, weights, eps, norm, interleaved):
-    """Checks and parameters that the two directions share: (sets, params, device index,
-    batched), a set being (name, x, weight)."""
+    """Checks and parameters that the two directions share: (sets, params, device index), a
+    set being (name, x, weight)."""
     shape = q.shape
     batched = len(shape) == 4
     if not batched and len(shape) != 3:
@@ -857,7 +863,7 @@ def _norm_rope_call(q, rho, k, cos, sin, positions, weights, eps, norm, interlea
         raise ValueError(f"{T} tokens need as many rows of cos and sin, got {max_pos}")
     p = _NORM_ROPE.pack(B, T, d, rot, max_pos, 1 if interleaved else 0, 1 if norm else 0, _dtype_code(dtype), eps,
                         pos_stride)
-    return sets, p, index, batched
+    return sets, p, index
 
 
 def norm_rope(q, rho, k, cos, sin, positions=None, *, q_weight=None, rho_weight=None, k_weight=None, eps=1e-6,
@@ -875,22 +881,24 @@ def norm_rope(q, rho, k, cos, sin, positions=None, *, q_weight=None, rho_weight=
     may be the input itself: in place).  Returns (q, rho, k), None where the
     input is.
     """
-    sets, p, index, batched = _norm_rope_call(q, rho, k, cos, sin, positions, (q_weight, rho_weight, k_weight), eps,
-                                              norm, interleaved)
+    sets, p, index = _norm_rope_call(q, rho, k, cos, sin, positions, (q_weight, rho_weight, k_weight), eps, norm,
+                                     interleaved)
     done, rows = {"q": None, "rho": None, "k": None}, b""
     given = dict(zip(done, out)) if out is not None else None
     for name, x, w in sets:
-        strides = _head_strides(name, x, batched)
+        shape = x.shape
+        dense = y_strides = _dense_strides(shape)
         if given is None:
             y = torch.empty_like(x, memory_format=torch.contiguous_format)
         else:
             y = given.get(name)
-            if y is None or y.shape != x.shape:
-                raise ValueError(f"out's {name} must have shape {tuple(x.shape)}")
+            if y is None or y.shape != shape:
+                raise ValueError(f"out's {name} must have shape {tuple(shape)}")
             _on(index, "out's " + name, y, x.dtype)
+            y_strides = _head_strides("out's " + name, y, dense)
         done[name] = y
-        rows += _HEAD_ROWS.pack(x.data_ptr(), y.data_ptr(), 0 if w is None else w.data_ptr(), x.shape[1], *strides,
-                                *_head_strides("out's", y, batched))
+        rows += _HEAD_ROWS.pack(x.data_ptr(), y.data_ptr(), 0 if w is None else w.data_ptr(), shape[1],
+                                *_head_strides(name, x, dense), *y_strides)
     with _device_guard(index):
         st = lib.parallax_norm_rope(rows, len(sets), _raw(positions), _raw(cos), _raw(sin), p, _raw_stream(index))
     if st != 0:
@@ -907,30 +915,33 @@ def norm_rope_backward(dq, drho, dk, q, rho, k, cos, sin, positions=None, *, q_w
     over all rows; None without norm, and everything is None for a set that is.
     Without given weights, the gradients of weights of one are returned.
     """
-    sets, p, index, batched = _norm_rope_call(q, rho, k, cos, sin, positions, (q_weight, rho_weight, k_weight), eps,
-                                              norm, interleaved)
+    sets, p, index = _norm_rope_call(q, rho, k, cos, sin, positions, (q_weight, rho_weight, k_weight), eps, norm,
+                                     interleaved)
     names = ("q", "rho", "k")
     incoming, dxs, dws = dict(zip(names, (dq, drho, dk))), dict.fromkeys(names), dict.fromkeys(names)
     rows = grads = b""
     no_strides = (0,) * 3
+    if norm:
+        dws.update(zip((name for name, _, _ in sets),
+                       q.new_empty((len(sets), q.shape[-1]), dtype=torch.float32).unbind()))
     for name, x, w in sets:
-        dy = incoming[name]
-        if dy is None or dy.shape != x.shape:
-            raise ValueError(f"d{name} must have shape {tuple(x.shape)}")
+        dy, shape = incoming[name], x.shape
+        if dy is None or dy.shape != shape:
+            raise ValueError(f"d{name} must have shape {tuple(shape)}")
         _on(index, "d" + name, dy, x.dtype)
+        dense = _dense_strides(shape)
         dx = dxs[name] = torch.empty_like(x, memory_format=torch.contiguous_format)
-        if norm:
-            dws[name] = torch.empty(x.shape[-1], dtype=torch.float32, device=x.device)
-        rows += _HEAD_ROWS.pack(x.data_ptr(), 0, _raw0(w), x.shape[1], *_head_strides(name, x, batched), *no_strides)
-        grads += _HEAD_GRADS.pack(dy.data_ptr(), dx.data_ptr(), _raw0(dws[name]),
-                                  *_head_strides("d" + name, dy, batched), *_head_strides("d" + name, dx, batched))
+        rows += _HEAD_ROWS.pack(x.data_ptr(), 0, 0 if w is None else w.data_ptr(), shape[1],
+                                *_head_strides(name, x, dense), *no_strides)
+        grads += _HEAD_GRADS.pack(dy.data_ptr(), dx.data_ptr(), dws[name].data_ptr() if norm else 0,
+                                  *_head_strides("d" + name, dy, dense), *dense)
     with _device_guard(index):
         ws, nbytes = None, 0
         if norm:
             nbytes = lib.parallax_norm_rope_backward_workspace_size(p, len(sets))
             if nbytes == SIZE_MAX:
                 raise ParallaxError(2, "parallax_norm_rope_backward_workspace_size")
-            ws = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
+            ws = q.new_empty(nbytes, dtype=torch.uint8)
         st = lib.parallax_norm_rope_backward(rows, grads, len(sets), _raw(positions), _raw(cos), _raw(sin), _raw(ws),
                                              nbytes, p, _raw_stream(index))
     if st != 0:
