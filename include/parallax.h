@@ -539,7 +539,8 @@ plx_status parallax_norm_rope(const plx_head_rows* rows, int32_t num_sets, const
  *   workspace   device, >= parallax_norm_rope_backward_workspace_size() bytes,
  *               16-byte aligned; no initialisation needed.  May be NULL when no dw is asked for.
  * Every output element is written exactly once and every sum has a fixed
- * order (no atomics, deterministic).  Two launches, one without any dw. */
+ * order (no atomics, deterministic).  Two launches, one without any dw.
+ * T == 0 writes zeros to dw. */
 typedef struct plx_head_grads {
   const void* dy;
   void* dx;

@@ -70,14 +70,16 @@ plx_status validate_norm_rope(const plx_head_rows* rows, const plx_head_grads* g
     if ((int64_t)r.heads * p->batch * p->tokens >= (int64_t)INT32_MAX || r.heads > 16384) return PLX_ERR_UNSUPPORTED;
     if ((int64_t)p->batch * p->tokens >= (int64_t)INT32_MAX / 32) return PLX_ERR_UNSUPPORTED;
     if (r.w && (!p->norm || !aligned(r.w, 16))) return PLX_ERR_INVALID_ARG;
+    const bool any = p->tokens > 0;   // (an empty tensor has no address)
     if (!aligned(r.x, 16) || !strides_ok(r.x_stride, 3, elt)) return PLX_ERR_INVALID_ARG;
     const int64_t count[3] = {p->batch, p->tokens, r.heads};
-    if (!distinct(grads ? grads[i].dx_stride : r.y_stride, count, 3)) return PLX_ERR_INVALID_ARG;
+    if (any && !distinct(grads ? grads[i].dx_stride : r.y_stride, count, 3)) return PLX_ERR_INVALID_ARG;
     if (grads == nullptr) {
-      if (!r.x || !r.y || !aligned(r.y, 16) || !strides_ok(r.y_stride, 3, elt)) return PLX_ERR_INVALID_ARG;
+      if ((any && (!r.x || !r.y)) || !aligned(r.y, 16) || !strides_ok(r.y_stride, 3, elt)) return PLX_ERR_INVALID_ARG;
     } else {
       const plx_head_grads& g = grads[i];
-      if ((!r.x && p->norm) || !g.dy || !g.dx || !aligned(g.dy, 16) || !aligned(g.dx, 16)) return PLX_ERR_INVALID_ARG;
+      if (any && ((!r.x && p->norm) || !g.dy || !g.dx)) return PLX_ERR_INVALID_ARG;
+      if (!aligned(g.dy, 16) || !aligned(g.dx, 16)) return PLX_ERR_INVALID_ARG;
       if (!strides_ok(g.dy_stride, 3, elt) || !strides_ok(g.dx_stride, 3, elt)) return PLX_ERR_INVALID_ARG;
       if (g.dw && (!p->norm || !aligned(g.dw, 4))) return PLX_ERR_INVALID_ARG;
     }

@@ -194,6 +194,52 @@ def test_peaked_rows_and_negative_scale(px):
     _check(px, _inputs([500], 4, 2, 128, seed=13), scale=0.0)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("kv_len", [1, 63, 64, 200, 1000])
+@pytest.mark.parametrize("H,Hkv", [(4, 2), (7, 1)])
+def test_contiguous_without_lengths(px, d, kv_len, H, Hkv):
+    # every sequence has kv_len tokens; kv_len need not fill its last page
+    x = _inputs([kv_len] * 3, H, Hkv, d, paged=False, seed=kv_len)
+    ref, bound = _reference(x, 0.1)
+    got = px.decode_q4(x["q"], x["rho"], x["cache"], 0.1, kv_len=kv_len, out_dtype=torch.float32)
+    assert (np.abs(to_f64(got) - ref) <= bound * (1 + U) + U * np.abs(ref)).all()
+    if kv_len % 64 == 0:
+        assert torch.equal(px.decode_q4(x["q"], x["rho"], x["cache"], 0.1, out_dtype=torch.float32), got)
+
+
+def test_a_pool_past_32_bits(px):
+    # 4.9 GB of blocks: pages, slots and rows beyond 2^32 bytes
+    P, Hkv, d, n = 265_000, 2, 128, 150
+    cache = torch.empty(P, Hkv, 72 * d, dtype=torch.uint8, device="cuda")
+    pages = torch.tensor([[P - 1, 3, P - 7]], dtype=torch.int32, device="cuda")
+    t = torch.arange(n, device="cuda")
+    slots = pages[0, t // 64].long() * 64 + t % 64
+    k, v = (torch.randn(n, Hkv, d, device="cuda").bfloat16() for _ in range(2))
+    px.cache_append_q4(k, v, slots, cache)
+    small = px.q4_cache(3, Hkv, d)
+    px.cache_append_q4(k, v, t, small)
+    for a, b in zip(px.cache_gather_q4(cache, slots), px.cache_gather_q4(small, t)):
+        assert torch.equal(a, b)
+    q, rho = (torch.randn(1, 4, d, device="cuda").bfloat16() for _ in range(2))
+    lens = torch.tensor([n], dtype=torch.int32, device="cuda")
+    got = px.decode_q4(q, rho, cache, seq_lens=lens, page_table=pages)
+    assert torch.equal(got, px.decode_q4(q, rho, small, seq_lens=lens,
+                                         page_table=torch.arange(3, dtype=torch.int32, device="cuda")[None]))
+    assert px.last_device_error() == 0
+
+
+def test_not_a_number_stays_in_its_rows(px):
+    # NaN or infinities in one query, probe or key row reach that row's outputs and no other
+    x = _inputs([100, 70], 4, 2, 128, seed=40)
+    want = _run(px, x, None)
+    x["q"][0, 1, 5] = float("nan")
+    x["rho"][1, 2, 7] = float("inf")
+    got = _run(px, x, None)
+    bad = torch.zeros(2, 4, dtype=torch.bool, device="cuda")
+    bad[0, 1] = bad[1, 2] = True
+    assert torch.equal(got[~bad], want[~bad]) and not torch.isfinite(got[bad].float()).any()
+
+
 def test_bad_lengths_and_pages_are_reported(px):
     x = _inputs([100, 70], 4, 2, 64, seed=14)
     x["table"][0, 1] = x["cache"].shape[0]

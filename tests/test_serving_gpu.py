@@ -385,6 +385,35 @@ def test_norm_rope_autograd_of_single_sets_and_captured(px):
                        px.norm_rope_backward(torch.ones_like(q), None, None, q.detach(), None, None, cos, sin, norm=False)[0])
 
 
+def test_norm_rope_without_tokens(px):
+    q, w = torch.empty(0, 4, 64, device="cuda").bfloat16(), torch.ones(64, device="cuda").bfloat16()
+    cos, sin = _tables(4, 64)
+    y, none, z = px.norm_rope(q, None, q, cos, sin, q_weight=w)
+    assert y.shape == q.shape and z.shape == q.shape and none is None
+    g = px.norm_rope_backward(q, None, q, q, None, q, cos, sin, q_weight=w)
+    assert g[0].shape == q.shape and (g[3] == 0).all() and g[4] is None and (g[5] == 0).all()
+    b = torch.empty(2, 4, 0, 128, device="cuda")
+    assert px.norm_rope(b, None, None, None, None)[0].shape == b.shape
+    assert (px.norm_rope_backward(b, None, None, b, None, None, None, None)[3] == 0).all()
+
+
+def test_norm_rope_past_32_bits(px):
+    # more than 2^31 elements: rows on both sides of the border
+    N, H, d = 4_300_000, 4, 128
+    x = torch.empty(N, H, d, dtype=torch.bfloat16, device="cuda")
+    rows = torch.tensor([0, 1, N // 2, 2 ** 31 // (H * d) - 1, 2 ** 31 // (H * d), N - 2, N - 1], device="cuda")
+    x.zero_()
+    x[rows] = torch.randn(len(rows), H, d, device="cuda").bfloat16()
+    cos, sin = _tables(64, d)
+    pos = (torch.arange(N, device="cuda") % 64).int()
+    y = px.norm_rope(x, None, None, cos, sin, pos)[0]
+    assert torch.equal(y[rows], px.norm_rope(x[rows], None, None, cos, sin, pos[rows])[0])
+    assert not y[2:1000].any() and not y[N - 1000:N - 2].any()
+    dx = px.norm_rope_backward(x, None, None, x, None, None, cos, sin, pos)
+    want = px.norm_rope_backward(x[rows], None, None, x[rows], None, None, cos, sin, pos[rows])
+    assert torch.equal(dx[0][rows], want[0]) and torch.allclose(dx[3], want[3], rtol=1e-5, atol=1e-5)
+
+
 def test_rows_of_one_entry_have_any_stride(px):
     # torch leaves odd strides on dimensions of one entry; rows still start at 16 bytes
     base = torch.randn(4096, device="cuda").bfloat16()
