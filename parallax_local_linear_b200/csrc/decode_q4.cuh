@@ -27,10 +27,11 @@
 // Ranges.  q and rho are scaled by a power of two to at most 2^14 per row
 // (exact: they are bf16).  e s and e a s have to fit fp16, whatever the size of
 // s and a: the running reference is not the largest score alone but
-//     M = max_i x_i + log2(max_i,g s_ig max_i(1, |a_i|)),      p_i = 2^(x_i - M + 14)
-// with x_i the score in powers of two (maxima of a page; M never falls), so
-// every product is at most 2^14, and nothing above 2^-38 of the largest is
-// lost.  Sequences of fewer than 128 keys add a second product with the
+//     M = max_i x_i + log2(max_i,g s_ig max_i(1, |a_i|)),      p_i = 2^(x_i - M + 10)
+// with x_i the score in powers of two (maxima of a page).  M stays until a page
+// needs it to be more than 5 larger, so every product is at most 2^15, nothing
+// above 2^-34 of the largest is lost, and after a unit's first page the
+// sums are hardly ever rescaled.  Sequences of fewer than 128 keys add a second product with the
 // weights' low halves (22 bits together): with |a| about 10 the rounding to
 // 2^-12 would show in rows of a few keys.  Over more keys it averages out
 // (and the output is a sum of as many terms); without it a page takes 64
@@ -76,6 +77,10 @@ struct DecodeQ4Args {
 
 // Sequences with fewer keys than this get 22-bit weights in the value product.
 constexpr int kQ4FineKeys = 128;
+
+// Weights against a new reference are at most 2^kQ4Top, and 2^kQ4Slack times
+// that before it moves: together below fp16's 2^16.
+constexpr float kQ4Top = 10.f, kQ4Slack = 5.f;
 
 // Warps of a CTA (one CTA per SM) and its shared memory.  A ring slot holds
 // one half of a block, K's or V's codes and parameters.
@@ -373,7 +378,7 @@ __device__ __forceinline__ void q4_value_sums(Q4WarpState<D, NT>& st, const uint
       lds_words<G>(slot + SM::kCodes + (16 * kk + r + 8 * half) * (4 * G), vp);
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
-        const float p = ex2(fmaf(fs[t], x[t][e], 14.f - st.m[t])), pa = p * av[t][e];
+        const float p = ex2(fmaf(fs[t], x[t][e], kQ4Top - st.m[t])), pa = p * av[t][e];
         st.l[t] += p;
         st.c[t] += pa;
 #pragma unroll
@@ -752,7 +757,7 @@ __global__ void __launch_bounds__(Q4Smem<D, NT>::kThreads, 1) decode_q4_kernel(c
         vmax = __reduce_max_sync(0xffffffffu, *reinterpret_cast<uint32_t*>(&m2) << 16);   // (scales are in the low half)
       }
       bool moved = false;
-      float alpha[NT];
+      float m_new[NT];
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
 #pragma unroll
@@ -761,28 +766,29 @@ __global__ void __launch_bounds__(Q4Smem<D, NT>::kThreads, 1) decode_q4_kernel(c
           ma[t] = fmaxf(ma[t], __shfl_xor_sync(0xffffffffu, ma[t], off));
         }
         const float big = ma[t] * __uint_as_float(vmax);
-        const float m_new = fmaxf(st.m[t], fs[t] * mx[t] + lg2(fminf(fmaxf(big, 0x1p-60f), 0x1p60f)));
-        alpha[t] = ex2(st.m[t] - m_new);
-        moved = moved || m_new != st.m[t];
-        st.m[t] = m_new;
+        const float need = fs[t] * mx[t] + lg2(fminf(fmaxf(big, 0x1p-60f), 0x1p60f));
+        m_new[t] = need > st.m[t] + kQ4Slack ? need : st.m[t];
+        moved = moved || m_new[t] != st.m[t];
       }
       if (__any_sync(0xffffffffu, moved)) {
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
+          const float alpha = m_new[t] == st.m[t] ? 1.f : ex2(st.m[t] - m_new[t]);
+          st.m[t] = m_new[t];
 #pragma unroll
           for (int k = 0; k < 2 * J; ++k) {
-            st.o[t][k][0] *= alpha[t];
-            st.o[t][k][1] *= alpha[t];
-            st.o[t][k][2] *= alpha[t];
-            st.o[t][k][3] *= alpha[t];
+            st.o[t][k][0] *= alpha;
+            st.o[t][k][1] *= alpha;
+            st.o[t][k][2] *= alpha;
+            st.o[t][k][3] *= alpha;
           }
 #pragma unroll
           for (int g = 0; g < G; ++g) {
-            st.pm[t][g][0] *= alpha[t];
-            st.pm[t][g][1] *= alpha[t];
+            st.pm[t][g][0] *= alpha;
+            st.pm[t][g][1] *= alpha;
           }
-          st.l[t] *= alpha[t];
-          st.c[t] *= alpha[t];
+          st.l[t] *= alpha;
+          st.c[t] *= alpha;
         }
       }
 

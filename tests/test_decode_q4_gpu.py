@@ -228,6 +228,21 @@ def test_a_pool_past_32_bits(px):
     assert px.last_device_error() == 0
 
 
+@pytest.mark.parametrize("step", [-4.0, 0.7, 1.9, 4.0])
+@pytest.mark.parametrize("H", [4, 8])
+def test_scores_and_values_that_rise_from_page_to_page(px, step, H):
+    # every page's scores lie about `step` powers of two above (or below) the last page's, its
+    # values' scales one power above: the running reference moves at every page, at some, at none
+    x = _inputs([1500, 130, 90], H, 1, 128, paged=False, seed=7)
+    x["q"] = x["q"].abs()
+    par = x["cache"][..., 64 * 128:].view(torch.bfloat16).view(3, -1, 2, 64, 2, 2)
+    p = torch.arange(par.shape[1], device="cuda").view(1, -1, 1, 1)
+    mean = float(x["q"].float().sum(-1).mean())
+    par[:, :, 0, :, :, 1] = (par[:, :, 0, :, :, 1] + step * np.log(2.0) * 128 ** 0.5 / mean * p).bfloat16()
+    par[:, :, 1] = (par[:, :, 1].float() * torch.exp2((p % 8).float())[..., None]).bfloat16()
+    _check(px, x)
+
+
 def test_not_a_number_stays_in_its_rows(px):
     # NaN or infinities in one query, probe or key row reach that row's outputs and no other
     x = _inputs([100, 70], 4, 2, 128, seed=40)
