@@ -11,14 +11,7 @@
 // so the tensor cores multiply bare codes.  A code masked out of its word is
 // already an fp16 number: bits 0..3 of a half are the subnormal n 2^-24 and bits
 // 4..7 are n 2^-20.  One AND makes two operands; the powers of two are taken
-// out of the queries on one side and of the results on the other.  The value
-// product also takes two codes of a half at once, n_0 + 16 n_1 (bits 0..7), for its even
-// columns: the odd columns' sums are there anyway and are taken off at the
-// end.  That saves one of five integer instructions (decode_long 190.6 to
-// 186.8 us) and costs an even column fp32 roundings of sums larger than its own
-// by 16 n_1, never more than 2^8 codes.  (The weights' roundings are the same in
-// both and go with the difference; a column of zero codes comes out as exactly
-// its minima.)
+// out of the queries on one side and of the results on the other.
 //
 // Operands (mma.sync m16n8k16, fp16 in, fp32 sums; the contraction has 8 columns
 // for 4 heads, far below what a tcgen05 tile needs, and its operands would have
@@ -38,12 +31,11 @@
 // with x_i the score in powers of two (maxima of a page).  M stays until a page
 // needs it to be more than 5 larger, so every product is at most 2^15, nothing
 // above 2^-34 of the largest is lost, and after a unit's first page the
-// sums are hardly ever rescaled.  Sequences of fewer than 128 keys keep the
-// columns apart and add a second product with the weights' low halves (22 bits
-// together): with |a| about 10 the rounding to 2^-12 would show in rows of a few
-// keys.  Over more keys it averages out (and the output is a sum of as many
-// terms); without it a page takes 64 products instead of 96 and the call 13%
-// less time.
+// sums are hardly ever rescaled.  Sequences of fewer than 128 keys add a second product with the
+// weights' low halves (22 bits together): with |a| about 10 the rounding to
+// 2^-12 would show in rows of a few keys.  Over more keys it averages out
+// (and the output is a sum of as many terms); without it a page takes 64
+// products instead of 96 and the call 13% less time.
 // a_i is taken relative to the probe value of the first token the warp sees of
 // a unit; any constant leaves the output unchanged, and merging pieces shifts
 // c and O2 to a common one.
@@ -165,12 +157,6 @@ __device__ __forceinline__ float lg2(float x) {
   float y;
   asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
-}
-
-// The codes at bits 0..7 (odd: 8..15) of both halves of a word, two to a half:
-// as an fp16 number the subnormal (n_0 + 16 n_1) 2^-24.
-__device__ __forceinline__ uint32_t code_pairs(uint32_t w, bool odd) {
-  return odd ? __byte_perm(w, 0, 0x4341) : w & 0x00ff00ffu;
 }
 
 // N consecutive words of shared memory.
@@ -316,9 +302,8 @@ struct Q4WarpState {
     }
   }
   // Sums over the lanes that hold other tokens of the same heads; the codes'
-  // powers of two, the odd columns' share of the even ones' sums and the
-  // minima's sums go into o.
-  __device__ __forceinline__ void close(bool fine) {
+  // powers of two and the minima's sums go into o.
+  __device__ __forceinline__ void close() {
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
 #pragma unroll
@@ -333,8 +318,8 @@ struct Q4WarpState {
       }
 #pragma unroll
       for (int i = 0; i < 2 * J; ++i) {
-        o[t][i][0] = fmaf(o[t][i][0] - (fine ? 0.f : o[t][i][2]), 16777216.f, pm[t][i / 4][0]);
-        o[t][i][1] = fmaf(o[t][i][1] - (fine ? 0.f : o[t][i][3]), 16777216.f, pm[t][i / 4][1]);
+        o[t][i][0] = fmaf(o[t][i][0], 16777216.f, pm[t][i / 4][0]);
+        o[t][i][1] = fmaf(o[t][i][1], 16777216.f, pm[t][i / 4][1]);
         o[t][i][2] = fmaf(o[t][i][2], 1048576.f, pm[t][i / 4][0]);
         o[t][i][3] = fmaf(o[t][i][3], 1048576.f, pm[t][i / 4][1]);
       }
@@ -419,10 +404,10 @@ __device__ __forceinline__ void q4_value_sums(Q4WarpState<D, NT>& st, const uint
       uint32_t av4[4][4];
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        const uint32_t u0 = code_pairs(w0[j + q / 2], q & 1), u1 = code_pairs(w1[j + q / 2], q & 1);
-        av4[q][0] = kFine ? u0 & 0x000f000fu : u0;
+        const uint32_t u0 = w0[j + q / 2] >> (8 * (q & 1)), u1 = w1[j + q / 2] >> (8 * (q & 1));
+        av4[q][0] = u0 & 0x000f000fu;
         av4[q][1] = u0 & 0x00f000f0u;
-        av4[q][2] = kFine ? u1 & 0x000f000fu : u1;
+        av4[q][2] = u1 & 0x000f000fu;
         av4[q][3] = u1 & 0x00f000f0u;
       }
 #pragma unroll
@@ -807,8 +792,7 @@ __global__ void __launch_bounds__(Q4Smem<D, NT>::kThreads, 1) decode_q4_kernel(c
         }
       }
 
-      const bool fine = cur.len < kQ4FineKeys;
-      if (fine)
+      if (cur.len < kQ4FineKeys)
         q4_value_sums<D, NT, true>(st, slot, fs, x, av);
       else
         q4_value_sums<D, NT, false>(st, slot, fs, x, av);
@@ -817,7 +801,7 @@ __global__ void __launch_bounds__(Q4Smem<D, NT>::kThreads, 1) decode_q4_kernel(c
 
       if (cur.local + 1 == cur.tiles && (i + 1 < n || seg == cur.tiles)) {
         // the unit ends here: finish it, or leave the run's first piece
-        st.close(fine);
+        st.close();
         if (seg == cur.tiles) {
           st.write_out(a, cur.b, cur.hu);
         } else {
@@ -833,8 +817,7 @@ __global__ void __launch_bounds__(Q4Smem<D, NT>::kThreads, 1) decode_q4_kernel(c
       if (i + 1 < n) cur.next_page(sp);
     }
     if (seg > 0) {   // the run's last piece, into the ring, which holds no copy any more
-      const bool fine = cur.len < kQ4FineKeys;
-      st.close(fine);
+      st.close();
       st.deposit(reinterpret_cast<float*>(ring));
       if (lane == 0) {
         meta[warp * 8 + 3] = cur.b * a.Hkv + cur.hu;

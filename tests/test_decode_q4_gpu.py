@@ -243,31 +243,6 @@ def test_scores_and_values_that_rise_from_page_to_page(px, step, H):
     _check(px, x)
 
 
-@pytest.mark.parametrize("H", [4, 8])
-def test_small_codes_beside_large_ones(px, H):
-    # From 128 keys on an even column is the difference of sums over n_0 + 16 n_1 and 16 n_1, n_1 the
-    # code of the odd column beside it.  Sixteen tokens are one addition, which may truncate (2u), so
-    # both are off by (n / 16 + 8) 2u of at most 16 n_1 sum w (1 + |abar| + |a| + 2 A) s and their own.
-    x = _inputs([300, 128, 1000, 127, 64], H, 1, 128, seed=12)
-    codes = x["cache"][..., 64 * 64:64 * 128].view(*x["cache"].shape[:-1], 32, 8, 4, 4)   # pair, r, j, bytes
-    codes[..., :2, :] = 0xf0        # group 0: even columns 0, odd columns 15
-    codes[..., 2:, :] = 0xf1        # group 1: 1 and 15
-    par = x["cache"][..., 64 * 128:].view(torch.bfloat16).view(*x["cache"].shape[:-1], 2, 64, 2, 2)
-    par[..., 1, :, :, 1] = torch.where(par[..., 1, :, :, 1].isnan(), float("nan"), 0.0)
-    scale = 128 ** -0.5
-    ref, bound = _reference(x, scale)
-    got = to_f64(_run(px, x, scale, out_dtype=torch.float32))
-    assert (got[..., 0:64:2] == 0).all()
-    for b, n in enumerate(x["lens"]):
-        k, v = (t.reshape(-1, 128)[:n] for t in S.q4_unblock(
-            x["cache"].cpu().numpy()[x["table"][b, :-(-n // 64)].cpu().numpy(), 0], 128))
-        for h in range(H):
-            w, a = oracle.softmax_weights(scale * (k @ to_f64(x["q"])[b, h])), k @ to_f64(x["rho"])[b, h]
-            sums = (w * (1 + abs(w @ a) + np.abs(a) + 2 * np.abs(a).max())) @ (16 * v[:, 1::2])
-            bound[b, h, 0::2] += (n / 16 + 8) * 4 * U * sums
-    assert (np.abs(got - ref) <= bound * (1 + U) + U * np.abs(ref)).all()
-
-
 def test_not_a_number_stays_in_its_rows(px):
     # NaN or infinities in one query, probe or key row reach that row's outputs and no other
     x = _inputs([100, 70], 4, 2, 128, seed=40)
