@@ -31,11 +31,12 @@
 // with x_i the score in powers of two (maxima of a page).  M stays until a page
 // needs it to be more than 5 larger, so every product is at most 2^15, nothing
 // above 2^-34 of the largest is lost, and after a unit's first page the
-// sums are hardly ever rescaled.  Sequences of fewer than 128 keys add a second product with the
-// weights' low halves (22 bits together): with |a| about 10 the rounding to
-// 2^-12 would show in rows of a few keys.  Over more keys it averages out
-// (and the output is a sum of as many terms); without it a page takes 64
-// products instead of 96 and the call 13% less time.
+// sums are hardly ever rescaled (1.5% of the time).  Sequences of
+// fewer than 128 keys add a second product with the weights' low halves (22 bits
+// together): with |a| about 10 the rounding to 2^-12 would show in rows of a few
+// keys.  Over more keys it averages out (and the output is a sum of as many
+// terms); without it a page takes 64 products instead of 96 and the call 13%
+// less time.
 // a_i is taken relative to the probe value of the first token the warp sees of
 // a unit; any constant leaves the output unchanged, and merging pieces shifts
 // c and O2 to a common one.
@@ -49,6 +50,11 @@
 // inside a run are finished in registers; pieces of cut units are merged in
 // the CTA after one barrier, and across CTAs in the workspace, by the last CTA
 // that finishes a piece (a counter per unit, which that CTA takes back to zero).
+//
+// Measured (device time): 32 sequences of 32768 keys, 32/8 heads, d = 128 (1.21
+// GB) 191 us, 6.3 TB/s; 8 of 4096, 16/8 heads (38 MB) 16.7 us, of which set-up,
+// first pages and merge take 8; 16 of 16384 and 4 KV heads (151 MB) 35 us with
+// 4 query heads each and 49 us with 8.
 #pragma once
 
 #include <type_traits>

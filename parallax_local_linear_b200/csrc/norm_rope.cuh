@@ -15,6 +15,10 @@
 // whole 16-byte vectors the partner's came by four shuffles and was unpacked a
 // second time.  A group of lanes takes several heads of one token, so a
 // token's cos and sin are read once for them.
+//
+// Measured (device time, bf16, d = 128): 4 x 8192 tokens of 3 x 16 heads forward (810
+// MB) 127 to 136 us, 5.9 to 6.4 TB/s; 4 x 8192 of 16 + 16 + 4 heads backward
+// (910 MB) 149 us, 6.1 TB/s; 8 tokens forward 2.3 us.
 #pragma once
 
 #include "ptx.cuh"
@@ -51,7 +55,7 @@ struct NormRopeArgs {
 };
 
 // Rows are read once and written once: neither way through L1, and out of L2
-// first (rope_prefill 147 to 133 us).
+// first (810 MB forward: 147 to 133 us).
 __device__ __forceinline__ uint2 load_row(const void* p) {
   uint2 v;
   asm volatile("ld.global.L1::no_allocate.v2.u32 {%0, %1}, [%2];"
@@ -272,7 +276,7 @@ __global__ void __launch_bounds__(kNrThreads, kNrBwdCtasPerSm) norm_rope_bwd_ker
   // An item is kNrBwdHeads heads of a token.  The next item's rows come into the
   // warp's own part of shared memory while it works on the current one (loading
   // two rows at a time into registers left 24 warps waiting: 231 against 177 us
-  // for rope_grad).
+  // for 910 MB).
   struct Item {
     const T* x;
     const T* dy;

@@ -10,7 +10,8 @@
 // grid, and a row finds its request by a binary search in shared memory.  A
 // row's page is an old table entry or a free page found from the prefix sum,
 // never a table entry that this launch writes, so rows and table entries are
-// written in any order.
+// written in any order.  Latency bounds it: 128 requests of one row take 3.5 us,
+// 1024 requests of 300 000 rows (3.6 MB) 7 us, device time.
 #pragma once
 
 #include "ptx.cuh"
