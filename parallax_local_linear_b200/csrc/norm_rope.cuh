@@ -284,24 +284,28 @@ __global__ void __launch_bounds__(kNrThreads, kNrBwdCtasPerSm) norm_rope_bwd_ker
     int heads, pos;      // rows to write; position, or -1
   };
   // The group's items are `groups` tokens apart, chunk after chunk; stepping
-  // through them needs no division.
-  int chunk = 0, b = 0;
+  // through long rows needs no division.
+  int chunk = items > 0 ? 0 : set.chunks, b = 0;
   uint32_t t = group;
   auto settle = [&] {
-    while (b < a.B && t >= (uint32_t)a.T) {
+    if (t >= (uint32_t)a.T) {
       t -= a.T;
       ++b;
+      if (t >= (uint32_t)a.T) {
+        b += t / a.T;
+        t %= a.T;
+      }
     }
-    while (b >= a.B && chunk < set.chunks) {
+    if (b >= a.B) {
       b -= a.B;
       ++chunk;
-      while (b < a.B && t >= (uint32_t)a.T) {
-        t -= a.T;
-        ++b;
+      if (b >= a.B) {
+        chunk += b / a.B;
+        b %= a.B;
       }
     }
   };
-  settle();
+  if (items > 0) settle();
   auto here = [&] {
     Item it;
     const bool in = chunk < set.chunks;

@@ -397,6 +397,21 @@ def test_norm_rope_without_tokens(px):
     assert (px.norm_rope_backward(b, None, None, b, None, None, None, None)[3] == 0).all()
 
 
+@pytest.mark.parametrize("B,T", [(20000, 1), (3001, 3), (1, 9000)])
+@pytest.mark.parametrize("H", [1, 4, 9])
+def test_norm_rope_backward_of_many_short_rows(px, B, T, H):
+    # the batched rows are the packed ones with their positions written out
+    x, dy = (torch.randn(B, H, T, 64, device="cuda").bfloat16() for _ in range(2))
+    w, (cos, sin) = torch.randn(64, device="cuda").bfloat16(), _tables(T, 64)
+    rows = lambda v: v.transpose(1, 2).reshape(B * T, H, 64)
+    dx, _, _, dw, _, _ = px.norm_rope_backward(dy, None, None, x, None, None, cos, sin, q_weight=w)
+    pos = torch.arange(T, device="cuda").repeat(B).int()
+    px_, _, _, pw, _, _ = px.norm_rope_backward(rows(dy), None, None, rows(x), None, None, cos, sin, pos, q_weight=w)
+    assert torch.equal(rows(dx), px_)
+    # the same addends, which the same groups take in the same order
+    assert torch.equal(dw, pw)
+
+
 def test_norm_rope_past_32_bits(px):
     # more than 2^31 elements: rows on both sides of the border
     N, H, d = 4_300_000, 4, 128
