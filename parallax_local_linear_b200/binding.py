@@ -10,7 +10,6 @@ no fallback.
 from __future__ import annotations
 
 import collections
-import contextlib
 import ctypes
 import os
 import struct
@@ -722,14 +721,46 @@ def _check_shape(name, t, shape):
         raise ValueError(f"{name} must be contiguous")
 
 
+def _check_contiguous(name, t):
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
 _raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
-_no_guard = contextlib.nullcontext()
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
-def _device_guard(index):
-    """The library launches on the current device: make it the tensors' own."""
-    return _no_guard if torch.cuda.current_device() == index else torch.cuda.device(index)
+def _call(index, fn, *args):
+    """fn(*args, stream) with device ``index`` current (the library launches on the
+    current device), on that device's current stream."""
+    if _current_device() == index:
+        st = fn(*args, _raw_stream(index))
+    else:
+        with torch.cuda.device(index):
+            st = fn(*args, _raw_stream(index))
+    if st != 0:
+        raise ParallaxError(st, fn.__name__)
+
+
+def _workspace_size(index, status, fn, *args):
+    """fn(*args), bytes, with device ``index`` current; ``status`` is raised for what fn refuses."""
+    if _current_device() == index:
+        nbytes = fn(*args)
+    else:
+        with torch.cuda.device(index):
+            nbytes = fn(*args)
+    if nbytes == SIZE_MAX:
+        raise ParallaxError(status, fn.__name__)
+    return nbytes
+
+
+def _capturing(index):
+    """Whether device ``index``'s current stream is being captured."""
+    if _current_device() == index:
+        return torch.cuda.is_current_stream_capturing()
+    with torch.cuda.device(index):
+        return torch.cuda.is_current_stream_capturing()
 
 
 def _raw(t):
@@ -758,11 +789,11 @@ def page_plan(cached_lens, new_lens, page_table, free_pages, *, num_rows, num_pa
     """
     if cached_lens.dim() != 1 or page_table.dim() != 2 or free_pages.dim() != 1:
         raise ValueError("cached_lens and free_pages must be 1-D and page_table 2-D")
-    B, width = cached_lens.shape[0], page_table.shape[1]
-    _check_shape("cached_lens", cached_lens, (B,))
+    (B,), width = cached_lens.shape, page_table.shape[1]
+    _check_contiguous("cached_lens", cached_lens)
     _check_shape("new_lens", new_lens, (B,))
     _check_shape("page_table", page_table, (B, width))
-    _check_shape("free_pages", free_pages, free_pages.shape)
+    _check_contiguous("free_pages", free_pages)
     if free_head is not None and free_head.numel() != 1:
         raise ValueError("free_head must hold one element")
     index = _cuda_index("cached_lens", cached_lens)
@@ -778,14 +809,10 @@ def page_plan(cached_lens, new_lens, page_table, free_pages, *, num_rows, num_pa
     slots, seq_lens, cu, positions, used = cached_lens.new_empty(3 * num_rows + 2 * B + 2).split_with_sizes(
         (2 * num_rows, B, B + 1, num_rows, 1))
     slots = slots.view(torch.int64)
-    with _device_guard(index):
-        st = lib.parallax_page_plan(cached_lens.data_ptr(), new_lens.data_ptr(), page_table.data_ptr(),
-                                    free_pages.data_ptr(), _raw(free_head), seq_lens.data_ptr(), cu.data_ptr(),
-                                    slots.data_ptr(), positions.data_ptr(), used.data_ptr(),
-                                    _PAGE_PLAN.pack(B, num_rows, PAGE_SIZE, num_pages, width, free_pages.shape[0]),
-                                    _raw_stream(index))
-    if st != 0:
-        raise ParallaxError(st, "parallax_page_plan")
+    _call(index, lib.parallax_page_plan, cached_lens.data_ptr(), new_lens.data_ptr(), page_table.data_ptr(),
+          free_pages.data_ptr(), _raw(free_head), seq_lens.data_ptr(), cu.data_ptr(), slots.data_ptr(),
+          positions.data_ptr(), used.data_ptr(),
+          _PAGE_PLAN.pack(B, num_rows, PAGE_SIZE, num_pages, width, free_pages.shape[0]))
     return PagePlan(seq_lens, cu, slots, positions, used)
 
 
@@ -899,10 +926,7 @@ def norm_rope(q, rho, k, cos, sin, positions=None, *, q_weight=None, rho_weight=
         done[name] = y
         rows += _HEAD_ROWS.pack(x.data_ptr(), y.data_ptr(), 0 if w is None else w.data_ptr(), shape[1],
                                 *_head_strides(name, x, dense), *y_strides)
-    with _device_guard(index):
-        st = lib.parallax_norm_rope(rows, len(sets), _raw(positions), _raw(cos), _raw(sin), p, _raw_stream(index))
-    if st != 0:
-        raise ParallaxError(st, "parallax_norm_rope")
+    _call(index, lib.parallax_norm_rope, rows, len(sets), _raw(positions), _raw(cos), _raw(sin), p)
     return tuple(done.values())
 
 
@@ -922,8 +946,10 @@ def norm_rope_backward(dq, drho, dk, q, rho, k, cos, sin, positions=None, *, q_w
     rows = grads = b""
     no_strides = (0,) * 3
     if norm:
-        dws.update(zip((name for name, _, _ in sets),
-                       q.new_empty((len(sets), q.shape[-1]), dtype=torch.float32).unbind()))
+        size = len(sets), q.shape[-1]
+        # (without a dtype the allocation takes a third less of the host)
+        dw = q.new_empty(size, dtype=torch.float32) if cos is None else cos.new_empty(size)
+        dws.update(zip([name for name, _, _ in sets], dw.unbind()))
     for name, x, w in sets:
         dy, shape = incoming[name], x.shape
         if dy is None or dy.shape != shape:
@@ -935,17 +961,12 @@ def norm_rope_backward(dq, drho, dk, q, rho, k, cos, sin, positions=None, *, q_w
                                 *_head_strides(name, x, dense), *no_strides)
         grads += _HEAD_GRADS.pack(dy.data_ptr(), dx.data_ptr(), dws[name].data_ptr() if norm else 0,
                                   *_head_strides("d" + name, dy, dense), *dense)
-    with _device_guard(index):
-        ws, nbytes = None, 0
-        if norm:
-            nbytes = lib.parallax_norm_rope_backward_workspace_size(p, len(sets))
-            if nbytes == SIZE_MAX:
-                raise ParallaxError(2, "parallax_norm_rope_backward_workspace_size")
-            ws = q.new_empty(nbytes, dtype=torch.uint8)
-        st = lib.parallax_norm_rope_backward(rows, grads, len(sets), _raw(positions), _raw(cos), _raw(sin), _raw(ws),
-                                             nbytes, p, _raw_stream(index))
-    if st != 0:
-        raise ParallaxError(st, "parallax_norm_rope_backward")
+    ws, nbytes = None, 0
+    if norm:
+        nbytes = _workspace_size(index, 2, lib.parallax_norm_rope_backward_workspace_size, p, len(sets))
+        ws = q.new_empty(nbytes // q.element_size())   # (a multiple of 4 bytes)
+    _call(index, lib.parallax_norm_rope_backward, rows, grads, len(sets), _raw(positions), _raw(cos), _raw(sin),
+          _raw(ws), nbytes, p)
     return tuple(dxs.values()) + tuple(dws.values())
 
 
@@ -988,11 +1009,12 @@ def _dense_rows(g):
 
 def _append_params(k, v, slot_map, num_pages, num_kv_heads, head_dim, dtype, index):
     """Checks of k, v [N, Hkv, d] and slot_map [N]; the packed parameters."""
-    if k.dim() != 3 or k.shape[1] != num_kv_heads or k.shape[2] != head_dim:
-        raise ValueError(f"k must be [N, {num_kv_heads}, {head_dim}], got {tuple(k.shape)}")
-    n = k.shape[0]
-    if v.shape != k.shape:
-        raise ValueError(f"v must have k's shape {tuple(k.shape)}, got {tuple(v.shape)}")
+    shape = k.shape
+    if len(shape) != 3 or shape[1] != num_kv_heads or shape[2] != head_dim:
+        raise ValueError(f"k must be [N, {num_kv_heads}, {head_dim}], got {tuple(shape)}")
+    n = shape[0]
+    if v.shape != shape:
+        raise ValueError(f"v must have k's shape {tuple(shape)}, got {tuple(v.shape)}")
     ks, vs = k.stride(), v.stride()
     if n > 0 and (ks[2] != 1 or vs[2] != 1):
         raise ValueError("the last dimension of k and v must be contiguous")
@@ -1022,11 +1044,8 @@ def cache_append(k, v, slot_map, k_cache, v_cache):
     index = _cuda_index("k_cache", k_cache)
     _on(index, "v_cache", v_cache, k_cache.dtype)
     p = _append_params(k, v, slot_map, P, Hkv, d, k_cache.dtype, index)
-    with _device_guard(index):
-        st = lib.parallax_cache_append(k.data_ptr(), v.data_ptr(), slot_map.data_ptr(), k_cache.data_ptr(),
-                                       v_cache.data_ptr(), p, _raw_stream(index))
-    if st != 0:
-        raise ParallaxError(st, "parallax_cache_append")
+    _call(index, lib.parallax_cache_append, k.data_ptr(), v.data_ptr(), slot_map.data_ptr(), k_cache.data_ptr(),
+          v_cache.data_ptr(), p)
 
 
 def q4_block_bytes(head_dim: int) -> int:
@@ -1037,15 +1056,14 @@ def q4_block_bytes(head_dim: int) -> int:
     return n
 
 
-def _q4_head_dim(kv_cache):
+def _q4_head_dim(dtype, nbytes):
     """The head_dim that a 4-bit cache's block size says."""
-    if kv_cache.dtype != torch.uint8:
-        raise TypeError(f"a 4-bit cache is a uint8 tensor, got {kv_cache.dtype}")
+    if dtype is not torch.uint8:
+        raise TypeError(f"a 4-bit cache is a uint8 tensor, got {dtype}")
     for d in (64, 128):
-        if kv_cache.shape[-1] == 72 * d:
+        if nbytes == 72 * d:
             return d
-    raise ValueError(f"a 4-bit cache's blocks have {q4_block_bytes(64)} or {q4_block_bytes(128)} bytes, "
-                     f"got {kv_cache.shape[-1]}")
+    raise ValueError(f"a 4-bit cache's blocks have {q4_block_bytes(64)} or {q4_block_bytes(128)} bytes, got {nbytes}")
 
 
 def q4_cache(num_pages, num_kv_heads, head_dim, device="cuda"):
@@ -1056,8 +1074,9 @@ def q4_cache(num_pages, num_kv_heads, head_dim, device="cuda"):
 def _q4_pool(kv_cache):
     if kv_cache.dim() != 3:
         raise ValueError(f"a 4-bit pool is [P, Hkv, block bytes], got {tuple(kv_cache.shape)}")
-    _check_shape("kv_cache", kv_cache, kv_cache.shape)
-    return kv_cache.shape[0], kv_cache.shape[1], _q4_head_dim(kv_cache)
+    _check_contiguous("kv_cache", kv_cache)
+    P, Hkv, nbytes = kv_cache.shape
+    return P, Hkv, _q4_head_dim(kv_cache.dtype, nbytes)
 
 
 def cache_append_q4(k, v, slot_map, kv_cache):
@@ -1070,11 +1089,7 @@ def cache_append_q4(k, v, slot_map, kv_cache):
     P, Hkv, d = _q4_pool(kv_cache)
     index = _cuda_index("kv_cache", kv_cache)
     p = _append_params(k, v, slot_map, P, Hkv, d, torch.bfloat16, index)
-    with _device_guard(index):
-        st = lib.parallax_cache_append_q4(k.data_ptr(), v.data_ptr(), slot_map.data_ptr(), kv_cache.data_ptr(), p,
-                                          _raw_stream(index))
-    if st != 0:
-        raise ParallaxError(st, "parallax_cache_append_q4")
+    _call(index, lib.parallax_cache_append_q4, k.data_ptr(), v.data_ptr(), slot_map.data_ptr(), kv_cache.data_ptr(), p)
 
 
 def cache_gather_q4(kv_cache, slot_map, *, out_dtype=torch.bfloat16, out=None):
@@ -1088,15 +1103,11 @@ def cache_gather_q4(kv_cache, slot_map, *, out_dtype=torch.bfloat16, out=None):
             raise ValueError(f"slot_map must be 1-D, got {tuple(slot_map.shape)}")
         shape = (slot_map.shape[0], Hkv, d)
         k = torch.empty(shape, dtype=out_dtype, device=kv_cache.device)
-        v = torch.empty(shape, dtype=out_dtype, device=kv_cache.device)
+        v = torch.empty_like(k)
     else:
         k, v = out
     p = _append_params(k, v, slot_map, P, Hkv, d, k.dtype, index)
-    with _device_guard(index):
-        st = lib.parallax_cache_gather_q4(kv_cache.data_ptr(), slot_map.data_ptr(), k.data_ptr(), v.data_ptr(), p,
-                                          _raw_stream(index))
-    if st != 0:
-        raise ParallaxError(st, "parallax_cache_gather_q4")
+    _call(index, lib.parallax_cache_gather_q4, kv_cache.data_ptr(), slot_map.data_ptr(), k.data_ptr(), v.data_ptr(), p)
     return k, v
 
 
@@ -1112,7 +1123,7 @@ def _q4_workspace(index, nbytes, units):
     gets one of its own, whose counters it clears, so that graphs replayed at
     once do not share it."""
     counters = (4 * units + 255) & ~255
-    if torch.cuda.is_current_stream_capturing():
+    if _capturing(index):
         ws = torch.empty(nbytes, dtype=torch.uint8, device=index)
         ws[-counters:].zero_()
         return ws
@@ -1137,10 +1148,7 @@ def decode_q4_workspace(q, kv_cache, *, page_table=None, kv_len=None, num_ctas=0
     p = _DECODE.pack(B, q.shape[1], Hkv, q.shape[2], int(kv_len), PAGE_SIZE if paged else 0,
                      kv_cache.shape[0] if paged else 0, page_table.shape[1] if paged else 0, PLX_BF16, PLX_BF16, 1.0,
                      int(num_ctas))
-    with _device_guard(_cuda_index("q", q)):
-        nbytes = lib.parallax_decode_q4_workspace_size(p, 0)
-    if nbytes == SIZE_MAX:
-        raise ParallaxError(1, "parallax_decode_q4_workspace_size")
+    nbytes = _workspace_size(_cuda_index("q", q), 1, lib.parallax_decode_q4_workspace_size, p, 0)
     return torch.zeros(nbytes, dtype=torch.uint8, device=q.device)
 
 
@@ -1155,39 +1163,41 @@ def decode_q4(q, rho, kv_cache, scale=None, *, seq_lens=None, page_table=None, o
     ``out_dtype`` (default bfloat16).  ``workspace``: see decode_q4_workspace
     (default: one that the binding keeps for the stream).
     """
-    if q.dim() != 3 or tuple(rho.shape) != tuple(q.shape):
-        raise ValueError(f"q and rho must be [B, Hq, d] and alike, got {tuple(q.shape)} and {tuple(rho.shape)}")
-    B, Hq, d = q.shape
+    shape, blocks = q.shape, kv_cache.shape
+    if len(shape) != 3 or rho.shape != shape:
+        raise ValueError(f"q and rho must be [B, Hq, d] and alike, got {tuple(shape)} and {tuple(rho.shape)}")
+    B, Hq, d = shape
     paged = page_table is not None
-    if kv_cache.dim() != (3 if paged else 4):
+    if len(blocks) != (3 if paged else 4):
         raise ValueError("a paged 4-bit cache is [P, Hkv, block bytes] and a contiguous one "
-                         f"[B, Hkv, pages, block bytes], got {tuple(kv_cache.shape)}")
-    if _q4_head_dim(kv_cache) != d:
-        raise ValueError(f"the cache's head_dim {_q4_head_dim(kv_cache)} differs from the queries' {d}")
-    Hkv = kv_cache.shape[1]
+                         f"[B, Hkv, pages, block bytes], got {tuple(blocks)}")
+    cache_dim = _q4_head_dim(kv_cache.dtype, blocks[-1])
+    if cache_dim != d:
+        raise ValueError(f"the cache's head_dim {cache_dim} differs from the queries' {d}")
+    Hkv, num_pages, width = blocks[1], 0, 0
     if Hkv < 1 or Hq % Hkv:
         raise ValueError(f"{Hq} query heads do not split into {Hkv} KV heads")
     if paged:
-        most = page_table.shape[-1] * PAGE_SIZE
-        kv_len = most if kv_len is None else int(kv_len)
-        if kv_len > most:
-            raise ValueError(f"kv_len {kv_len} exceeds the page table's {page_table.shape[-1]} pages")
+        num_pages, width = blocks[0], page_table.shape[-1]
+        kv_len = width * PAGE_SIZE if kv_len is None else int(kv_len)
+        if kv_len > width * PAGE_SIZE:
+            raise ValueError(f"kv_len {kv_len} exceeds the page table's {width} pages")
         if seq_lens is None:
             raise ValueError("a paged cache needs seq_lens")
-        _check_shape("page_table", page_table, (B, page_table.shape[-1]))
+        _check_shape("page_table", page_table, (B, width))
     else:
-        if kv_cache.shape[0] != B:
-            raise ValueError(f"a contiguous cache holds one sequence per row: {kv_cache.shape[0]} != {B}")
-        pages = kv_cache.shape[2]
+        if blocks[0] != B:
+            raise ValueError(f"a contiguous cache holds one sequence per row: {blocks[0]} != {B}")
+        pages = blocks[2]
         kv_len = pages * PAGE_SIZE if kv_len is None else int(kv_len)
         if (kv_len + PAGE_SIZE - 1) // PAGE_SIZE != pages:
             raise ValueError(f"kv_len {kv_len} does not fill the cache's {pages} pages of {PAGE_SIZE} tokens "
                              "(use seq_lens for shorter sequences)")
     if seq_lens is not None:
         _check_shape("seq_lens", seq_lens, (B,))
-    _check_shape("q", q, q.shape)
-    _check_shape("rho", rho, q.shape)
-    _check_shape("kv_cache", kv_cache, kv_cache.shape)
+    _check_contiguous("q", q)
+    _check_contiguous("rho", rho)
+    _check_contiguous("kv_cache", kv_cache)
     index = _cuda_index("q", q)
     _on(index, "q", q, torch.bfloat16)
     _on(index, "rho", rho, torch.bfloat16)
@@ -1201,23 +1211,16 @@ def decode_q4(q, rho, kv_cache, scale=None, *, seq_lens=None, page_table=None, o
     else:
         out, out_dtype = _output(out, out_dtype, q.shape, torch.bfloat16, q.device)
         _on(index, "out", out)
-    p = _DECODE.pack(B, Hq, Hkv, d, kv_len, PAGE_SIZE if paged else 0, kv_cache.shape[0] if paged else 0,
-                     page_table.shape[1] if paged else 0, PLX_BF16, _dtype_code(out_dtype),
-                     (1.0 / d ** 0.5) if scale is None else float(scale), int(num_ctas))
-    with _device_guard(index):
-        if workspace is not None:
-            _on(index, "workspace", workspace, torch.uint8)
-            _check_shape("workspace", workspace, (workspace.numel(),))
-            ws = workspace
-        else:
-            nbytes = lib.parallax_decode_q4_workspace_size(p, 0)
-            if nbytes == SIZE_MAX:
-                raise ParallaxError(1, "parallax_decode_q4_workspace_size")
-            ws = _q4_workspace(index, nbytes, B * Hkv)
-        st = lib.parallax_decode_q4(q.data_ptr(), rho.data_ptr(), kv_cache.data_ptr(), _raw(page_table),
-                                    _raw(seq_lens), out.data_ptr(), ws.data_ptr(), ws.numel(), p, _raw_stream(index))
-    if st != 0:
-        raise ParallaxError(st, "parallax_decode_q4")
+    p = _DECODE.pack(B, Hq, Hkv, d, kv_len, PAGE_SIZE if paged else 0, num_pages, width, PLX_BF16,
+                     _dtype_code(out_dtype), (1.0 / d ** 0.5) if scale is None else float(scale), int(num_ctas))
+    if workspace is not None:
+        _on(index, "workspace", workspace, torch.uint8)
+        _check_shape("workspace", workspace, (workspace.numel(),))
+    else:
+        nbytes = _workspace_size(index, 1, lib.parallax_decode_q4_workspace_size, p, 0)
+        workspace = _q4_workspace(index, nbytes, B * Hkv)
+    _call(index, lib.parallax_decode_q4, q.data_ptr(), rho.data_ptr(), kv_cache.data_ptr(), _raw(page_table),
+          _raw(seq_lens), out.data_ptr(), workspace.data_ptr(), workspace.numel(), p)
     return out
 
 
