@@ -824,11 +824,9 @@ def _dense_strides(shape):
     return 0, shape[1] * shape[2], shape[2]
 
 
-def _head_strides(name, t, dense):
-    """The same of any tensor of that shape, ``dense`` being its contiguous strides
-    (0 for a dimension of one entry, whatever torch says there)."""
-    if t.is_contiguous():
-        return dense
+def _head_strides(name, t):
+    """The same of a tensor that is not contiguous (0 for a dimension of one entry,
+    whatever torch says there)."""
     s, n = t.stride(), t.shape
     if s[-1] != 1 and t.numel() > 0:
         raise ValueError(f"{name}'s last dimension must be contiguous")
@@ -839,7 +837,8 @@ def _head_strides(name, t, dense):
 
 def _norm_rope_call(q, rho, k, cos, sin, positions, weights, eps, norm, interleaved):
     """Checks and parameters that the two directions share: (sets, params, device index), a
-    set being (name, x, weight)."""
+    set being (name, x, shape, its contiguous strides, the input part of its plx_head_rows:
+    address, weight's address, heads and strides)."""
     shape = q.shape
     batched = len(shape) == 4
     if not batched and len(shape) != 3:
@@ -847,24 +846,30 @@ def _norm_rope_call(q, rho, k, cos, sin, positions, weights, eps, norm, interlea
     d = shape[-1]
     B, T = (shape[0], shape[2]) if batched else (1, shape[0])
     index, dtype = _cuda_index("q", q), q.dtype
-    sets = [("q", q, weights[0])]
+    dense = _dense_strides(shape)
+    tensors = [("q", q, shape, dense, weights[0])]
     if rho is not None:
         if rho.shape != shape:
             raise ValueError(f"rho must have q's shape {tuple(shape)}, got {tuple(rho.shape)}")
         _on(index, "rho", rho, dtype)
-        sets.append(("rho", rho, weights[1]))
+        tensors.append(("rho", rho, shape, dense, weights[1]))
     if k is not None:
         ks = k.shape
         if len(ks) != len(shape) or ks[-1] != d or ks[0] != shape[0] or (batched and ks[2] != T):
             raise ValueError(f"k's rows {tuple(ks)} do not match q's {tuple(shape)}")
         _on(index, "k", k, dtype)
-        sets.append(("k", k, weights[2]))
-    for name, _, w in sets:
+        tensors.append(("k", k, ks, _dense_strides(ks), weights[2]))
+    sets = []
+    for name, x, n, dense, w in tensors:
+        at = 0
         if w is not None:
             if not norm:
                 raise ValueError(f"{name}_weight needs norm=True")
             _check_shape(name + "_weight", w, (d,))
             _on(index, name + "_weight", w, dtype)
+            at = w.data_ptr()
+        sets.append((name, x, n, dense,
+                     (x.data_ptr(), at, n[1], dense if x.is_contiguous() else _head_strides(name, x))))
     rot, max_pos = 0, 0
     if cos is not None and sin is not None:
         if cos.dim() != 2 or cos.shape != sin.shape:
@@ -912,9 +917,7 @@ def norm_rope(q, rho, k, cos, sin, positions=None, *, q_weight=None, rho_weight=
                                      interleaved)
     done, rows = {"q": None, "rho": None, "k": None}, b""
     given = dict(zip(done, out)) if out is not None else None
-    for name, x, w in sets:
-        shape = x.shape
-        dense = y_strides = _dense_strides(shape)
+    for name, x, shape, y_strides, (at, weight, heads, strides) in sets:
         if given is None:
             y = torch.empty_like(x, memory_format=torch.contiguous_format)
         else:
@@ -922,10 +925,10 @@ def norm_rope(q, rho, k, cos, sin, positions=None, *, q_weight=None, rho_weight=
             if y is None or y.shape != shape:
                 raise ValueError(f"out's {name} must have shape {tuple(shape)}")
             _on(index, "out's " + name, y, x.dtype)
-            y_strides = _head_strides("out's " + name, y, dense)
+            if not y.is_contiguous():
+                y_strides = _head_strides("out's " + name, y)
         done[name] = y
-        rows += _HEAD_ROWS.pack(x.data_ptr(), y.data_ptr(), 0 if w is None else w.data_ptr(), shape[1],
-                                *_head_strides(name, x, dense), *y_strides)
+        rows += _HEAD_ROWS.pack(at, y.data_ptr(), weight, heads, *strides, *y_strides)
     _call(index, lib.parallax_norm_rope, rows, len(sets), _raw(positions), _raw(cos), _raw(sin), p)
     return tuple(done.values())
 
@@ -944,23 +947,21 @@ def norm_rope_backward(dq, drho, dk, q, rho, k, cos, sin, positions=None, *, q_w
     names = ("q", "rho", "k")
     incoming, dxs, dws = dict(zip(names, (dq, drho, dk))), dict.fromkeys(names), dict.fromkeys(names)
     rows = grads = b""
-    no_strides = (0,) * 3
     if norm:
         size = len(sets), q.shape[-1]
         # (without a dtype the allocation takes a third less of the host)
         dw = q.new_empty(size, dtype=torch.float32) if cos is None else cos.new_empty(size)
-        dws.update(zip([name for name, _, _ in sets], dw.unbind()))
-    for name, x, w in sets:
-        dy, shape = incoming[name], x.shape
+        dws.update(zip([one[0] for one in sets], dw.unbind()))
+    for name, x, shape, dense, (at, weight, heads, strides) in sets:
+        dy = incoming[name]
         if dy is None or dy.shape != shape:
             raise ValueError(f"d{name} must have shape {tuple(shape)}")
-        _on(index, "d" + name, dy, x.dtype)
-        dense = _dense_strides(shape)
+        if dy.get_device() != index or dy.dtype is not x.dtype:
+            _on(index, "d" + name, dy, x.dtype)
         dx = dxs[name] = torch.empty_like(x, memory_format=torch.contiguous_format)
-        rows += _HEAD_ROWS.pack(x.data_ptr(), 0, 0 if w is None else w.data_ptr(), shape[1],
-                                *_head_strides(name, x, dense), *no_strides)
+        rows += _HEAD_ROWS.pack(at, 0, weight, heads, *strides, 0, 0, 0)
         grads += _HEAD_GRADS.pack(dy.data_ptr(), dx.data_ptr(), dws[name].data_ptr() if norm else 0,
-                                  *_head_strides("d" + name, dy, dense), *dense)
+                                  *(dense if dy.is_contiguous() else _head_strides("d" + name, dy)), *dense)
     ws, nbytes = None, 0
     if norm:
         nbytes = _workspace_size(index, 2, lib.parallax_norm_rope_backward_workspace_size, p, len(sets))
