@@ -5,14 +5,15 @@
 // bounds them on long prompts (the 4-bit append its issue slots first) and
 // launch latency on single tokens: append_q4 reads 4 d bytes of a token and head
 // and writes 72 d / 64.  16382 tokens of 8 heads of 128 columns, appended and
-// gathered in fp32 (239 MB): 47 us, 5.1 TB/s; 128 tokens of 4 heads: 4 us, device time.
+// gathered in fp32 (239 MB): 46 us, 5.2 TB/s; 128 tokens of 4 heads: 3.8 us, device
+// time.
 #pragma once
 
 #include "ptx.cuh"
 
 namespace plx {
 
-constexpr int kAppendThreads = 256;
+constexpr int kAppendThreads = 128;   // (256: 46.9 instead of 46.1 us for the prompts, 4.0 instead of 3.8 for the step)
 constexpr int kQ4Page = 64;
 
 // Byte offsets inside a block.
