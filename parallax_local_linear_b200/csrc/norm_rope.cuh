@@ -17,7 +17,7 @@
 // token's cos and sin are read once for them.
 //
 // Measured (device time, bf16, d = 128): 4 x 8192 tokens of 3 x 16 heads forward (810
-// MB) 127 to 136 us, 5.9 to 6.4 TB/s; 4 x 8192 of 16 + 16 + 4 heads backward
+// MB) 134 us, 6.0 TB/s; 4 x 8192 of 16 + 16 + 4 heads backward
 // (910 MB) 149 us, 6.1 TB/s; 8 tokens forward 2.3 us.
 #pragma once
 
@@ -25,7 +25,8 @@
 
 namespace plx {
 
-constexpr int kNrThreads = 256;
+constexpr int kNrFwdThreads = 64;   // (810 MB: 133.4 us; 134.4 with 128 threads, 136.1 with 256)
+constexpr int kNrThreads = 256;     // backward (128: 1% slower on long rows, 15% on short ones)
 constexpr int kNrMaxSets = 3;
 constexpr int kNrBwdCtasPerSm = 3;
 constexpr int kNrBwdHeads = 4;                                    // rows of an item
@@ -186,7 +187,7 @@ __device__ __forceinline__ int nr_position(const NormRopeArgs& a, int b, int t) 
 // A group of LPR lanes takes the rows of chunk blockIdx.y (a set's next `hpg`
 // heads) of one token; neighbouring groups take neighbouring tokens.
 template <typename T, int D, bool kInter>
-__global__ void __launch_bounds__(kNrThreads, 5) norm_rope_kernel(const NormRopeArgs a) {
+__global__ void __launch_bounds__(kNrFwdThreads, 20) norm_rope_kernel(const NormRopeArgs a) {
   using L = NrLane<T, D, kInter>;
   constexpr int P = L::P;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -195,7 +196,7 @@ __global__ void __launch_bounds__(kNrThreads, 5) norm_rope_kernel(const NormRope
   int chunk = blockIdx.y, si = 0;
   while (chunk >= a.set[si].chunks) chunk -= a.set[si++].chunks;
   const NormRopeSet& set = a.set[si];
-  const int tok = (int)((blockIdx.x * kNrThreads + threadIdx.x) / L::LPR);
+  const int tok = (int)((blockIdx.x * kNrFwdThreads + threadIdx.x) / L::LPR);
   const int b = a.B == 1 ? 0 : tok / a.T, t = tok - b * a.T;
   const int h0 = chunk * a.hpg;
   const int pos = b < a.B && t < a.T ? nr_position(a, b, t) : -1;
@@ -220,7 +221,7 @@ __global__ void __launch_bounds__(kNrThreads, 5) norm_rope_kernel(const NormRope
   const T* x = static_cast<const T*>(set.x) + b * set.xs[0] + t * set.xs[1] + h0 * set.xs[2];
   T* y = static_cast<T*>(set.y) + b * set.ys[0] + t * set.ys[1] + h0 * set.ys[2];
   const int heads = live ? min(a.hpg, set.heads - h0) : 0;
-  constexpr int U = 2;   // rows in flight (four on three CTAs an SM instead of five are 1% slower, and more in small calls)
+  constexpr int U = 2;   // rows in flight (four, on 24 warps an SM instead of 40, are 1% slower, and more in small calls)
   for (int j = 0; j < a.hpg; j += U) {
     uint2 v0[U], v1[U];
 #pragma unroll

@@ -141,12 +141,12 @@ NormRopeArgs norm_rope_args(const plx_head_rows* rows, int32_t num_sets, const i
 
 template <typename T, int D, bool kInter>
 plx_status launch_norm_rope(const NormRopeArgs& a, cudaStream_t stream) {
-  constexpr int per_cta = kNrThreads / NrLane<T, D, kInter>::LPR;
+  constexpr int per_cta = kNrFwdThreads / NrLane<T, D, kInter>::LPR;
   long long chunks = 0;
   for (int i = 0; i < a.sets; ++i) chunks += a.set[i].chunks;
   const long long tokens = (long long)a.B * a.T;
   return launch_pdl(norm_rope_kernel<T, D, kInter>, dim3((unsigned)((tokens + per_cta - 1) / per_cta), (unsigned)chunks),
-                    dim3(kNrThreads), 0, stream, a) == cudaSuccess
+                    dim3(kNrFwdThreads), 0, stream, a) == cudaSuccess
              ? PLX_OK
              : PLX_ERR_CUDA;
 }
