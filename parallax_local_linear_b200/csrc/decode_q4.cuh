@@ -31,15 +31,23 @@
 // with x_i the score in powers of two (maxima of a page).  M stays until a page
 // needs it to be more than 5 larger, so every product is at most 2^15, nothing
 // above 2^-34 of the largest is lost, and after a unit's first page the
-// sums are hardly ever rescaled (1.5% of the time).  Sequences of
-// fewer than 128 keys add a second product with the weights' low halves (22 bits
-// together): with |a| about 10 the rounding to 2^-12 would show in rows of a few
-// keys.  Over more keys it averages out (and the output is a sum of as many
-// terms); without it a page takes 64 products instead of 96 and the call 13%
-// less time.
-// a_i is taken relative to the probe value of the first token the warp sees of
-// a unit; any constant leaves the output unchanged, and merging pieces shifts
-// c and O2 to a common one.
+// sums are hardly ever rescaled (1.5% of the time).
+//
+// Exactness.  The output is the difference of two sums whose terms are w_i
+// |a_i - aref| |v_i|, so what is rounded in them comes back |a - aref| times.
+//   - The weights enter with their low halves in a second product (22 bits
+//     together), as in decode.cuh.
+//   - aref is the probe value of the key with the largest score so far, or of one
+//     within 2^5 of it in weight (any constant leaves the output unchanged):
+//     the sums are shifted when a page brings a larger one, and merging
+//     shifts c and O2 of the pieces to a common one.  So where one key holds the
+//     weight its own term is about zero.  This also keeps the tensor cores' grid
+//     harmless: they add the terms of a product in steps set by the largest exponents,
+//     where a subnormal code counts as 2^-14, so beside one heavy weight the other
+//     15 tokens' terms are cut at 2^-14 of it (measured: 1.1e-4 of the heavy
+//     weight, always downwards).
+// With 11 bits and the first key's probe value a row with one key 12 above 1000
+// others was up to 6% off, with 22 bits alone 0.4%, with both 0.01%.
 //
 // Work.  The pages of every (sequence, KV head) unit are laid end to end and
 // cut into equal runs, one per warp: no warp waits for another until its run
@@ -81,11 +89,9 @@ struct DecodeQ4Args {
   int min_pages;                   // a CTA takes at least this many pages
 };
 
-// Sequences with fewer keys than this get 22-bit weights in the value product.
-constexpr int kQ4FineKeys = 128;
-
 // Weights against a new reference are at most 2^kQ4Top, and 2^kQ4Slack times
-// that before it moves: together below fp16's 2^16.
+// that before it moves: together below fp16's 2^16.  A key 2^kQ4Slack above the
+// one that gave aref takes its place.
 constexpr float kQ4Top = 10.f, kQ4Slack = 5.f;
 
 // Warps of a CTA (one CTA per SM) and its shared memory.  A ring slot holds
@@ -295,6 +301,7 @@ struct Q4WarpState {
   float o[NT][2 * J][4];       // codes' sums: [2 j + h]: columns +2 h, +2 h + 1 (O1, O2 each)
   float pm[NT][G][2];          // sum p m, sum pa m of the lane's tokens
   float m[NT], l[NT], c[NT], aref[NT];
+  float xref[NT];              // score of the key whose probe value is aref
 
   __device__ __forceinline__ void reset() {
 #pragma unroll
@@ -303,7 +310,7 @@ struct Q4WarpState {
       for (int i = 0; i < 2 * J; ++i) o[t][i][0] = o[t][i][1] = o[t][i][2] = o[t][i][3] = 0.f;
 #pragma unroll
       for (int g = 0; g < G; ++g) pm[t][g][0] = pm[t][g][1] = 0.f;
-      m[t] = -INFINITY;
+      m[t] = xref[t] = -INFINITY;
       l[t] = c[t] = aref[t] = 0.f;
     }
   }
@@ -367,8 +374,8 @@ struct Q4WarpState {
 
 // Adds a page's tokens to the sums: weights from the scores fs x and probe
 // values av against the reference st.m, 16 tokens at a time.  `slot`: the page's value
-// codes and parameters.  kFine: with the weights' low halves.
-template <int D, int NT, bool kFine>
+// codes and parameters.  Weights are fp16 pairs: rounded, and what that left.
+template <int D, int NT>
 __device__ __forceinline__ void q4_value_sums(Q4WarpState<D, NT>& st, const uint8_t* slot, const float (&fs)[NT],
                                               const float (&x)[NT][8], const float (&av)[NT][8]) {
   using SM = Q4Smem<D, NT>;
@@ -395,10 +402,8 @@ __device__ __forceinline__ void q4_value_sums(Q4WarpState<D, NT>& st, const uint
           const float ps = p * s, pas = pa * s;
           const uint32_t hi = pack_half(ps, pas);
           bh[t][g][half] = transpose_8x8(hi);
-          if constexpr (kFine) {
-            const float2 hf = unpack_half(hi);
-            bl[t][g][half] = transpose_8x8(pack_half(ps - hf.x, pas - hf.y));
-          }
+          const float2 hf = unpack_half(hi);
+          bl[t][g][half] = transpose_8x8(pack_half(ps - hf.x, pas - hf.y));
         }
       }
     }
@@ -421,12 +426,9 @@ __device__ __forceinline__ void q4_value_sums(Q4WarpState<D, NT>& st, const uint
 #pragma unroll
         for (int q = 0; q < 4; ++q)
           mma_f16_16816(st.o[t][2 * j + q], av4[q][0], av4[q][1], av4[q][2], av4[q][3], bh[t][j / 2][0], bh[t][j / 2][1]);
-        if constexpr (kFine) {
 #pragma unroll
-          for (int q = 0; q < 4; ++q)
-            mma_f16_16816(st.o[t][2 * j + q], av4[q][0], av4[q][1], av4[q][2], av4[q][3], bl[t][j / 2][0],
-                          bl[t][j / 2][1]);
-        }
+        for (int q = 0; q < 4; ++q)
+          mma_f16_16816(st.o[t][2 * j + q], av4[q][0], av4[q][1], av4[q][2], av4[q][3], bl[t][j / 2][0], bl[t][j / 2][1]);
       }
     }
   }
@@ -722,14 +724,6 @@ __global__ void __launch_bounds__(Q4Smem<D, NT>::kThreads, 1) decode_q4_kernel(c
         }
       }
       leave(std::integral_constant<bool, S % 2 != 0>{});   // part 2 i + S
-      if (seg == 0) {   // the lane with token 0 (always valid) of the head
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-          st.aref[t] = __shfl_sync(0xffffffffu, av[t][0], hc);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) av[t][e] -= st.aref[t];
-        }
-      }
 
       landed();
       if (nvalid < kQ4Page) {   // tokens past the sequence's end weigh nothing, whatever their parameters
@@ -762,15 +756,54 @@ __global__ void __launch_bounds__(Q4Smem<D, NT>::kThreads, 1) decode_q4_kernel(c
         for (int k = 1; k < 2 * G; ++k) m2 = __hmax2(m2, __habs2(*reinterpret_cast<__nv_bfloat162*>(&w[k])));
         vmax = __reduce_max_sync(0xffffffffu, *reinterpret_cast<uint32_t*>(&m2) << 16);   // (scales are in the low half)
       }
-      bool moved = false;
-      float m_new[NT];
 #pragma unroll
-      for (int t = 0; t < NT; ++t) {
+      for (int t = 0; t < NT; ++t)
 #pragma unroll
         for (int off = 4; off < 32; off <<= 1) {
           mx[t] = fmaxf(mx[t], __shfl_xor_sync(0xffffffffu, mx[t], off));
           ma[t] = fmaxf(ma[t], __shfl_xor_sync(0xffffffffu, ma[t], off));
         }
+      bool above = false;
+#pragma unroll
+      for (int t = 0; t < NT; ++t) above = above || fs[t] * mx[t] > st.xref[t] + kQ4Slack;
+      if (__any_sync(0xffffffffu, above)) {   // aref goes to the key with the page's largest score
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          bool mine = false;
+          float here = 0.f;
+#pragma unroll
+          for (int e = 7; e >= 0; --e)
+            if (x[t][e] == mx[t]) {
+              mine = true;
+              here = av[t][e];
+            }
+          const uint32_t holders = __ballot_sync(0xffffffffu, mine) & (0x11111111u << hc);
+          float shift = __shfl_sync(0xffffffffu, here, holders ? __ffs(holders) - 1 : 0);
+          if (!(fs[t] * mx[t] > st.xref[t] + kQ4Slack) || holders == 0) shift = 0.f;
+          else st.xref[t] = fs[t] * mx[t];
+          st.aref[t] += shift;
+          st.c[t] = fmaf(-shift, st.l[t], st.c[t]);
+#pragma unroll
+          for (int k = 0; k < 2 * J; ++k) {
+            st.o[t][k][1] = fmaf(-shift, st.o[t][k][0], st.o[t][k][1]);
+            st.o[t][k][3] = fmaf(-shift, st.o[t][k][2], st.o[t][k][3]);
+          }
+#pragma unroll
+          for (int g = 0; g < G; ++g) st.pm[t][g][1] = fmaf(-shift, st.pm[t][g][0], st.pm[t][g][1]);
+          ma[t] = 1.f;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            if (x[t][e] > -INFINITY) av[t][e] -= shift;   // (tokens past the end keep theirs, 0)
+            ma[t] = fmaxf(ma[t], fabsf(av[t][e]));
+          }
+#pragma unroll
+          for (int off = 4; off < 32; off <<= 1) ma[t] = fmaxf(ma[t], __shfl_xor_sync(0xffffffffu, ma[t], off));
+        }
+      }
+      bool moved = false;
+      float m_new[NT];
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
         const float big = ma[t] * __uint_as_float(vmax);
         const float need = fs[t] * mx[t] + lg2(fminf(fmaxf(big, 0x1p-60f), 0x1p60f));
         m_new[t] = need > st.m[t] + kQ4Slack ? need : st.m[t];
@@ -798,10 +831,7 @@ __global__ void __launch_bounds__(Q4Smem<D, NT>::kThreads, 1) decode_q4_kernel(c
         }
       }
 
-      if (cur.len < kQ4FineKeys)
-        q4_value_sums<D, NT, true>(st, slot, fs, x, av);
-      else
-        q4_value_sums<D, NT, false>(st, slot, fs, x, av);
+      q4_value_sums<D, NT>(st, slot, fs, x, av);
       leave(std::integral_constant<bool, S % 2 == 0>{});
       ++seg;
 
