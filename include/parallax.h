@@ -633,6 +633,10 @@ plx_status parallax_cache_gather_q4(const void* kv_cache, const int64_t* slot_ma
  *               partials (the rest of what a call needs, from the front)
  *               never reach another call's counters.
  *   the rest    as parallax_decode.  Hq / Hkv <= 8.
+ * Weights enter the value product in 22 bits, sums are fp32.  Range: entries
+ * of q and rho below 2^114 in size, value scales s of 2^-84 or more (smaller
+ * ones count less, down to not at all; 0 is exact) and below 2^100, and
+ * results that fp32 holds; past the upper limits the output may be NaN.
  * One launch. */
 size_t parallax_decode_q4_workspace_size(const plx_decode_params* p, int32_t num_sms);
 plx_status parallax_decode_q4(const void* q, const void* rho, const void* kv_cache, const int32_t* page_table,

@@ -25,13 +25,14 @@
 // from accumulator to operand by a transposing move (movmatrix).
 //
 // Ranges.  q and rho are scaled by a power of two to at most 2^14 per row
-// (exact: they are bf16).  e s and e a s have to fit fp16, whatever the size of
-// s and a: the running reference is not the largest score alone but
+// (exact: they are bf16; up to 2^114).  e s and e a s have to fit fp16: the
+// running reference is not the largest score alone but
 //     M = max_i x_i + log2(max_i,g s_ig max_i(1, |a_i|)),      p_i = 2^(x_i - M + 10)
 // with x_i the score in powers of two (maxima of a page).  M stays until a page
 // needs it to be more than 5 larger, so every product is at most 2^15, nothing
 // above 2^-34 of the largest is lost, and after a unit's first page the
-// sums are hardly ever rescaled (1.5% of the time).
+// sums are hardly ever rescaled (1.5% of the time).  Probe values above 2^10 are
+// taken in a larger unit.
 //
 // Exactness.  The output is the difference of two sums whose terms are w_i
 // |a_i - aref| |v_i|, so what is rounded in them comes back |a - aref| times.
@@ -93,6 +94,10 @@ struct DecodeQ4Args {
 // that before it moves: together below fp16's 2^16.  A key 2^kQ4Slack above the
 // one that gave aref takes its place.
 constexpr float kQ4Top = 10.f, kQ4Slack = 5.f;
+
+// Probe values (from aref, in their unit) are at most this: p s, which is smaller by
+// them than p a s, keeps its low half.
+constexpr float kQ4MaxProbe = 1024.f;
 
 // Warps of a CTA (one CTA per SM) and its shared memory.  A ring slot holds
 // one half of a block, K's or V's codes and parameters.
@@ -302,6 +307,7 @@ struct Q4WarpState {
   float pm[NT][G][2];          // sum p m, sum pa m of the lane's tokens
   float m[NT], l[NT], c[NT], aref[NT];
   float xref[NT];              // score of the key whose probe value is aref
+  float unit[NT];              // aref, c and O2 are in this many ones (a power of two)
 
   __device__ __forceinline__ void reset() {
 #pragma unroll
@@ -312,10 +318,13 @@ struct Q4WarpState {
       for (int g = 0; g < G; ++g) pm[t][g][0] = pm[t][g][1] = 0.f;
       m[t] = xref[t] = -INFINITY;
       l[t] = c[t] = aref[t] = 0.f;
+      unit[t] = 1.f;
     }
   }
   // Sums over the lanes that hold other tokens of the same heads; the codes'
-  // powers of two and the minima's sums go into o.
+  // powers of two, the minima's sums and the unit go in.  l becomes 1 to 2
+  // first (and m what that took), so that c and O2 are no larger than the probe
+  // values make them.
   __device__ __forceinline__ void close() {
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
@@ -329,13 +338,19 @@ struct Q4WarpState {
           pm[t][g][1] += __shfl_xor_sync(0xffffffffu, pm[t][g][1], off);
         }
       }
+      const int e = min(max((int)(__float_as_uint(l[t]) >> 23) - 127, -126), 126);
+      const float f = __uint_as_float((uint32_t)(127 - e) << 23);
+      m[t] += e;
+      l[t] *= f;
+      c[t] = c[t] * f * unit[t];
 #pragma unroll
       for (int i = 0; i < 2 * J; ++i) {
-        o[t][i][0] = fmaf(o[t][i][0], 16777216.f, pm[t][i / 4][0]);
-        o[t][i][1] = fmaf(o[t][i][1], 16777216.f, pm[t][i / 4][1]);
-        o[t][i][2] = fmaf(o[t][i][2], 1048576.f, pm[t][i / 4][0]);
-        o[t][i][3] = fmaf(o[t][i][3], 1048576.f, pm[t][i / 4][1]);
+        o[t][i][0] = fmaf(o[t][i][0], 16777216.f, pm[t][i / 4][0]) * f;
+        o[t][i][1] = fmaf(o[t][i][1], 16777216.f, pm[t][i / 4][1]) * f * unit[t];
+        o[t][i][2] = fmaf(o[t][i][2], 1048576.f, pm[t][i / 4][0]) * f;
+        o[t][i][3] = fmaf(o[t][i][3], 1048576.f, pm[t][i / 4][1]) * f * unit[t];
       }
+      aref[t] *= unit[t];
     }
   }
   // After close(): the finished output rows.
@@ -747,14 +762,16 @@ __global__ void __launch_bounds__(Q4Smem<D, NT>::kThreads, 1) decode_q4_kernel(c
                      max3(fabsf(av[t][3]), fabsf(av[t][4]), fabsf(av[t][5])),
                      max3(fabsf(av[t][6]), fabsf(av[t][7]), 1.f));
       }
-      uint32_t vmax;
+      float vbig;   // log2 of the largest scale, or of what keeps the sums of p m (below 2^99) in fp32's range where it is smaller
       {
         uint32_t w[2 * G];
         lds_words<2 * G>(slot + SM::kCodes + lane * (8 * G), w);
         __nv_bfloat162 m2 = __habs2(*reinterpret_cast<__nv_bfloat162*>(&w[0]));
 #pragma unroll
         for (int k = 1; k < 2 * G; ++k) m2 = __hmax2(m2, __habs2(*reinterpret_cast<__nv_bfloat162*>(&w[k])));
-        vmax = __reduce_max_sync(0xffffffffu, *reinterpret_cast<uint32_t*>(&m2) << 16);   // (scales are in the low half)
+        const uint32_t both = *reinterpret_cast<uint32_t*>(&m2);   // scales are in the low half
+        const float v = max3(bf16_lo_f(both), bf16_hi_f(both) * 0x1p-40f, 0x1p-84f);
+        vbig = lg2(__uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(v))));
       }
 #pragma unroll
       for (int t = 0; t < NT; ++t)
@@ -763,12 +780,17 @@ __global__ void __launch_bounds__(Q4Smem<D, NT>::kThreads, 1) decode_q4_kernel(c
           mx[t] = fmaxf(mx[t], __shfl_xor_sync(0xffffffffu, mx[t], off));
           ma[t] = fmaxf(ma[t], __shfl_xor_sync(0xffffffffu, ma[t], off));
         }
-      bool above = false;
+      float need[NT];
+      bool due = false;
 #pragma unroll
-      for (int t = 0; t < NT; ++t) above = above || fs[t] * mx[t] > st.xref[t] + kQ4Slack;
-      if (__any_sync(0xffffffffu, above)) {   // aref goes to the key with the page's largest score
+      for (int t = 0; t < NT; ++t) {
+        need[t] = fs[t] * mx[t] + fminf(lg2(ma[t]) + vbig, 100.f);
+        due = due || need[t] > st.m[t] + kQ4Slack || fs[t] * mx[t] > st.xref[t] + kQ4Slack || ma[t] > kQ4MaxProbe;
+      }
+      if (__any_sync(0xffffffffu, due)) {
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
+          // aref goes to the key with the page's largest score
           bool mine = false;
           float here = 0.f;
 #pragma unroll
@@ -781,15 +803,6 @@ __global__ void __launch_bounds__(Q4Smem<D, NT>::kThreads, 1) decode_q4_kernel(c
           float shift = __shfl_sync(0xffffffffu, here, holders ? __ffs(holders) - 1 : 0);
           if (!(fs[t] * mx[t] > st.xref[t] + kQ4Slack) || holders == 0) shift = 0.f;
           else st.xref[t] = fs[t] * mx[t];
-          st.aref[t] += shift;
-          st.c[t] = fmaf(-shift, st.l[t], st.c[t]);
-#pragma unroll
-          for (int k = 0; k < 2 * J; ++k) {
-            st.o[t][k][1] = fmaf(-shift, st.o[t][k][0], st.o[t][k][1]);
-            st.o[t][k][3] = fmaf(-shift, st.o[t][k][2], st.o[t][k][3]);
-          }
-#pragma unroll
-          for (int g = 0; g < G; ++g) st.pm[t][g][1] = fmaf(-shift, st.pm[t][g][0], st.pm[t][g][1]);
           ma[t] = 1.f;
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
@@ -798,36 +811,36 @@ __global__ void __launch_bounds__(Q4Smem<D, NT>::kThreads, 1) decode_q4_kernel(c
           }
 #pragma unroll
           for (int off = 4; off < 32; off <<= 1) ma[t] = fmaxf(ma[t], __shfl_xor_sync(0xffffffffu, ma[t], off));
-        }
-      }
-      bool moved = false;
-      float m_new[NT];
+          // large probe values get a larger unit
+          const int up = ma[t] > kQ4MaxProbe ? min((int)(__float_as_uint(ma[t]) >> 23) - 127, 126) : 0;
+          const float f = __uint_as_float((uint32_t)(127 - up) << 23);
+          st.unit[t] *= __uint_as_float((uint32_t)(127 + up) << 23);
+          fa[t] *= f;
+          ma[t] = fmaxf(ma[t] * f, 1.f);
 #pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        const float big = ma[t] * __uint_as_float(vmax);
-        const float need = fs[t] * mx[t] + lg2(fminf(fmaxf(big, 0x1p-60f), 0x1p60f));
-        m_new[t] = need > st.m[t] + kQ4Slack ? need : st.m[t];
-        moved = moved || m_new[t] != st.m[t];
-      }
-      if (__any_sync(0xffffffffu, moved)) {
+          for (int g = 0; g < G; ++g) rs[t][g] *= f;
 #pragma unroll
-        for (int t = 0; t < NT; ++t) {
-          const float alpha = m_new[t] == st.m[t] ? 1.f : ex2(st.m[t] - m_new[t]);
-          st.m[t] = m_new[t];
+          for (int e = 0; e < 8; ++e) av[t][e] *= f;
+          // and the reference moves if it still has to
+          need[t] = fs[t] * mx[t] + fminf(lg2(ma[t]) + vbig, 100.f);
+          const float m_new = need[t] > st.m[t] + kQ4Slack ? need[t] : st.m[t];
+          const float alpha = m_new == st.m[t] ? 1.f : ex2(st.m[t] - m_new), alpha2 = alpha * f;
+          st.m[t] = m_new;
+          st.aref[t] = (st.aref[t] + shift) * f;
+          st.c[t] = fmaf(-shift, st.l[t], st.c[t]) * alpha2;
+          st.l[t] *= alpha;
 #pragma unroll
           for (int k = 0; k < 2 * J; ++k) {
+            st.o[t][k][1] = fmaf(-shift, st.o[t][k][0], st.o[t][k][1]) * alpha2;
+            st.o[t][k][3] = fmaf(-shift, st.o[t][k][2], st.o[t][k][3]) * alpha2;
             st.o[t][k][0] *= alpha;
-            st.o[t][k][1] *= alpha;
             st.o[t][k][2] *= alpha;
-            st.o[t][k][3] *= alpha;
           }
 #pragma unroll
           for (int g = 0; g < G; ++g) {
+            st.pm[t][g][1] = fmaf(-shift, st.pm[t][g][0], st.pm[t][g][1]) * alpha2;
             st.pm[t][g][0] *= alpha;
-            st.pm[t][g][1] *= alpha;
           }
-          st.l[t] *= alpha;
-          st.c[t] *= alpha;
         }
       }
 

@@ -50,16 +50,18 @@ def px():
     return binding
 
 
-def _rows(px, n, H, d, rho, strong, boost, seed):
-    """A paged cache of two sequences of n keys of one KV head; every query points at the keys `strong` (places)."""
+def _rows(px, n, H, d, rho, strong, boost, seed, qs=1.0, ks=1.0, vs=1.0):
+    """A paged cache of two sequences of n keys of one KV head; every query points at the keys `strong` (places).
+    qs, ks, vs: the sizes of queries, keys and values."""
     g = torch.Generator(device="cuda")
     g.manual_seed(seed)
     normal = lambda *s: torch.randn(*s, device="cuda", generator=g)
     base = normal(2, 1, d)
-    q = (base + 0.1 * normal(2, H, d)).bfloat16()
+    q = (qs * (base + 0.1 * normal(2, H, d))).bfloat16()
     k, v = normal(2, n, d), normal(2, n, d)
     for at in strong:
         k[:, at] += boost * d ** 0.5 / base.square().sum(-1) * base[:, 0]
+    k, v = ks * k, vs * v
     pages = -(-n // 64)
     table = torch.tensor(np.random.default_rng(seed).permutation(2 * pages + 3)[:2 * pages].reshape(2, pages),
                          dtype=torch.int32, device="cuda")
@@ -105,6 +107,7 @@ def _check(px, x, **kw):
                               out_dtype=torch.float32, **kw))
     ref, bound, size = _reference(x)
     over = np.abs(got - ref) - (bound * (1 + U) + U * np.abs(ref))
+    assert np.isfinite(got).all()
     assert (over <= 0).all(), f"{over.max():.3e} over the worst case"
     rel = _rms(got - ref) / size
     assert (rel <= 2.0 ** -9).all(), f"a row is {rel.max():.2e} of its terms' size off"
@@ -139,3 +142,17 @@ def test_a_few_keys_hold_the_weight_in_every_form(px, H, d):
 @pytest.mark.parametrize("ctas", [1, 3, 148])
 def test_a_long_row_and_other_grids(px, ctas):
     _check(px, _rows(px, 40000, 4, 128, 1.0, [23456], 12.0, seed=1), num_ctas=ctas)
+
+
+# sizes of queries, keys, values and probes, at both ends of the stated range: entries of q and rho below 2^114, value
+# scales (about a quarter of a value) down to 2^-80, differences of probe values times a value scale up to 2^100
+SIZES = [(1e-10, 1e10, 1e10, 1e5), (2.0 ** -30, 2.0 ** 30, 2.0 ** 30, 2.0 ** 30), (1.0, 1.0, 1e-3, 2.0 ** 100),
+         (1.0, 1.0, 2.0 ** 60, 2.0 ** 30), (1.0, 1.0, 2.0 ** 97, 0.02), (1.0, 1.0, 2.0 ** -75, 1.0),
+         (2.0 ** 75, 2.0 ** -75, 2.0 ** -75, 2.0 ** 70), (2.0 ** 105, 2.0 ** -105, 1.0, 2.0 ** 105),
+         (2.0 ** -100, 2.0 ** 100, 1.0, 2.0 ** -100)]
+
+
+@pytest.mark.parametrize("qs,ks,vs,rho", SIZES)
+def test_sizes_at_the_ends_of_the_range(px, qs, ks, vs, rho):
+    for n, strong in ((200, []), (100, [50]), (700, [7, 640])):
+        _check(px, _rows(px, n, 4, 128, rho, strong, 9.0, seed=n, qs=qs, ks=ks, vs=vs))
