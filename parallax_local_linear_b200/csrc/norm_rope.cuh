@@ -200,7 +200,7 @@ __global__ void __launch_bounds__(kNrFwdThreads, 20) norm_rope_kernel(const Norm
   const int b = a.B == 1 ? 0 : tok / a.T, t = tok - b * a.T;
   const int h0 = chunk * a.hpg;
   const int pos = b < a.B && t < a.T ? nr_position(a, b, t) : -1;
-  const bool live = pos >= 0;
+  const bool live = pos >= 0, turns = ln.col0 < a.rot;
   // y = r (x wc + partner(x) ws) with the weights taken into the rotation
   float2 wc[P], ws[P];
   {
@@ -243,8 +243,10 @@ __global__ void __launch_bounds__(kNrFwdThreads, 20) norm_rope_kernel(const Norm
         for (int i = 0; i < P; ++i) ss = fma2(mul2(f[i], make_float2(1.f / D, 1.f / D)), f[i], ss);   // (overflows only with the mean itself)
         r = rsqrtf(row_sum<L::LPR>(ss.x + ss.y) + a.eps);
       }
+      // (past rot a column passes through: no term of a partner that may not be finite)
 #pragma unroll
-      for (int i = 0; i < P; ++i) o[i] = mul2(fma2(f[i], wc[i], mul2(L::partner(f, i), ws[i])), make_float2(r, r));
+      for (int i = 0; i < P; ++i)
+        o[i] = mul2(turns ? fma2(f[i], wc[i], mul2(L::partner(f, i), ws[i])) : mul2(f[i], wc[i]), make_float2(r, r));
       if (j + u < heads) ln.store(y + (j + u) * set.ys[2], o);
     }
   }
@@ -270,6 +272,7 @@ __global__ void __launch_bounds__(kNrThreads, kNrBwdCtasPerSm) norm_rope_bwd_ker
     if (set.w == nullptr) w[i] = make_float2(1.f, 1.f);
     acc[i] = make_float2(0.f, 0.f);
   }
+  const bool turns = ln.col0 < a.rot;   // (past rot a column passes through)
   const int groups = set.ctas * (kNrThreads / L::LPR), tokens = a.B * a.T;
   const uint32_t items = (uint32_t)tokens * set.chunks;
   const uint32_t group = (blockIdx.x - set.first_cta) * (kNrThreads / L::LPR) + threadIdx.x / L::LPR;
@@ -370,8 +373,9 @@ __global__ void __launch_bounds__(kNrThreads, kNrBwdCtasPerSm) norm_rope_bwd_ker
       for (int i = 0; i < P; ++i) {
         // dn: the transposed rotation
         const float2 sn = tn.s[i % tn.N];
-        d[i] = fma2(e[i], tn.c[i % tn.N],
-                    mul2(L::partner(e, i), kInter ? make_float2(sn.x, -sn.y) : i < L::H ? sn : neg2(sn)));
+        d[i] = turns ? fma2(e[i], tn.c[i % tn.N],
+                            mul2(L::partner(e, i), kInter ? make_float2(sn.x, -sn.y) : i < L::H ? sn : neg2(sn)))
+                     : e[i];
         g[i] = mul2(d[i], w[i]);
         const float2 fd = mul2(f[i], make_float2(1.f / D, 1.f / D));
         ss = fma2(fd, f[i], ss);
