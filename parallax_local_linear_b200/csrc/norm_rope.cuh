@@ -167,8 +167,9 @@ struct NrLane {
   static __device__ __forceinline__ float2 partner(const float2 (&f)[P], int i) {
     return kInter ? make_float2(f[i].y, f[i].x) : f[(i + H) % P];
   }
-  __device__ __forceinline__ void store(T* row, const float2 (&o)[P]) const {
-    const uint4 v = RowVec<T>::pack(o);
+  // Zeros where `zero`.
+  __device__ __forceinline__ void store(T* row, const float2 (&o)[P], bool zero = false) const {
+    const uint4 v = zero ? make_uint4(0, 0, 0, 0) : RowVec<T>::pack(o);
     store_row(row + col0, v.x, v.y);
     store_row(row + col1, v.z, v.w);
   }
@@ -390,7 +391,7 @@ __global__ void __launch_bounds__(kNrThreads, kNrBwdCtasPerSm) norm_rope_bwd_ker
           acc[i] = fma2(d[i], mul2(f[i], make_float2(r, r)), acc[i]);
         }
       }
-      if (j < it.heads) ln.store(it.dx + j * set.ys[2], g);
+      if (j < it.heads) ln.store(it.dx + j * set.ys[2], g, it.pos < 0);   // (a weight may not be finite)
     }
   }
   if (set.dw == nullptr) return;

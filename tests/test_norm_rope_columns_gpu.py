@@ -88,3 +88,17 @@ def test_infinite_rows_with_the_norm(px, d, rot, inter, dtype):
     w = (1 + 0.1 * torch.randn(d, device="cuda")).to(dtype)
     y = px.norm_rope(x, None, None, cos, sin, q_weight=w, interleaved=inter)[0]
     assert torch.isnan(y[hit]).all() and (y[~hit] == 0).all()
+
+
+@pytest.mark.parametrize("norm", [True, False])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_padding_rows_get_zero_gradients_whatever_the_weights(px, norm, dtype):
+    x, cos, sin = _case(128, 64, dtype, seed=5)
+    pos = torch.arange(37, device="cuda", dtype=torch.int32)
+    pos[::3] = -1
+    w = torch.ones(128, device="cuda", dtype=dtype)
+    w[7], w[100] = float("inf"), float("nan")
+    x[::3, :, 4] = float("nan")       # padding rows are not read
+    dx, _, _, dw, _, _ = px.norm_rope_backward(x, None, None, x, None, None, cos, sin, pos,
+                                               q_weight=w if norm else None, norm=norm)
+    assert (dx[::3] == 0).all() and (not norm or torch.isfinite(dw).all())
