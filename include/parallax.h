@@ -673,6 +673,12 @@ int32_t parallax_last_cuda_error(void);
 /* CUDA's description of a cudaError_t value. */
 const char* parallax_cuda_error_string(int32_t code);
 
+/* A number that names the capture which `stream` is in (the same for every
+ * stream of one capture, another for every capture of the process), or 0 when
+ * the stream is not being captured.  For callers that keep workspaces: what a
+ * capture records happens when its graph runs, not at once. */
+uint64_t parallax_capture_id(cudaStream_t stream);
+
 /* Static string naming a status. */
 const char* parallax_status_string(plx_status s);
 

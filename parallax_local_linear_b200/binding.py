@@ -137,6 +137,8 @@ lib.parallax_last_cuda_error.restype = ctypes.c_int32
 lib.parallax_last_cuda_error.argtypes = []
 lib.parallax_cuda_error_string.restype = ctypes.c_char_p
 lib.parallax_cuda_error_string.argtypes = [ctypes.c_int32]
+lib.parallax_capture_id.restype = ctypes.c_uint64
+lib.parallax_capture_id.argtypes = [_vp]
 lib.parallax_last_device_error.restype = ctypes.c_int
 lib.parallax_last_device_error.argtypes = [_vp, ctypes.POINTER(ctypes.c_int32)]
 
@@ -280,29 +282,42 @@ _ws_lock = threading.Lock()
 _workspaces = {}
 
 
-def _workspace(device, nbytes, params):
-    """A zero-initialised workspace per device, grown on demand.
+def _kept_workspace(kind, index, partials, counters):
+    """(tensor, bytes for counters) of a workspace that the binding keeps for calls of ``kind``:
+    that many bytes for counters at one end, which are zero before every call, and the rest for
+    partials, each the most that a call has needed, so that one call's partials never lie where
+    another's counters do.
 
-    The counter region at its front (4 bytes per unit, padded to 256) must
-    start at zero, and the library leaves it zero after every call.  What lies
-    behind one call's counters holds its partials, though, and a later call
-    with more units has counters there: those are cleared for it.
+    There is one per device and stream, since calls on different streams may overlap, and
+    another per capture and stream: graphs may be replayed at once, and what a capture records
+    is not done yet.  A graph clears its counters when it starts; after that, as in direct
+    calls, every call leaves them zero.
     """
-    if nbytes == 0:
-        return None
+    stream = _raw_stream(index)
+    capture = lib.parallax_capture_id(stream) if _capturing(index) else 0
+    key = kind, index, stream, capture != 0
+    with _ws_lock:
+        ws, owner, most, room = _workspaces.get(key, (None, 0, 0, 0))
+        if ws is None or owner != capture or partials > most or counters > room:
+            if owner != capture:
+                most = room = 0
+            most, room = max(most, partials, 1 << 20), max(room, counters, 1 << 14)
+            if capture:
+                ws = torch.empty(room + most, dtype=torch.uint8, device=index)
+                (ws[-room:] if kind == "q4" else ws[:room]).zero_()
+            else:
+                ws = torch.zeros(room + most, dtype=torch.uint8, device=index)
+            _workspaces[key] = ws, capture, most, room
+        return ws, room
+
+
+def _decode_workspace(index, nbytes, params):
+    """(address, bytes) of a decode's workspace: its counters (4 bytes per unit, padded to 256) end
+    where the partials of every call start."""
     units = params.batch * (params.num_kv_heads if params.in_dtype == PLX_BF16 else params.num_q_heads)
     counters = (4 * units + 255) & ~255
-    idx = device.index if device.index is not None else torch.cuda.current_device()
-    with _ws_lock:
-        ws, clean = _workspaces.get(idx, (None, 0))
-        if ws is None or ws.numel() < nbytes:
-            ws = torch.zeros(max(nbytes, 1 << 20), dtype=torch.uint8, device=device)
-        elif counters > clean:
-            ws[:counters].zero_()
-            if torch.cuda.is_current_stream_capturing():   # cleared when the graph runs, not yet
-                counters = clean
-        _workspaces[idx] = (ws, counters)
-        return ws
+    ws, room = _kept_workspace("decode", index, nbytes - counters, counters)
+    return ws.data_ptr() + room - counters, ws.numel() - room + counters
 
 
 _lla_workspaces = {}
@@ -368,10 +383,9 @@ def decode(q, rho, k_cache, v_cache, scale=None, *, seq_lens=None, page_table=No
     p = decode_params(q, k_cache, page_table=page_table, kv_len=kv_len, scale=scale,
                       out_dtype=out_dtype, num_ctas=num_ctas)
     nbytes = decode_workspace_size(p)
-    ws = _workspace(q.device, nbytes, p)
+    ws, ws_bytes = _decode_workspace(q.get_device(), nbytes, p)
     st = lib.parallax_decode(_ptr(q), _ptr(rho), _ptr(k_cache), _ptr(v_cache), _ptr(page_table),
-                             _ptr(seq_lens), _ptr(out), _ptr(ws), 0 if ws is None else ws.numel(),
-                             ctypes.byref(p), _stream_ptr(q.device))
+                             _ptr(seq_lens), _ptr(out), ws, ws_bytes, ctypes.byref(p), _stream_ptr(q.device))
     if st != 0:
         raise ParallaxError(st, "parallax_decode")
     return out
@@ -476,11 +490,11 @@ def decode_projected(x, w_q, w_rho, k_cache, v_cache, scale=None, *, seq_lens=No
     p = decode_params(q_out, k_cache, page_table=page_table, kv_len=kv_len, scale=scale,
                       out_dtype=out_dtype, num_ctas=num_ctas)
     nbytes = decode_workspace_size(p)
-    ws = _workspace(x.device, nbytes, p)
+    ws, ws_bytes = _decode_workspace(x.get_device(), nbytes, p)
     st = lib.parallax_decode_projected(_ptr(x), _ptr(w_q), _ptr(w_rho), int(x.shape[1]), _ptr(k_cache),
                                        _ptr(v_cache), _ptr(page_table), _ptr(seq_lens), _ptr(q_out),
-                                       _ptr(rho_out), _ptr(out), _ptr(ws), 0 if ws is None else ws.numel(),
-                                       ctypes.byref(p), _stream_ptr(x.device))
+                                       _ptr(rho_out), _ptr(out), ws, ws_bytes, ctypes.byref(p),
+                                       _stream_ptr(x.device))
     if st != 0:
         raise ParallaxError(st, "parallax_decode_projected")
     return out, q_out, rho_out
@@ -1112,36 +1126,10 @@ def cache_gather_q4(kv_cache, slot_map, *, out_dtype=torch.bfloat16, out=None):
     return k, v
 
 
-_q4_workspaces = {}
-
-
-def _q4_workspace(index, nbytes, units):
-    """The 4-bit decode's workspace where the caller gives none: one per device
-    and stream, since calls on different streams may overlap.  Partials are at
-    its front and the counters (4 bytes a unit) at its end; it is large enough
-    for the most of either that a call has needed, so that one call's partials
-    never reach another's counters, and zeroed when allocated.  A captured graph
-    gets one of its own, whose counters it clears, so that graphs replayed at
-    once do not share it."""
-    counters = (4 * units + 255) & ~255
-    if _capturing(index):
-        ws = torch.empty(nbytes, dtype=torch.uint8, device=index)
-        ws[-counters:].zero_()
-        return ws
-    key = (index, _raw_stream(index))
-    with _ws_lock:
-        ws, most_slots, most_counters = _q4_workspaces.get(key, (None, 1 << 20, 1 << 14))
-        if ws is None or nbytes - counters > most_slots or counters > most_counters:
-            most_slots, most_counters = max(most_slots, nbytes - counters), max(most_counters, counters)
-            ws = torch.zeros(most_slots + most_counters, dtype=torch.uint8, device=index)
-            _q4_workspaces[key] = ws, most_slots, most_counters
-        return ws
-
-
 def decode_q4_workspace(q, kv_cache, *, page_table=None, kv_len=None, num_ctas=0):
     """A zeroed workspace for decode_q4 calls of these shapes (pass it as
-    ``workspace``): for a captured graph, which otherwise clears counters at each
-    replay.  Calls that share one must not overlap on the GPU."""
+    ``workspace``), for a graph that otherwise clears the counters when it starts.
+    Calls that share one must not overlap on the GPU."""
     B, Hkv = q.shape[0], kv_cache.shape[1]
     if kv_len is None:
         kv_len = PAGE_SIZE * (kv_cache.shape[2] if page_table is None else page_table.shape[1])
@@ -1162,7 +1150,7 @@ def decode_q4(q, rho, kv_cache, scale=None, *, seq_lens=None, page_table=None, o
     kv_cache [B, Hkv, ceil(kv_len / 64), block bytes] with ``kv_len`` (default:
     all of its pages' tokens) and optional seq_lens.  Returns out [B, Hq, d] in
     ``out_dtype`` (default bfloat16).  ``workspace``: see decode_q4_workspace
-    (default: one that the binding keeps for the stream).
+    (default: one that the binding keeps for the stream or the capture).
     """
     shape, blocks = q.shape, kv_cache.shape
     if len(shape) != 3 or rho.shape != shape:
@@ -1219,7 +1207,8 @@ def decode_q4(q, rho, kv_cache, scale=None, *, seq_lens=None, page_table=None, o
         _check_shape("workspace", workspace, (workspace.numel(),))
     else:
         nbytes = _workspace_size(index, 1, lib.parallax_decode_q4_workspace_size, p, 0)
-        workspace = _q4_workspace(index, nbytes, B * Hkv)
+        counters = (4 * B * Hkv + 255) & ~255   # at the end
+        workspace, _ = _kept_workspace("q4", index, nbytes - counters, counters)
     _call(index, lib.parallax_decode_q4, q.data_ptr(), rho.data_ptr(), kv_cache.data_ptr(), _raw(page_table),
           _raw(seq_lens), out.data_ptr(), workspace.data_ptr(), workspace.numel(), p)
     return out

@@ -1021,6 +1021,16 @@ int32_t parallax_last_cuda_error(void) {
   return e;
 }
 
+uint64_t parallax_capture_id(cudaStream_t stream) {
+  cudaStreamCaptureStatus status = cudaStreamCaptureStatusNone;
+  unsigned long long id = 0;
+  if (cudaStreamGetCaptureInfo(stream, &status, &id) != cudaSuccess) {
+    (void)cudaGetLastError();
+    return 0;
+  }
+  return status == cudaStreamCaptureStatusActive ? (uint64_t)id + 1 : 0;
+}
+
 const char* parallax_cuda_error_string(int32_t code) { return cudaGetErrorString((cudaError_t)code); }
 
 plx_status parallax_last_device_error(cudaStream_t stream, int32_t* code) {
