@@ -284,9 +284,9 @@ _workspaces = {}
 
 def _kept_workspace(kind, index, partials, counters):
     """(tensor, bytes for counters) of a workspace that the binding keeps for calls of ``kind``:
-    that many bytes for counters at one end, which are zero before every call, and the rest for
-    partials, each the most that a call has needed, so that one call's partials never lie where
-    another's counters do.
+    that many bytes for counters at one end (none where ``counters`` is 0), which are zero before
+    every call, and the rest for partials, each the most that a call has needed, so that one
+    call's partials never lie where another's counters do.
 
     There is one per device and stream, since calls on different streams may overlap, and
     another per capture and stream: graphs may be replayed at once, and what a capture records
@@ -301,12 +301,9 @@ def _kept_workspace(kind, index, partials, counters):
         if ws is None or owner != capture or partials > most or counters > room:
             if owner != capture:
                 most = room = 0
-            most, room = max(most, partials, 1 << 20), max(room, counters, 1 << 14)
-            if capture:
-                ws = torch.empty(room + most, dtype=torch.uint8, device=index)
-                (ws[-room:] if kind == "q4" else ws[:room]).zero_()
-            else:
-                ws = torch.zeros(room + most, dtype=torch.uint8, device=index)
+            most, room = max(most, partials, 1 << 20), max(room, counters, 1 << 14) if counters else 0
+            ws = torch.empty(room + most, dtype=torch.uint8, device=index)
+            (ws[most:] if kind == "q4" else ws[:room]).zero_()
             _workspaces[key] = ws, capture, most, room
         return ws, room
 
@@ -318,22 +315,6 @@ def _decode_workspace(index, nbytes, params):
     counters = (4 * units + 255) & ~255
     ws, room = _kept_workspace("decode", index, nbytes - counters, counters)
     return ws.data_ptr() + room - counters, ws.numel() - room + counters
-
-
-_lla_workspaces = {}
-
-
-def _lla_workspace(device, nbytes):
-    """The LLA pass's scratch per device, grown on demand.  It is kept apart
-    from the decode workspace: LLA writes its records over the whole buffer,
-    while a decode workspace's counter region must stay zero between calls."""
-    idx = device.index if device.index is not None else torch.cuda.current_device()
-    with _ws_lock:
-        ws = _lla_workspaces.get(idx)
-        if ws is None or ws.numel() < nbytes:
-            ws = torch.empty(max(nbytes, 1 << 20), dtype=torch.uint8, device=device)
-            _lla_workspaces[idx] = ws
-        return ws
 
 
 def decode_params(q, k_cache, *, page_table=None, kv_len=None, scale=None, out_dtype=None,
@@ -544,9 +525,9 @@ def lla_decode(q, k_cache, v_cache, scale=None, ridge=0.0, *, seq_lens=None, pag
     nbytes = lib.parallax_lla_decode_workspace_size(ctypes.byref(p), float(ridge), 0)
     if nbytes == SIZE_MAX:
         raise ParallaxError(1, "parallax_lla_decode_workspace_size")
-    ws = _lla_workspace(q.device, nbytes)
+    ws, _ = _kept_workspace("lla", q.get_device(), nbytes, 0)   # (written before it is read)
     st = lib.parallax_lla_decode(_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(page_table), _ptr(seq_lens),
-                                 float(ridge), _ptr(rho_out), _ptr(out), _ptr(ws), 0 if ws is None else ws.numel(),
+                                 float(ridge), _ptr(rho_out), _ptr(out), _ptr(ws), ws.numel(),
                                  ctypes.byref(p), _stream_ptr(q.device))
     if st != 0:
         raise ParallaxError(st, "parallax_lla_decode")

@@ -164,3 +164,27 @@ def test_a_graph_clears_its_counters_once(px):
         out.fill_(float("nan"))
         g.replay()
         assert torch.equal(out, want)
+
+
+def test_streams_and_captures_have_workspaces_of_their_own(px):
+    # what overlapping calls write must lie apart, also where a race would rarely show
+    index = torch.cuda.current_device()
+    for kind, counters in (("decode", 512), ("q4", 512), ("lla", 0)):
+        spans = []
+        def take(nbytes):
+            ws, room = px._kept_workspace(kind, index, nbytes, counters)
+            assert ws.numel() - room >= nbytes and room >= counters
+            spans.append((ws.data_ptr(), ws.data_ptr() + ws.numel()))
+            return ws
+        keep = [take(1000)]
+        assert keep[0].data_ptr() == take(2000).data_ptr() and spans.pop()
+        for s in (torch.cuda.Stream(), torch.cuda.Stream()):
+            with torch.cuda.stream(s):
+                keep.append(take(1000))
+        graphs = [torch.cuda.CUDAGraph() for _ in range(2)]
+        for g in graphs:
+            torch.cuda.synchronize()
+            with torch.cuda.graph(g):
+                keep.append(take(3 << 20))
+        spans.sort()
+        assert all(a[1] <= b[0] for a, b in zip(spans, spans[1:]))
