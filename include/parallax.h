@@ -509,8 +509,10 @@ typedef struct plx_norm_rope_params {
 /* One set of head rows: x[b, t, h] at x + b * x_stride[0] + t * x_stride[1] +
  * h * x_stride[2] elements, d contiguous columns; y likewise.  Pointers are
  * 16-byte aligned and strides multiples of 16 bytes.  y may be x itself with
- * the same strides (in place); otherwise it must not overlap any input.  A
- * stride of y is 0 only where there is one entry. */
+ * the same strides (in place); otherwise it overlaps no input and no other
+ * output (PLX_ERR_INVALID_ARG; rows that lie in each other's gaps, as slices of
+ * one fused projection do, are apart).  A stride of y is 0 only where there is
+ * one entry. */
 typedef struct plx_head_rows {
   const void* x;
   void* y;
@@ -532,7 +534,8 @@ plx_status parallax_norm_rope(const plx_head_rows* rows, int32_t num_sets, const
 /* Gradients.  Set i of the forward has its x and w in rows[i].x and .w, and
  * grads[i]:
  *   dy          device, dL/dy, strides dy_stride (as x_stride).
- *   dx          device, dL/dx, strides dx_stride; may be dy itself with the same strides.
+ *   dx          device, dL/dx, strides dx_stride; may be the set's dy or x itself with the same
+ *               strides; dx and dw otherwise overlap no input and no other output.
  *   dw          device float32 [d], dL/dw summed over every row, or NULL.
  * rows[i].y is not used.  Padding rows (as above) get dx = 0 and add nothing
  * to dw.  With norm 0 dw must be NULL.

@@ -46,6 +46,133 @@ bool distinct(const int64_t* s, const int64_t* count, int n) {
   return true;
 }
 
+// Strided runs of bytes: at base + sum k_i stride_i, k_i < count_i, `run` bytes
+// each, all within lo .. hi - 1.
+using Wide = __int128;   // (strides are the caller's)
+struct Runs {
+  const void* base;
+  Wide stride[3];
+  int64_t count[3], run;
+  Wide lo, hi;
+};
+
+Runs head_runs(const void* base, const int64_t* stride, const int64_t* count, int d, int elt) {
+  Runs r{base, {}, {}, (int64_t)d * elt, (Wide)reinterpret_cast<uintptr_t>(base), 0};
+  r.hi = r.lo + r.run;
+  for (int i = 0; i < 3; ++i) {
+    r.stride[i] = (Wide)stride[i] * elt;
+    r.count[i] = count[i];
+    const Wide last = r.stride[i] * (count[i] - 1);
+    (last < 0 ? r.lo : r.hi) += last;
+  }
+  return r;
+}
+Runs flat_run(const void* base, int64_t bytes) {
+  const Wide at = (Wide)reinterpret_cast<uintptr_t>(base);
+  return {base, {0, 0, 0}, {1, 1, 1}, bytes, at, at + bytes};
+}
+bool same_runs(const Runs& a, const Runs& b) {
+  bool same = a.base == b.base && a.run == b.run;
+  for (int i = 0; i < 3; ++i) same = same && a.count[i] == b.count[i] && (a.stride[i] == b.stride[i] || a.count[i] == 1);
+  return same;
+}
+
+// Do runs of a and b share a byte?  Exact, so that slices of one fused
+// projection, which lie in each other's gaps, do not count: is there a difference
+// of places sum k_i stride_i + (a - b) within (-a.run, b.run)?  Dimensions are
+// taken from the largest stride down; what the smaller ones can still add leaves
+// one or two k for each (where strides lie so that there are many, the answer
+// after kMaxSteps is yes).
+bool runs_overlap(const Runs& a, const Runs& b) {
+  if (a.hi <= b.lo || b.hi <= a.lo) return false;
+  struct Dim {
+    Wide stride, lo, hi;   // k in lo .. hi
+  };
+  if (a.base == nullptr || b.base == nullptr || a.run <= 0 || b.run <= 0) return false;
+  Dim dim[6];
+  int n = 0;
+  auto put = [&](Wide stride, Wide lo, Wide hi) {
+    if (stride == 0 || lo == hi) return;
+    if (stride < 0) {
+      stride = -stride;
+      const Wide t = lo;
+      lo = -hi;
+      hi = -t;
+    }
+    int at = 0;
+    while (at < n && dim[at].stride > stride) ++at;
+    if (at < n && dim[at].stride == stride) {
+      dim[at].lo += lo;
+      dim[at].hi += hi;
+      return;
+    }
+    for (int i = n++; i > at; --i) dim[i] = dim[i - 1];
+    dim[at] = {stride, lo, hi};
+  };
+  for (int i = 0; i < 3; ++i) {
+    if (a.count[i] <= 0 || b.count[i] <= 0) return false;
+    put(a.stride[i], 0, a.count[i] - 1);
+    put(b.stride[i], -(b.count[i] - 1), 0);
+  }
+  constexpr int kMaxSteps = 4096;
+  int steps = 0;
+  auto meet = [&](auto&& self, int i, Wide delta) -> bool {
+    Wide lo = 0, hi = 0;   // what dimensions i and on can add
+    for (int k = i; k < n; ++k) {
+      lo += dim[k].lo * dim[k].stride;
+      hi += dim[k].hi * dim[k].stride;
+    }
+    if (delta + hi <= -a.run || delta + lo >= b.run) return false;
+    if (i == n || ++steps > kMaxSteps) return true;
+    const Wide s = dim[i].stride, rest_lo = lo - dim[i].lo * s, rest_hi = hi - dim[i].hi * s;
+    // k s in (-a.run - delta - rest_hi, b.run - delta - rest_lo)
+    Wide k = (-a.run - delta - rest_hi) / s - 1, end = (b.run - delta - rest_lo) / s + 1;
+    if (k < dim[i].lo) k = dim[i].lo;
+    if (end > dim[i].hi) end = dim[i].hi;
+    for (; k <= end; ++k)
+      if (self(self, i + 1, delta + k * s)) return true;
+    return false;
+  };
+  return meet(meet, 0, (Wide)reinterpret_cast<uintptr_t>(a.base) - (Wide)reinterpret_cast<uintptr_t>(b.base));
+}
+
+// Outputs of a norm + rotation call lie apart from each other and from what it
+// reads; one may be its own set's rows, place by place.
+bool norm_rope_apart(const plx_head_rows* rows, const plx_head_grads* grads, int32_t num_sets, const float* cos,
+                     const float* sin, const int32_t* positions, const plx_norm_rope_params* p) {
+  const int elt = p->dtype == PLX_BF16 ? 2 : 4, d = p->head_dim;
+  if (p->tokens == 0) return true;
+  Runs in[2 * kNrMaxSets], out[2 * kNrMaxSets], flat[kNrMaxSets + 3];
+  int n_in = 0, n_out = 0, n_flat = 0;
+  for (int i = 0; i < num_sets; ++i) {
+    const int64_t count[3] = {p->batch, p->tokens, rows[i].heads};
+    out[n_out++] = grads ? head_runs(grads[i].dx, grads[i].dx_stride, count, d, elt)
+                         : head_runs(rows[i].y, rows[i].y_stride, count, d, elt);
+    if (!grads || p->norm) in[n_in++] = head_runs(rows[i].x, rows[i].x_stride, count, d, elt);
+    if (grads) in[n_in++] = head_runs(grads[i].dy, grads[i].dy_stride, count, d, elt);
+    if (rows[i].w) flat[n_flat++] = flat_run(rows[i].w, (int64_t)d * elt);
+  }
+  const int rows_out = n_out;
+  const int per_set = n_in / num_sets;
+  if (grads)
+    for (int i = 0; i < num_sets; ++i)
+      if (grads[i].dw) out[n_out++] = flat_run(grads[i].dw, (int64_t)d * 4);
+  if (p->rot_dim > 0) {
+    flat[n_flat++] = flat_run(cos, (int64_t)p->max_pos * p->rot_dim * 2);
+    flat[n_flat++] = flat_run(sin, (int64_t)p->max_pos * p->rot_dim * 2);
+  }
+  if (positions) flat[n_flat++] = flat_run(positions, 4 * (p->pos_batch_stride * (p->batch - 1) + p->tokens));
+  for (int i = 0; i < n_out; ++i) {
+    for (int j = 0; j < n_in; ++j)
+      if (!(i < rows_out && j / per_set == i && same_runs(out[i], in[j])) && runs_overlap(out[i], in[j])) return false;
+    for (int j = 0; j < n_flat; ++j)
+      if (runs_overlap(out[i], flat[j])) return false;
+    for (int j = 0; j < i; ++j)
+      if (runs_overlap(out[i], out[j])) return false;
+  }
+  return true;
+}
+
 plx_status validate_norm_rope(const plx_head_rows* rows, const plx_head_grads* grads, int32_t num_sets,
                               const float* cos, const float* sin, const int32_t* positions,
                               const plx_norm_rope_params* p) {
@@ -84,7 +211,7 @@ plx_status validate_norm_rope(const plx_head_rows* rows, const plx_head_grads* g
       if (g.dw && (!p->norm || !aligned(g.dw, 4))) return PLX_ERR_INVALID_ARG;
     }
   }
-  return PLX_OK;
+  return norm_rope_apart(rows, grads, num_sets, cos, sin, positions, p) ? PLX_OK : PLX_ERR_INVALID_ARG;
 }
 
 // The backward's grid: one CTA per set at least.
