@@ -577,7 +577,8 @@ typedef struct plx_append_params {
  *   slot_map   device int64 [N].  A negative slot skips its row; one past the
  *              pool sets PLX_DEVERR_BAD_PAGE and skips it.  Slots are distinct
  *              (a slot that two rows share gets either's bytes, or some of both).
- *   k_cache, v_cache  device [P, Hkv, 64, d] of p->dtype. */
+ *   k_cache, v_cache  device [P, Hkv, 64, d] of p->dtype, apart from each other
+ *              and from slot_map (PLX_ERR_INVALID_ARG). */
 plx_status parallax_cache_append(const void* k, const void* v, const int64_t* slot_map, void* k_cache,
                                  void* v_cache, const plx_append_params* p, cudaStream_t stream);
 
@@ -614,7 +615,8 @@ plx_status parallax_cache_append_q4(const void* k, const void* v, const int64_t*
 /* The keys and values that the slots stand for: k, v [N, Hkv, d] of p->dtype
  * (fp32: s n + m rounded once; bf16: that rounded again) with p's strides.
  * Rows with a negative slot, or one past the pool (PLX_DEVERR_BAD_PAGE), are
- * left as they were. */
+ * left as they were.  k and v overlap neither each other nor an input
+ * (PLX_ERR_INVALID_ARG; rows in each other's gaps are apart). */
 plx_status parallax_cache_gather_q4(const void* kv_cache, const int64_t* slot_map, void* k, void* v,
                                     const plx_append_params* p, cudaStream_t stream);
 

@@ -314,6 +314,16 @@ plx_status validate_append(const plx_append_params* p) {
   return PLX_OK;
 }
 
+// Two pools, or two results of a gather, apart from each other and from the slots
+// (and results from the cache).
+bool rows_apart(const Runs& k, const Runs& v, const int64_t* slots, const plx_append_params* p,
+                const Runs& cache = flat_run(nullptr, 0)) {
+  const Runs s = flat_run(slots, 8 * (int64_t)p->num_rows);
+  return !runs_overlap(k, v) && !runs_overlap(k, s) && !runs_overlap(v, s) && !runs_overlap(k, cache) &&
+         !runs_overlap(v, cache);
+}
+int64_t pool_bytes(const plx_append_params* p, int64_t block) { return (int64_t)p->num_pages * p->num_kv_heads * block; }
+
 AppendArgs append_args(const int64_t* slots, const plx_append_params* p) {
   AppendArgs a{};
   a.slots = slots;
@@ -518,6 +528,9 @@ plx_status parallax_cache_append(const void* k, const void* v, const int64_t* sl
   if (!k_cache || !v_cache || !aligned(k_cache, 16) || !aligned(v_cache, 16)) return PLX_ERR_INVALID_ARG;
   if (p->num_rows == 0) return PLX_OK;
   if (!k || !v || !slot_map || !aligned(k, 16) || !aligned(v, 16) || !aligned(slot_map, 8)) return PLX_ERR_INVALID_ARG;
+  const int64_t block = (int64_t)kQ4Page * p->head_dim * (p->dtype == PLX_BF16 ? 2 : 4);
+  if (!rows_apart(flat_run(k_cache, pool_bytes(p, block)), flat_run(v_cache, pool_bytes(p, block)), slot_map, p))
+    return PLX_ERR_INVALID_ARG;
   AppendArgs a = append_args(slot_map, p);
   a.k = k;
   a.v = v;
@@ -558,6 +571,12 @@ plx_status parallax_cache_gather_q4(const void* kv_cache, const int64_t* slot_ma
   if (!k || !v || !slot_map || !aligned(k, 16) || !aligned(v, 16) || !aligned(slot_map, 8)) return PLX_ERR_INVALID_ARG;
   const int64_t count[2] = {p->num_rows, p->num_kv_heads};
   if (!distinct(p->k_stride, count, 2) || !distinct(p->v_stride, count, 2)) return PLX_ERR_INVALID_ARG;
+  const int elt = p->dtype == PLX_BF16 ? 2 : 4;
+  const int64_t rows[3] = {1, count[0], count[1]}, ks[3] = {0, p->k_stride[0], p->k_stride[1]},
+                vs[3] = {0, p->v_stride[0], p->v_stride[1]};
+  if (!rows_apart(head_runs(k, ks, rows, p->head_dim, elt), head_runs(v, vs, rows, p->head_dim, elt), slot_map, p,
+                  flat_run(kv_cache, pool_bytes(p, parallax_q4_block_bytes(p->head_dim)))))
+    return PLX_ERR_INVALID_ARG;
   AppendArgs a = append_args(slot_map, p);
   a.k_out = k;
   a.v_out = v;

@@ -67,3 +67,16 @@ def test_overlapping_outputs_are_refused(px):
     for out in ((y, y, None), (y, x, None)):
         with pytest.raises(px.ParallaxError):
             px.norm_rope(x, y.clone(), None, cos, sin, out=out)
+
+
+def test_gather_into_gaps(px):
+    # keys and values of a token side by side, as a fused [N, 2, Hkv, d] buffer holds them
+    k, v = (torch.randn(70, 2, 128, device="cuda").bfloat16() for _ in range(2))
+    cache, slots = px.q4_cache(2, 2, 128), torch.arange(70, device="cuda") + 13
+    px.cache_append_q4(k, v, slots, cache)
+    want = px.cache_gather_q4(cache, slots)
+    both = torch.zeros(70, 2, 2, 128, device="cuda").bfloat16()
+    px.cache_gather_q4(cache, slots, out=(both[:, 0], both[:, 1]))
+    assert torch.equal(both[:, 0], want[0]) and torch.equal(both[:, 1], want[1])
+    with pytest.raises(px.ParallaxError):
+        px.cache_gather_q4(cache, slots, out=(both[:, 0], both[:, 0]))
