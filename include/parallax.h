@@ -637,6 +637,8 @@ plx_status parallax_cache_gather_q4(const void* kv_cache, const int64_t* slot_ma
  *               parameters with the same workspace_bytes as long as the
  *               partials (the rest of what a call needs, from the front)
  *               never reach another call's counters.
+ *   out         may be q or rho itself (bf16); otherwise it overlaps no input and
+ *               not the workspace (PLX_ERR_INVALID_ARG).
  *   the rest    as parallax_decode.  Hq / Hkv <= 8.
  * Weights enter the value product in 22 bits, sums are fp32.  Range: entries
  * of q and rho below 2^114 in size, value scales s of 2^-84 or more (smaller

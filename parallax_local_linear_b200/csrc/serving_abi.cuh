@@ -607,6 +607,17 @@ plx_status parallax_decode_q4(const void* q, const void* rho, const void* kv_cac
   if (paged && (page_table == nullptr || seq_lens == nullptr)) return PLX_ERR_INVALID_ARG;
   if (!paged && page_table != nullptr) return PLX_ERR_INVALID_ARG;
   if ((page_table && !aligned(page_table, 4)) || (seq_lens && !aligned(seq_lens, 4))) return PLX_ERR_INVALID_ARG;
+  // (a unit's queries and probes are read before its rows are written, by all that read them)
+  const bool in_place = p->out_dtype == PLX_BF16;
+  const size_t rows = (size_t)p->batch * p->num_q_heads * p->head_dim, n = rows * (in_place ? 2 : 4);
+  const size_t pages = paged ? p->num_pages : (size_t)p->batch * ((p->kv_len + kQ4Page - 1) / kQ4Page);
+  if ((!(in_place && out == q) && overlaps(out, n, q, 2 * rows)) ||
+      (!(in_place && out == rho) && overlaps(out, n, rho, 2 * rows)) ||
+      overlaps(out, n, kv_cache, pages * p->num_kv_heads * parallax_q4_block_bytes(p->head_dim)) ||
+      (workspace && overlaps(out, n, workspace, workspace_bytes)) ||
+      (page_table && overlaps(out, n, page_table, 4 * (size_t)p->batch * p->max_pages_per_seq)) ||
+      (seq_lens && overlaps(out, n, seq_lens, 4 * (size_t)p->batch)))
+    return PLX_ERR_INVALID_ARG;
   const int num_sms = current_device_sms();
   if (num_sms <= 0) return PLX_ERR_CUDA;
   const DecodeQ4Plan pl = plan_decode_q4(p, num_sms);
@@ -614,7 +625,6 @@ plx_status parallax_decode_q4(const void* q, const void* rho, const void* kv_cac
       workspace_bytes < pl.counter_bytes + pl.slot_bytes)
     return PLX_ERR_WORKSPACE;
   if (p->kv_len == 0) {   // every sequence is empty: the output is zero
-    const size_t n = (size_t)p->batch * p->num_q_heads * p->head_dim * (p->out_dtype == PLX_BF16 ? 2 : 4);
     return note(cudaMemsetAsync(out, 0, n, stream)) == cudaSuccess ? PLX_OK : PLX_ERR_CUDA;
   }
   DecodeQ4Args a{};

@@ -32,3 +32,14 @@ def test_append_pools(px, k_cache, v_cache, slots):
     (A, V(E.value + 9216), C, {}), (A, V(A.value + 256), C, dict(ks=(1024, 256), vs=(1024, 128)))])
 def test_gather_results(px, k, v, slots, kw):
     assert px.lib.parallax_cache_gather_q4(E, slots, k, v, _params(px, **kw), None) == 1
+
+
+@pytest.mark.parametrize("kw", [
+    dict(out=V(A.value + 16)), dict(out=V(A.value - 16)), dict(out=A, out_dtype=0), dict(out=V(B.value + 16)),
+    dict(out=V(C.value + 600 * 8 * 9216 - 16)), dict(out=E), dict(out=V(F.value - 16)), dict(out=V((6 << 32) + (1 << 22) - 16))])
+def test_decode_q4_output(px, kw):
+    kw = dict(out_dtype=1) | kw
+    p = px.DecodeParams(8, 16, 8, 128, 4096, 64, 600, 64, 1, kw["out_dtype"], 0.088, 0)
+    ws = V(6 << 32)
+    st = px.lib.parallax_decode_q4(A, B, C, E, F, kw["out"], ws, 1 << 22, ctypes.byref(p), None)
+    assert st == 1

@@ -188,3 +188,21 @@ def test_streams_and_captures_have_workspaces_of_their_own(px):
                 keep.append(take(3 << 20))
         spans.sort()
         assert all(a[1] <= b[0] for a, b in zip(spans, spans[1:]))
+
+
+def test_decode_q4_in_place(px):
+    # the output in the place of the queries or the probes: each unit's rows are read before they are written
+    g = torch.Generator(device="cuda")
+    g.manual_seed(8)
+    n = 40 * 640
+    k, v = (torch.randn(n, 2, 128, device="cuda", generator=g).bfloat16() for _ in range(2))
+    cache = px.q4_cache(n // 64, 2, 128)
+    px.cache_append_q4(k, v, torch.arange(n, device="cuda"), cache)
+    cache = cache.view(40, -1, 2, 72 * 128).transpose(1, 2).contiguous()
+    q, rho = (torch.randn(40, 8, 128, device="cuda", generator=g).bfloat16() for _ in range(2))
+    lens = torch.randint(0, 641, (40,), device="cuda", dtype=torch.int32)
+    for ctas in (0, 1, 148):
+        want = px.decode_q4(q, rho, cache, seq_lens=lens, num_ctas=ctas)
+        for place in (0, 1):
+            x = [q.clone(), rho.clone()]
+            assert torch.equal(px.decode_q4(*x, cache, seq_lens=lens, out=x[place], num_ctas=ctas), want)
