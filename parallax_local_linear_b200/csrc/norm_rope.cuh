@@ -186,7 +186,10 @@ __device__ __forceinline__ int nr_position(const NormRopeArgs& a, int b, int t) 
 }
 
 // A group of LPR lanes takes the rows of chunk blockIdx.y (a set's next `hpg`
-// heads) of one token; neighbouring groups take neighbouring tokens.
+// heads) of one token; neighbouring groups take neighbouring tokens.  20 CTAs an
+// SM hold the bf16, not interleaved kernels to 48 registers and spill 32 bytes of set-up
+// (810 MB: 134.1 us; 135.0 without the bound, on 56 registers, and 144.2 with 16 CTAs,
+// on 61; 128 packed tokens of 40 heads the other way round, 3.9, 3.6 and 3.7).
 template <typename T, int D, bool kInter>
 __global__ void __launch_bounds__(kNrFwdThreads, 20) norm_rope_kernel(const NormRopeArgs a) {
   using L = NrLane<T, D, kInter>;

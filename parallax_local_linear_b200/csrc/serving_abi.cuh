@@ -295,8 +295,10 @@ int norm_rope_heads_per_group(const plx_head_rows* rows, int32_t num_sets, const
   long long heads = 0;
   for (int i = 0; i < num_sets; ++i) heads += rows[i].heads;
   const int sms = current_device_sms();
-  const long long fill = (long long)(sms > 0 ? sms : 148) * 4 * kNrThreads / lanes;
-  int hpg = 16;   // (128 us for 4 x 8192 tokens of 3 x 16 heads; 133 with 8, 152 with 4, 192 with 2)
+  const long long fill = (long long)(sms > 0 ? sms : 148) * 16 * kNrFwdThreads / lanes;   // 16 of the 20 CTAs that an SM holds
+  // 4 x 8192 tokens of 3 x 16 heads (810 MB): 134.1 us; 137.1 with 8, 147.0 with 4, 205.7 with 2.  4 x 512 tokens: 13.7,
+  // 13.7, 12.5, 15.5.
+  int hpg = 16;
   while (hpg > 1 && (long long)p->batch * p->tokens * heads / hpg < fill) hpg /= 2;
   return hpg;
 }
