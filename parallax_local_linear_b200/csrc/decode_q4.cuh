@@ -47,6 +47,11 @@
 //     where a subnormal code counts as 2^-14, so beside one heavy weight the other
 //     15 tokens' terms are cut at 2^-14 of it (measured: 1.1e-4 of the heavy
 //     weight, always downwards).
+//   - The tensor cores truncate, and sums of codes (0 to 15) grow with every page, so what
+//     each step loses would add up: 0.07% of a flat row after 170 pages, percents of it
+//     after thousands. As a group's columns share their minima's sums, any
+//     constant may go from the former to the latter: every 16 pages one column's sums
+//     do, and the rest are differences of columns.
 // With 11 bits and the first key's probe value a row with one key 12 above 1000
 // others was up to 6% off, with 22 bits alone 0.4%, with both 0.01%.
 //
@@ -98,6 +103,11 @@ constexpr float kQ4Top = 10.f, kQ4Slack = 5.f;
 // Probe values (from aref, in their unit) are at most this: p s, which is smaller by
 // them than p a s, keeps its low half.
 constexpr float kQ4MaxProbe = 1024.f;
+
+// Pages after which a unit's sums of codes are taken back to about zero: with 8, 16
+// and 32 decode_long's shape takes 223.6, 221.5 and 220.5 us, and rows of 32768 keys in
+// runs of 170 pages are 2.5e-5, 3.4e-5 and 6.6e-5 of themselves off (6.7e-4 without).
+constexpr int kQ4Settle = 16;
 
 // Warps of a CTA (one CTA per SM) and its shared memory.  A ring slot holds
 // one half of a block, K's or V's codes and parameters.
@@ -320,6 +330,29 @@ struct Q4WarpState {
       l[t] = c[t] = aref[t] = 0.f;
       unit[t] = 1.f;
     }
+  }
+  // Moves one column's sums of codes, of every column of its group, into the
+  // minima's sums (which all columns share).
+  __device__ __forceinline__ void settle() {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int g = 0; g < G; ++g) {
+        const float d0 = __shfl_sync(0xffffffffu, o[t][4 * g][0], lane & 3);
+        const float d1 = __shfl_sync(0xffffffffu, o[t][4 * g][1], lane & 3);
+#pragma unroll
+        for (int i = 4 * g; i < 4 * g + 4; ++i) {
+          o[t][i][0] -= d0;
+          o[t][i][1] -= d1;
+          o[t][i][2] -= 16.f * d0;
+          o[t][i][3] -= 16.f * d1;
+        }
+        if (lane < 4) {
+          pm[t][g][0] = fmaf(d0, 16777216.f, pm[t][g][0]);
+          pm[t][g][1] = fmaf(d1, 16777216.f, pm[t][g][1]);
+        }
+      }
   }
   // Sums over the lanes that hold other tokens of the same heads; the codes'
   // powers of two, the minima's sums and the unit go in.  l becomes 1 to 2
@@ -787,7 +820,9 @@ __global__ void __launch_bounds__(Q4Smem<D, NT>::kThreads, 1) decode_q4_kernel(c
         need[t] = fs[t] * mx[t] + fminf(lg2(ma[t]) + vbig, 100.f);
         due = due || need[t] > st.m[t] + kQ4Slack || fs[t] * mx[t] > st.xref[t] + kQ4Slack || ma[t] > kQ4MaxProbe;
       }
-      if (__any_sync(0xffffffffu, due)) {
+      due = due || seg % kQ4Settle == kQ4Settle - 1;
+      if (__any_sync(0xffffffffu, due)) {   // (settling apart from this, each page waited for its products: 4% of the time)
+        st.settle();
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
           // aref goes to the key with the page's largest score

@@ -144,6 +144,12 @@ def test_a_long_row_and_other_grids(px, ctas):
     _check(px, _rows(px, 40000, 4, 128, 1.0, [23456], 12.0, seed=1), num_ctas=ctas)
 
 
+@pytest.mark.parametrize("H,d", [(2, 128), (8, 64)])
+def test_long_flat_rows_in_a_few_runs(px, H, d):
+    # thousands of pages summed by one warp: what each step loses must not add up beside a row that averages out
+    _check(px, _rows(px, 100_000, H, d, 0.1, [], 0.0, seed=2), num_ctas=1)
+
+
 # sizes of queries, keys, values and probes, at both ends of the stated range: entries of q and rho below 2^114, value
 # scales (about a quarter of a value) down to 2^-80, differences of probe values times a value scale up to 2^100
 SIZES = [(1e-10, 1e10, 1e10, 1e5), (2.0 ** -30, 2.0 ** 30, 2.0 ** 30, 2.0 ** 30), (1.0, 1.0, 1e-3, 2.0 ** 100),
