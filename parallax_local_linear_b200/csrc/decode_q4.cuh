@@ -1,6 +1,8 @@
-// Parallax decode over the 4-bit cache (bound: HBM; 144 bytes a token and KV
-// head at d = 128, so the arithmetic per byte is 3.6 times the bf16 decode's
-// and issue slots come next).
+// Parallax decode over the 4-bit cache: 144 bytes a token and KV head at d = 128,
+// so the arithmetic per byte is 3.6 times the bf16 decode's.  While the clock is up
+// the latencies of three warps a sub-partition bound it (57% of the issue slots, 52% of the
+// integer pipe in use at 1.65 GHz), in sustained runs, at 1.3 GHz, the issue slots
+// (1080 instructions a page).
 //
 // The sums are those of the single-pass form in decode.cuh,
 //     l = sum e_i,  c = sum e_i a_i,  O1 = sum e_i v_i,  O2 = sum e_i a_i v_i,
@@ -65,10 +67,11 @@
 // the CTA after one barrier, and across CTAs in the workspace, by the last CTA
 // that finishes a piece (a counter per unit, which that CTA takes back to zero).
 //
-// Measured (device time): 32 sequences of 32768 keys, 32/8 heads, d = 128 (1.21
-// GB) 191 us, 6.3 TB/s; 8 of 4096, 16/8 heads (38 MB) 16.7 us, of which set-up,
-// first pages and merge take 8; 16 of 16384 and 4 KV heads (151 MB) 35 us with
-// 4 query heads each and 49 us with 8.
+// Measured (device time in a graph, full clock): 32 sequences of 32768 keys, 32/8 heads, d =
+// 128 (1.21 GB) 222 us, 5.4 TB/s (269 us a call sustained for seconds under the power
+// cap); 8 of 4096, 16/8 heads (38 MB) 18.3 us, of which set-up, first pages and
+// merge take about 8; 16 of 16384 and 4 KV heads (151 MB) 39 us with 4 query heads
+// each and 60 us with 8.
 #pragma once
 
 #include <type_traits>

@@ -16,9 +16,10 @@
 // second time.  A group of lanes takes several heads of one token, so a
 // token's cos and sin are read once for them.
 //
-// Measured (device time, bf16, d = 128): 4 x 8192 tokens of 3 x 16 heads forward (810
-// MB) 134 us, 6.0 TB/s; 4 x 8192 of 16 + 16 + 4 heads backward
-// (910 MB) 149 us, 6.1 TB/s; 8 tokens forward 2.3 us.
+// Measured (device time in a graph, full clock, bf16, d = 128): 4 x 8192 tokens of 3 x 16
+// heads forward (810 MB) 134 us, 6.0 TB/s; 4 x 8192 of 16 + 16 + 4 heads backward (910 MB)
+// 150 us, 6.1 TB/s (138 to 141 and 168 to 171 us a call sustained for seconds); 8 tokens
+// forward 2.1 us.
 #pragma once
 
 #include "ptx.cuh"
