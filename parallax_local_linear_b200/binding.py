@@ -291,7 +291,9 @@ def _kept_workspace(kind, index, partials, counters):
     There is one per device and stream, since calls on different streams may overlap, and
     another per capture and stream: graphs may be replayed at once, and what a capture records
     is not done yet.  A graph clears its counters when it starts; after that, as in direct
-    calls, every call leaves them zero.
+    calls, every call leaves them zero.  (Memory taken under torch.cuda.graph belongs to the
+    graph.  Captures made in another way need a DecodePlan, or decode_q4's ``workspace``,
+    that outlives them.)
     """
     stream = _raw_stream(index)
     capture = lib.parallax_capture_id(stream) if _capturing(index) else 0
@@ -358,6 +360,8 @@ def decode(q, rho, k_cache, v_cache, scale=None, *, seq_lens=None, page_table=No
     [B], optional) limits each sequence.  Paged cache: pools [P, Hkv, 64, d]
     with ``page_table`` (int32 [B, max_pages]) and ``seq_lens`` (required).
     Returns out [B, Hq, d] in ``out_dtype`` (default: the input dtype).
+    Calls on several streams, and in several graphs (torch.cuda.graph), may
+    overlap.
     """
     _check_decode_inputs(q, rho, k_cache, v_cache, seq_lens, page_table, kv_len)
     out, out_dtype = _output(out, out_dtype, q.shape, q.dtype, q.device)
