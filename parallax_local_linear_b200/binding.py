@@ -298,25 +298,25 @@ def _kept_workspace(kind, index, partials, counters):
     stream = _raw_stream(index)
     capture = lib.parallax_capture_id(stream) if _capturing(index) else 0
     key = kind, index, stream, capture != 0
-    with _ws_lock:
-        ws, owner, most, room = _workspaces.get(key, (None, 0, 0, 0))
-        if ws is None or owner != capture or partials > most or counters > room:
-            if owner != capture:
-                most = room = 0
-            most, room = max(most, partials, 1 << 20), max(room, counters, 1 << 14) if counters else 0
+    kept = _workspaces.get(key)
+    if kept is None or kept[1] != capture or partials > kept[2] or counters > kept[3]:
+        with _ws_lock:
+            most, room = kept[2:] if kept is not None and kept[1] == capture else (1 << 20, 1 << 14 if counters else 0)
+            most, room = max(most, partials), max(room, counters)
             ws = torch.empty(room + most, dtype=torch.uint8, device=index)
             (ws[most:] if kind == "q4" else ws[:room]).zero_()
-            _workspaces[key] = ws, capture, most, room
-        return ws, room
+            kept = _workspaces[key] = ws, capture, most, room
+    return kept[0], kept[3]
 
 
 def _decode_workspace(index, nbytes, params):
-    """(address, bytes) of a decode's workspace: its counters (4 bytes per unit, padded to 256) end
-    where the partials of every call start."""
+    """(tensor, address, bytes) of a decode's workspace: its counters (4 bytes per unit, padded to
+    256) end where the partials of every call start.  The caller keeps the tensor until it has
+    launched (another thread may replace it)."""
     units = params.batch * (params.num_kv_heads if params.in_dtype == PLX_BF16 else params.num_q_heads)
     counters = (4 * units + 255) & ~255
     ws, room = _kept_workspace("decode", index, nbytes - counters, counters)
-    return ws.data_ptr() + room - counters, ws.numel() - room + counters
+    return ws, ws.data_ptr() + room - counters, ws.numel() - room + counters
 
 
 def decode_params(q, k_cache, *, page_table=None, kv_len=None, scale=None, out_dtype=None,
@@ -368,9 +368,9 @@ def decode(q, rho, k_cache, v_cache, scale=None, *, seq_lens=None, page_table=No
     p = decode_params(q, k_cache, page_table=page_table, kv_len=kv_len, scale=scale,
                       out_dtype=out_dtype, num_ctas=num_ctas)
     nbytes = decode_workspace_size(p)
-    ws, ws_bytes = _decode_workspace(q.get_device(), nbytes, p)
+    ws, ws_at, ws_bytes = _decode_workspace(q.get_device(), nbytes, p)
     st = lib.parallax_decode(_ptr(q), _ptr(rho), _ptr(k_cache), _ptr(v_cache), _ptr(page_table),
-                             _ptr(seq_lens), _ptr(out), ws, ws_bytes, ctypes.byref(p), _stream_ptr(q.device))
+                             _ptr(seq_lens), _ptr(out), ws_at, ws_bytes, ctypes.byref(p), _stream_ptr(q.device))
     if st != 0:
         raise ParallaxError(st, "parallax_decode")
     return out
@@ -475,10 +475,10 @@ def decode_projected(x, w_q, w_rho, k_cache, v_cache, scale=None, *, seq_lens=No
     p = decode_params(q_out, k_cache, page_table=page_table, kv_len=kv_len, scale=scale,
                       out_dtype=out_dtype, num_ctas=num_ctas)
     nbytes = decode_workspace_size(p)
-    ws, ws_bytes = _decode_workspace(x.get_device(), nbytes, p)
+    ws, ws_at, ws_bytes = _decode_workspace(x.get_device(), nbytes, p)
     st = lib.parallax_decode_projected(_ptr(x), _ptr(w_q), _ptr(w_rho), int(x.shape[1]), _ptr(k_cache),
                                        _ptr(v_cache), _ptr(page_table), _ptr(seq_lens), _ptr(q_out),
-                                       _ptr(rho_out), _ptr(out), ws, ws_bytes, ctypes.byref(p),
+                                       _ptr(rho_out), _ptr(out), ws_at, ws_bytes, ctypes.byref(p),
                                        _stream_ptr(x.device))
     if st != 0:
         raise ParallaxError(st, "parallax_decode_projected")
@@ -754,12 +754,15 @@ def _workspace_size(index, status, fn, *args):
     return nbytes
 
 
+_is_capturing = getattr(torch._C, "_cuda_isCurrentStreamCapturing", torch.cuda.is_current_stream_capturing)
+
+
 def _capturing(index):
     """Whether device ``index``'s current stream is being captured."""
     if _current_device() == index:
-        return torch.cuda.is_current_stream_capturing()
+        return _is_capturing()
     with torch.cuda.device(index):
-        return torch.cuda.is_current_stream_capturing()
+        return _is_capturing()
 
 
 def _raw(t):

@@ -206,3 +206,27 @@ def test_decode_q4_in_place(px):
         for place in (0, 1):
             x = [q.clone(), rho.clone()]
             assert torch.equal(px.decode_q4(*x, cache, seq_lens=lens, out=x[place], num_ctas=ctas), want)
+
+
+def test_threads_on_one_stream(px):
+    # calls of several host threads on one stream, of sizes that make the workspace grow between them
+    import threading
+
+    calls = [_call(px, kind, b, n, 9 + b) for kind in ("decode bf16", "q4") for b, n in ((1, 4000), (40, 600), (400, 200))]
+    for key in [k for k in px._workspaces if k[0] in ("decode", "q4")]:
+        del px._workspaces[key]
+    bad = []
+
+    def work(f, w):
+        for _ in range(30):
+            out = _out(w)
+            f(out)
+            if not torch.equal(out, w):
+                bad.append(f)
+
+    threads = [threading.Thread(target=work, args=c) for c in calls]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not bad and px.last_device_error() == 0
