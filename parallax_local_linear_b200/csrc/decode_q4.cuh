@@ -116,7 +116,7 @@ constexpr int kQ4Settle = 16;
 // one half of a block, K's or V's codes and parameters.
 template <int D, int NT>
 struct Q4Smem {
-  static constexpr int kWarps = NT == 1 ? 12 : 8;                  // 168 and 255 registers a thread
+  static constexpr int kWarps = NT == 1 ? 12 : 8;                  // 168 and 255 registers a thread (d = 128: 4 and 20 bytes spilled)
   static constexpr int kThreads = 32 * kWarps;
   static constexpr int kCodes = kQ4Page * D / 2;
   static constexpr int kPart = kCodes + Q4Block<D>::kParamBytes;
